@@ -1,4 +1,4 @@
-"""Thin ctypes binding of libep_b200.so (C ABI in include/ep.h).
+"""Thin ctypes binding of libep_b200.so (C ABI in include/ep.h, ep_router.h).
 
 Argument marshalling only: torch tensors are turned into device pointers and
 sizes, the current CUDA stream is passed through, and a non-OK status raises
@@ -26,6 +26,7 @@ EP_BF16, EP_FP32, EP_FP8_E4M3 = 0, 1, 2
 EP_INT8_PER_TOKEN, EP_FP8_E4M3_PER_TOKEN, EP_MXFP8_E4M3, EP_MXFP8_E5M2, EP_MXFP4_E2M1 = 3, 4, 5, 6, 7
 EP_LAYOUT_COMPACT, EP_LAYOUT_PADDED = 0, 1
 EP_ROUTING_TOPK, EP_ROUTING_EXPERT_CHOICE = 0, 1
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1  # ep_router.h
 EP_DEVERR_BAD_INDEX, EP_DEVERR_OVERFLOW, EP_DEVERR_TIMEOUT = 0x1, 0x2, 0x4
 
 EXPORTED = ("ep_workspace_bytes", "ep_workspace_init", "ep_get_layout", "ep_dispatch", "ep_combine",
@@ -33,7 +34,8 @@ EXPORTED = ("ep_workspace_bytes", "ep_workspace_init", "ep_get_layout", "ep_disp
             "ep_version", "ep_get_layout_no_alloc", "ep_get_rank_layout", "ep_dispatch_ranks", "ep_combine_ranks",
             "ep_dispatch_low_latency", "ep_layout_dispatch", "ep_peer_alloc", "ep_peer_free", "ep_peer_open",
             "ep_peer_close", "ep_peer_publish_counts", "ep_dispatch_peers", "ep_combine_peers",
-            "ep_layout_dispatch_expert_choice", "ep_layout_dispatch_ranks")
+            "ep_layout_dispatch_expert_choice", "ep_layout_dispatch_ranks", "ep_router_topk",
+            "ep_balance_workspace_bytes", "ep_balance_loss", "ep_router_backward")
 
 
 class EPError(RuntimeError):
@@ -65,6 +67,13 @@ class PeersDesc(ctypes.Structure):
                 ("recv_x", ctypes.c_void_p), ("recv_topk_idx", ctypes.c_void_p),
                 ("recv_topk_weights", ctypes.c_void_p), ("recv_src", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("rank_counts", ctypes.c_void_p)]
+
+
+class RouterDesc(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("logits_dtype", ctypes.c_int), ("num_tokens", ctypes.c_int32),
+                ("num_experts", ctypes.c_int32), ("num_topk", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("normalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -133,6 +142,15 @@ def lib():
         L.ep_dispatch_peers.argtypes = [P, i32, RP, LP, KP, P, PP, P]
         L.ep_combine_peers.restype = st
         L.ep_combine_peers.argtypes = [i32, RP, LP, KP, PP, P, st, P]
+        TP = ctypes.POINTER(RouterDesc)
+        L.ep_router_topk.restype = st
+        L.ep_router_topk.argtypes = [TP, P, P, P, P, P, P]
+        L.ep_balance_workspace_bytes.restype = ctypes.c_size_t
+        L.ep_balance_workspace_bytes.argtypes = [TP, i32]
+        L.ep_balance_loss.restype = st
+        L.ep_balance_loss.argtypes = [TP, P, P, P, P, i32, P, P, P, P, P, ctypes.c_size_t, P]
+        L.ep_router_backward.restype = st
+        L.ep_router_backward.argtypes = [TP, P, P, P, P, P, i32, P, P, P, P, P]
         if L.ep_version() != EP_ABI_VERSION:
             raise ImportError("libep_b200.so has ABI version %d, the binding expects %d; rebuild it"
                               % (L.ep_version(), EP_ABI_VERSION))
@@ -538,6 +556,128 @@ def ep_combine_peers(routing: Routing, layout: Layout, rank_layout: RankLayout, 
     _check(lib().ep_combine_peers(out.shape[1], ctypes.byref(routing.desc), ctypes.byref(layout.desc),
                                   ctypes.byref(rank_layout.desc), ctypes.byref(peers.desc), _ptr(out),
                                   _dtype_code(out), _stream(stream)), "ep_combine_peers")
+
+
+# ------------------------------------------------------------------ router
+def _arg(name: str, t, dtype, shape, device=None):
+    """Address of a dense tensor argument of the given type and shape (None
+    stays None); `device`: the device it has to be on."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise TypeError("%s must be a %s tensor of shape %s, got %s %s"
+                        % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("the C ABI takes dense row-major tensors; %s is a strided view" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, the other tensors are on %s" % (name, t.device, device))
+    return t.data_ptr()
+
+
+def _on_current_device(device) -> None:
+    """A call runs on the current device and its current stream."""
+    if device.type != "cuda":
+        raise ValueError("the tensors are on %s; the library takes CUDA tensors" % (device,))
+    if device.index != torch.cuda.current_device():
+        raise ValueError("the tensors are on %s, the current device is cuda:%d (use torch.cuda.device)"
+                         % (device, torch.cuda.current_device()))
+
+
+class Router:
+    """How logits become experts and weights (see include/ep_router.h)."""
+
+    def __init__(self, num_experts: int, num_topk: int, *, score=EP_SCORE_SOFTMAX, num_groups=1, topk_groups=1,
+                 group_top=1, normalize=True, scale=1.0):
+        self.num_experts, self.num_topk = int(num_experts), int(num_topk)
+        self._fields = (self.num_experts, self.num_topk, int(num_groups), int(topk_groups), int(group_top),
+                        1 if normalize else 0, float(scale))
+        self._score = int(score)
+
+    def desc(self, num_tokens: int, dtype) -> RouterDesc:
+        return RouterDesc(self._score, EP_BF16 if dtype == torch.bfloat16 else EP_FP32, num_tokens, *self._fields)
+
+    def of(self, logits: torch.Tensor) -> RouterDesc:
+        """The C descriptor for these logits, after checking them."""
+        if logits.dtype not in (torch.bfloat16, torch.float32) or logits.dim() != 2 or \
+                logits.shape[1] != self.num_experts:
+            raise TypeError("logits must be a bfloat16 or float32 tensor of shape (T, %d), got %s %s"
+                            % (self.num_experts, logits.dtype, tuple(logits.shape)))
+        if not logits.is_contiguous():
+            raise ValueError("the C ABI takes dense row-major tensors; logits is a strided view")
+        _on_current_device(logits.device)
+        return self.desc(logits.shape[0], logits.dtype)
+
+
+def ep_router_topk(logits: torch.Tensor, router: Router, topk_idx: torch.Tensor, topk_weights: torch.Tensor, *,
+                   bias=None, token_mask=None, stream=None) -> None:
+    """logits [T, E] (bf16 or fp32) -> topk_idx int64 [T, K], topk_weights fp32 [T, K]."""
+    d, dev = router.of(logits), logits.device
+    T, E, K = d.num_tokens, d.num_experts, d.num_topk
+    _check(lib().ep_router_topk(ctypes.byref(d), logits.data_ptr(), _arg("bias", bias, torch.float32, (E,), dev),
+                                _arg("token_mask", token_mask, torch.uint8, (T,), dev),
+                                _arg("topk_idx", topk_idx, torch.int64, (T, K), dev),
+                                _arg("topk_weights", topk_weights, torch.float32, (T, K), dev), _stream(stream)),
+           "ep_router_topk")
+
+
+class BalanceStats:
+    """Device buffers of ep_balance_loss for up to num_tokens tokens in
+    num_seqs sequences: losses fp32 [S, 2] (balance, z), counts int32 [S, E],
+    seq_tokens int32 [S], mean_scores fp32 [S, E], and the workspace."""
+
+    def __init__(self, router: Router, num_tokens: int, num_seqs: int = 1, device="cuda"):
+        S, E = int(num_seqs), router.num_experts
+        self.num_seqs = S
+        need = lib().ep_balance_workspace_bytes(ctypes.byref(router.desc(num_tokens, torch.float32)), S)
+        if need == 0:
+            raise EPError(EP_ERR_INVALID_ARG, "ep_balance_workspace_bytes")
+        self.losses = torch.empty((S, 2), dtype=torch.float32, device=device)
+        self.counts = torch.empty((S, E), dtype=torch.int32, device=device)
+        self.seq_tokens = torch.empty(S, dtype=torch.int32, device=device)
+        self.mean_scores = torch.empty((S, E), dtype=torch.float32, device=device)
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def ep_balance_loss(logits: torch.Tensor, router: Router, topk_idx: torch.Tensor, stats: BalanceStats, *,
+                    token_mask=None, seq_offsets=None, stream=None) -> BalanceStats:
+    """Balance and z losses and expert counts of each sequence, into `stats`.
+    seq_offsets: int32 [S + 1], or None for one sequence of all tokens."""
+    d, dev = router.of(logits), logits.device
+    T, E, K, S = d.num_tokens, d.num_experts, d.num_topk, stats.num_seqs
+    _check(lib().ep_balance_loss(ctypes.byref(d), logits.data_ptr(), _arg("topk_idx", topk_idx, torch.int64, (T, K), dev),
+                                 _arg("token_mask", token_mask, torch.uint8, (T,), dev),
+                                 _arg("seq_offsets", seq_offsets, torch.int32, (S + 1,), dev), S,
+                                 _arg("losses", stats.losses, torch.float32, (S, 2), dev),
+                                 _arg("counts", stats.counts, torch.int32, (S, E), dev),
+                                 _arg("seq_tokens", stats.seq_tokens, torch.int32, (S,), dev),
+                                 _arg("mean_scores", stats.mean_scores, torch.float32, (S, E), dev),
+                                 stats.workspace.data_ptr(), stats.workspace.numel(), _stream(stream)),
+           "ep_balance_loss")
+    return stats
+
+
+def ep_router_backward(logits: torch.Tensor, router: Router, topk_idx, d_logits: torch.Tensor, *,
+                       d_topk_weights=None, stats: BalanceStats | None = None, d_losses=None, token_mask=None,
+                       seq_offsets=None, stream=None) -> None:
+    """d_logits (the logits' type and shape) from d_topk_weights fp32 [T, K]
+    and / or d_losses fp32 [S, 2] (with the `stats` of ep_balance_loss)."""
+    d, dev = router.of(logits), logits.device
+    T, E, K = d.num_tokens, d.num_experts, d.num_topk
+    if d_losses is not None and stats is None:
+        raise ValueError("d_losses needs the stats of ep_balance_loss")
+    S = stats.num_seqs if d_losses is not None else 1
+    counts = seq_tokens = offsets = None
+    if d_losses is not None:
+        counts = _arg("counts", stats.counts, torch.int32, (S, E), dev)
+        seq_tokens = _arg("seq_tokens", stats.seq_tokens, torch.int32, (S,), dev)
+        offsets = _arg("seq_offsets", seq_offsets, torch.int32, (S + 1,), dev)
+    _check(lib().ep_router_backward(ctypes.byref(d), logits.data_ptr(),
+                                    _arg("topk_idx", topk_idx, torch.int64, (T, K), dev),
+                                    _arg("token_mask", token_mask, torch.uint8, (T,), dev),
+                                    _arg("d_topk_weights", d_topk_weights, torch.float32, (T, K), dev), offsets, S,
+                                    counts, seq_tokens, _arg("d_losses", d_losses, torch.float32, (S, 2), dev),
+                                    _arg("d_logits", d_logits, logits.dtype, (T, E), dev), _stream(stream)),
+           "ep_router_backward")
 
 
 def ep_get_layout_no_alloc(routing: Routing, layout: Layout, device_error_flags: torch.Tensor | None = None,

@@ -3,6 +3,7 @@
 // memory except ep_peer_alloc (buffers other processes map); only
 // ep_get_device_error, and a layout call given a num_valid_host pointer,
 // synchronise.
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <cuda_runtime.h>
@@ -11,6 +12,7 @@
 
 #include "ep.h"
 #include "ep_internal.h"
+#include "ep_router_launch.h"
 
 namespace {
 
@@ -898,6 +900,122 @@ ep_status_t ep_combine_peers(int32_t hidden, const ep_routing_desc_t* routing, c
                             ep::error_word(layout->workspace),
                             peer_tables(peers, rank_layout)};
     return from_cuda(ep::launch_rank_combine(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------- router
+namespace {
+
+ep_status_t check_router(const ep_router_desc_t* r)
+{
+    if (r == nullptr)
+        return EP_ERR_INVALID_ARG;
+    if ((r->score != EP_SCORE_SOFTMAX && r->score != EP_SCORE_SIGMOID) ||
+        (r->logits_dtype != EP_BF16 && r->logits_dtype != EP_FP32) || r->num_tokens < 0 || r->num_experts < 1 ||
+        r->num_topk < 1 || r->num_topk > r->num_experts || (r->normalize != 0 && r->normalize != 1))
+        return EP_ERR_INVALID_ARG;
+    if (r->num_groups < 1 || r->num_experts % r->num_groups != 0 || r->topk_groups < 1 ||
+        r->topk_groups > r->num_groups || (r->group_top != 1 && r->group_top != 2))
+        return EP_ERR_INVALID_ARG;
+    if (!std::isfinite(r->scale) || static_cast<int64_t>(r->num_tokens) * r->num_experts >= (int64_t{1} << 31))
+        return EP_ERR_INVALID_ARG; // num_topk <= num_experts: T * K is below 2^31 too
+    if (r->num_experts > ep::kRouterMaxExperts || r->num_topk > ep::kRouterMaxTopk ||
+        r->num_groups > ep::kRouterMaxGroups || (r->num_groups & (r->num_groups - 1)) != 0)
+        return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+// [T, ...] array of the router's tokens: needed when there are any.
+bool token_array(const ep_router_desc_t* r, const void* p, uintptr_t alignment)
+{
+    return r->num_tokens == 0 || (p != nullptr && aligned(p, alignment));
+}
+
+bool logits_array(const ep_router_desc_t* r, const void* p)
+{
+    return token_array(r, p, r->logits_dtype == EP_BF16 ? 2 : 4);
+}
+
+ep_status_t check_sequences(const int32_t* seq_offsets, int32_t num_seqs)
+{
+    if (num_seqs < 1 || num_seqs > (1 << 24) || (seq_offsets == nullptr && num_seqs != 1) || !aligned(seq_offsets, 4))
+        return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
+} // namespace
+
+ep_status_t ep_router_topk(const ep_router_desc_t* router, const void* logits, const float* bias,
+                           const uint8_t* token_mask, int64_t* topk_idx, float* topk_weights, ep_stream_t stream)
+{
+    CallRange range_("ep_router_topk");
+    const ep_status_t st = check_router(router);
+    if (st != EP_OK)
+        return st;
+    if (!logits_array(router, logits) || !token_array(router, topk_idx, 8) || !token_array(router, topk_weights, 4) ||
+        !aligned(bias, 4))
+        return EP_ERR_INVALID_ARG;
+    ep::RouterTopkLaunch a{*router, logits, bias, token_mask, topk_idx, topk_weights};
+    return from_cuda(ep::launch_router_topk(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t ep_balance_workspace_bytes(const ep_router_desc_t* router, int32_t num_seqs)
+{
+    if (check_router(router) != EP_OK || num_seqs < 1 || num_seqs > (1 << 24))
+        return 0;
+    return ep::balance_workspace_bytes(router->num_tokens, router->num_experts, num_seqs);
+}
+
+ep_status_t ep_balance_loss(const ep_router_desc_t* router, const void* logits, const int64_t* topk_idx,
+                            const uint8_t* token_mask, const int32_t* seq_offsets, int32_t num_seqs, float* losses,
+                            int32_t* counts, int32_t* seq_tokens, float* mean_scores, void* workspace,
+                            size_t workspace_bytes, ep_stream_t stream)
+{
+    CallRange range_("ep_balance_loss");
+    ep_status_t st = check_router(router);
+    if (st != EP_OK)
+        return st;
+    st = check_sequences(seq_offsets, num_seqs);
+    if (st != EP_OK)
+        return st;
+    if (!logits_array(router, logits) || !token_array(router, topk_idx, 8))
+        return EP_ERR_INVALID_ARG;
+    if (losses == nullptr || counts == nullptr || seq_tokens == nullptr || !aligned(losses, 4) ||
+        !aligned(counts, 4) || !aligned(seq_tokens, 4) || !aligned(mean_scores, 4))
+        return EP_ERR_INVALID_ARG;
+    if (workspace == nullptr || !aligned(workspace, 256) ||
+        workspace_bytes < ep::balance_workspace_bytes(router->num_tokens, router->num_experts, num_seqs))
+        return EP_ERR_WORKSPACE;
+    ep::BalanceLaunch a{*router, logits, topk_idx, token_mask, seq_offsets, num_seqs,
+                        losses,  counts, seq_tokens, mean_scores, workspace};
+    return from_cuda(ep::launch_balance_loss(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_router_backward(const ep_router_desc_t* router, const void* logits, const int64_t* topk_idx,
+                               const uint8_t* token_mask, const float* d_topk_weights, const int32_t* seq_offsets,
+                               int32_t num_seqs, const int32_t* counts, const int32_t* seq_tokens,
+                               const float* d_losses, void* d_logits, ep_stream_t stream)
+{
+    CallRange range_("ep_router_backward");
+    ep_status_t st = check_router(router);
+    if (st != EP_OK)
+        return st;
+    if (!logits_array(router, logits) || !logits_array(router, d_logits) ||
+        (router->num_tokens > 0 && d_logits == logits))
+        return EP_ERR_INVALID_ARG;
+    if (d_topk_weights != nullptr && (!aligned(d_topk_weights, 4) || !token_array(router, topk_idx, 8)))
+        return EP_ERR_INVALID_ARG;
+    if (d_losses != nullptr) {
+        st = check_sequences(seq_offsets, num_seqs);
+        if (st != EP_OK)
+            return st;
+        if (!aligned(d_losses, 4) || counts == nullptr || seq_tokens == nullptr || !aligned(counts, 4) ||
+            !aligned(seq_tokens, 4))
+            return EP_ERR_INVALID_ARG;
+    }
+    ep::RouterBackwardLaunch a{*router,     logits,   topk_idx, token_mask, d_topk_weights,
+                               seq_offsets, num_seqs, counts,   seq_tokens, d_losses,
+                               d_logits};
+    return from_cuda(ep::launch_router_backward(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 ep_status_t ep_get_device_error(const ep_layout_t* layout, uint32_t* flags, int clear, ep_stream_t stream)
