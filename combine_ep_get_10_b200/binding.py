@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libep_b200.so (C ABI in include/ep.h, ep_router.h).
+"""Thin ctypes binding of libep_b200.so (C ABI in include/ep.h, ep_router.h
+and ep_lora.h).
 
 Argument marshalling only: torch tensors are turned into device pointers and
 sizes, the current CUDA stream is passed through, and a non-OK status raises
@@ -35,7 +36,8 @@ EXPORTED = ("ep_workspace_bytes", "ep_workspace_init", "ep_get_layout", "ep_disp
             "ep_dispatch_low_latency", "ep_layout_dispatch", "ep_peer_alloc", "ep_peer_free", "ep_peer_open",
             "ep_peer_close", "ep_peer_publish_counts", "ep_dispatch_peers", "ep_combine_peers",
             "ep_layout_dispatch_expert_choice", "ep_layout_dispatch_ranks", "ep_router_topk",
-            "ep_balance_workspace_bytes", "ep_balance_loss", "ep_router_backward")
+            "ep_balance_workspace_bytes", "ep_balance_loss", "ep_router_backward", "ep_row_tokens", "ep_lora",
+            "ep_lora_backward")
 
 
 class EPError(RuntimeError):
@@ -74,6 +76,11 @@ class RouterDesc(ctypes.Structure):
                 ("num_experts", ctypes.c_int32), ("num_topk", ctypes.c_int32), ("num_groups", ctypes.c_int32),
                 ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("normalize", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
+
+
+class LoraDesc(ctypes.Structure):
+    _fields_ = [("rank", ctypes.c_int32), ("hidden_in", ctypes.c_int32), ("hidden_out", ctypes.c_int32),
+                ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 _lib = None
@@ -151,6 +158,13 @@ def lib():
         L.ep_balance_loss.argtypes = [TP, P, P, P, P, i32, P, P, P, P, P, ctypes.c_size_t, P]
         L.ep_router_backward.restype = st
         L.ep_router_backward.argtypes = [TP, P, P, P, P, P, i32, P, P, P, P, P]
+        AP = ctypes.POINTER(LoraDesc)
+        L.ep_row_tokens.restype = st
+        L.ep_row_tokens.argtypes = [RP, LP, st, i32, i64, P, P]
+        L.ep_lora.restype = st
+        L.ep_lora.argtypes = [P, P, RP, LP, st, i32, i64, P, AP, P, P, P]
+        L.ep_lora_backward.restype = st
+        L.ep_lora_backward.argtypes = [P, P, P, P, RP, LP, st, i32, i64, P, AP, P, P, P, P, P]
         if L.ep_version() != EP_ABI_VERSION:
             raise ImportError("libep_b200.so has ABI version %d, the binding expects %d; rebuild it"
                               % (L.ep_version(), EP_ABI_VERSION))
@@ -678,6 +692,88 @@ def ep_router_backward(logits: torch.Tensor, router: Router, topk_idx, d_logits:
                                     counts, seq_tokens, _arg("d_losses", d_losses, torch.float32, (S, 2), dev),
                                     _arg("d_logits", d_logits, logits.dtype, (T, E), dev), _stream(stream)),
            "ep_router_backward")
+
+
+# ------------------------------------------------------ low-rank adapters
+class Lora:
+    """The factors of E adapters: a bf16 [E, rank, hidden_in], b bf16 [E,
+    hidden_out, rank], scales fp32 [E] or None (1); see include/ep_lora.h."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scales: torch.Tensor | None = None):
+        if a.dim() != 3 or b.dim() != 3:
+            raise TypeError("a must be [E, rank, hidden_in] and b [E, hidden_out, rank]")
+        E, r, hin = a.shape
+        hout = b.shape[1]
+        self.E, self.rank, self.hidden_in, self.hidden_out = E, r, hin, hout
+        self.device = a.device
+        self.a, self.b, self.scales = a, b, scales  # kept alive with the descriptor
+        self.desc = LoraDesc(r, hin, hout, _arg("a", a, torch.bfloat16, (E, r, hin)),
+                             _arg("b", b, torch.bfloat16, (E, hout, r), a.device),
+                             _arg("scales", scales, torch.float32, (E,), a.device))
+
+
+def ep_row_tokens(routing: Routing, layout: Layout, row_token: torch.Tensor, *, mode=EP_LAYOUT_COMPACT,
+                  max_tokens_per_expert=0, stream=None) -> None:
+    """row_token int32 [num_rows]: the source token of every row (-1: no pair's)."""
+    if row_token.dtype != torch.int32 or row_token.dim() != 1:
+        raise TypeError("row_token must be an int32 vector")
+    _check(lib().ep_row_tokens(ctypes.byref(routing.desc), ctypes.byref(layout.desc), int(mode),
+                               int(max_tokens_per_expert), row_token.shape[0], _ptr(row_token), _stream(stream)),
+           "ep_row_tokens")
+
+
+def _row_token(t, layout, device):
+    """Address of the row table.  An empty one has none: any other stands in,
+    so that the call still is the one in token order (0 rows are read)."""
+    return None if t is None else _arg("row_token", t, torch.int32, (t.shape[0],), device) or layout.desc.workspace
+
+
+def _lora_rows(routing: Routing, lora: Lora, first: torch.Tensor, h: torch.Tensor, row_token):
+    """(rows of the row buffer, rows of x / base / out), after checking them."""
+    _on_current_device(first.device)
+    if routing.E != lora.E:
+        raise ValueError("the routing names %d adapters, the factors are of %d" % (routing.E, lora.E))
+    if lora.device != first.device:
+        raise ValueError("the factors are on %s, the rows are on %s" % (lora.device, first.device))
+    if h.dim() != 2 or (row_token is not None and row_token.shape[0] < h.shape[0]):
+        raise ValueError("the fp32 row buffer has shape %s, row_token %d entries"
+                         % (tuple(h.shape), -1 if row_token is None else row_token.shape[0]))
+    return h.shape[0], routing.T if row_token is not None else h.shape[0]
+
+
+def ep_lora(x: torch.Tensor, routing: Routing, layout: Layout, lora: Lora, out: torch.Tensor, h: torch.Tensor, *,
+            base: torch.Tensor | None = None, row_token: torch.Tensor | None = None, mode=EP_LAYOUT_COMPACT,
+            max_tokens_per_expert=0, stream=None) -> None:
+    """out = base + the rows' low-rank products; h fp32 [num_rows, rank] gets
+    the scaled products with the first factor.  With row_token (int32, at least
+    num_rows entries) x, base and out are [T, ...] in token order, without it
+    they are the num_rows dispatched rows.  base may be out itself."""
+    rows, n = _lora_rows(routing, lora, x, h, row_token)
+    dev, bf = x.device, torch.bfloat16
+    _check(lib().ep_lora(_arg("x", x, bf, (n, lora.hidden_in), dev), _arg("base", base, bf, (n, lora.hidden_out), dev),
+                         ctypes.byref(routing.desc), ctypes.byref(layout.desc), int(mode), int(max_tokens_per_expert),
+                         rows, _row_token(row_token, layout, dev), ctypes.byref(lora.desc),
+                         _arg("out", out, bf, (n, lora.hidden_out), dev),
+                         _arg("h", h, torch.float32, (h.shape[0], lora.rank), dev), _stream(stream)), "ep_lora")
+
+
+def ep_lora_backward(dy: torch.Tensor, x, h, routing: Routing, layout: Layout, lora: Lora, dh: torch.Tensor, *,
+                     dx: torch.Tensor | None = None, da: torch.Tensor | None = None, db: torch.Tensor | None = None,
+                     dx_base: torch.Tensor | None = None, row_token: torch.Tensor | None = None,
+                     mode=EP_LAYOUT_COMPACT, max_tokens_per_expert=0, stream=None) -> None:
+    """dh fp32 [num_rows, rank] (scratch), dx (added to dx_base), da and db from
+    dy, x and the h of the forward call (x and h may be None without da, db)."""
+    rows, n = _lora_rows(routing, lora, dy, dh, row_token)
+    dev, bf = dy.device, torch.bfloat16
+    E, r, hin, hout = lora.E, lora.rank, lora.hidden_in, lora.hidden_out
+    hp = None if h is None else _arg("h", h, torch.float32, (max(rows, h.shape[0]), r), dev)
+    _check(lib().ep_lora_backward(_arg("dy", dy, bf, (n, hout), dev), _arg("x", x, bf, (n, hin), dev), hp,
+                                  _arg("dx_base", dx_base, bf, (n, hin), dev), ctypes.byref(routing.desc),
+                                  ctypes.byref(layout.desc), int(mode), int(max_tokens_per_expert), rows,
+                                  _row_token(row_token, layout, dev), ctypes.byref(lora.desc),
+                                  _arg("dh", dh, torch.float32, (dh.shape[0], r), dev),
+                                  _arg("dx", dx, bf, (n, hin), dev), _arg("da", da, bf, (E, r, hin), dev),
+                                  _arg("db", db, bf, (E, hout, r), dev), _stream(stream)), "ep_lora_backward")
 
 
 def ep_get_layout_no_alloc(routing: Routing, layout: Layout, device_error_flags: torch.Tensor | None = None,

@@ -12,6 +12,7 @@
 
 #include "ep.h"
 #include "ep_internal.h"
+#include "ep_lora_launch.h"
 #include "ep_router_launch.h"
 
 namespace {
@@ -1016,6 +1017,150 @@ ep_status_t ep_router_backward(const ep_router_desc_t* router, const void* logit
                                seq_offsets, num_seqs, counts,   seq_tokens, d_losses,
                                d_logits};
     return from_cuda(ep::launch_router_backward(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// --------------------------------------------------------- low-rank adapters
+namespace {
+
+constexpr int kMaxLoraHidden = 1 << 20;
+constexpr int64_t kMaxLoraPairs = int64_t{1} << 24; // with kMaxLoraHidden: grids stay below 2^31 CTAs
+
+ep_status_t check_row_args(const ep_routing_desc_t* routing, const ep_layout_t* layout, ep_buffer_mode_t mode,
+                           int32_t max_tokens, int64_t num_rows)
+{
+    ep_status_t st = check_routing(routing);
+    if (st != EP_OK)
+        return st;
+    if (routing->routing != EP_ROUTING_TOPK)
+        return EP_ERR_INVALID_ARG;
+    st = check_workspace(routing, layout, false);
+    if (st != EP_OK)
+        return st;
+    st = check_rows(routing, layout, mode, max_tokens, num_rows);
+    if (st != EP_OK)
+        return st;
+    if (num_rows >= (int64_t{1} << 31))
+        return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
+ep_status_t check_lora(const ep_routing_desc_t* routing, const ep_layout_t* layout, ep_buffer_mode_t mode,
+                       int32_t max_tokens, int64_t num_rows, const int32_t* row_token, const ep_lora_desc_t* lora)
+{
+    const ep_status_t st = check_row_args(routing, layout, mode, max_tokens, num_rows);
+    if (st != EP_OK)
+        return st;
+    if (mode == EP_LAYOUT_PADDED &&
+        (layout->num_tokens_per_expert == nullptr || !aligned(layout->num_tokens_per_expert, 4)))
+        return EP_ERR_INVALID_ARG;
+    if (!aligned(row_token, 4) || (row_token != nullptr && routing->num_topk != 1))
+        return EP_ERR_INVALID_ARG;
+    if (lora == nullptr || lora->rank < 8 || lora->rank % 8 != 0 || lora->hidden_in < 8 || lora->hidden_in % 8 != 0 ||
+        lora->hidden_out < 8 || lora->hidden_out % 8 != 0 || lora->a == nullptr || lora->b == nullptr ||
+        !aligned(lora->a, 16) || !aligned(lora->b, 16) || !aligned(lora->scales, 4))
+        return EP_ERR_INVALID_ARG;
+    if (lora->rank > ep::kLoraMaxRank || routing->num_experts > ep::kLoraMaxAdapters ||
+        lora->hidden_in > kMaxLoraHidden || lora->hidden_out > kMaxLoraHidden ||
+        static_cast<int64_t>(routing->num_tokens) * routing->num_topk > kMaxLoraPairs)
+        return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+ep::LoraRows lora_rows(const ep_routing_desc_t* routing, const ep_layout_t* layout, ep_buffer_mode_t mode,
+                       int32_t max_tokens, int64_t num_rows, const int32_t* row_token)
+{
+    ep::LoraRows r{};
+    r.offsets = layout->expert_offsets;
+    r.counts = layout->num_tokens_per_expert;
+    r.mode = static_cast<int32_t>(mode);
+    r.max_tokens = max_tokens;
+    r.E = routing->num_experts;
+    r.num_rows = static_cast<int32_t>(num_rows);
+    r.pairs = routing->num_tokens * routing->num_topk;
+    r.row_token = row_token;
+    r.T = routing->num_tokens;
+    r.err = ep::error_word(layout->workspace);
+    return r;
+}
+
+// x, base, out and the like: rows of tokens (row_token given) or of the buffer
+bool row_array(const ep_routing_desc_t* routing, int64_t num_rows, const int32_t* row_token, const void* p)
+{
+    return (row_token != nullptr ? routing->num_tokens : num_rows) == 0 || (p != nullptr && aligned(p, 16));
+}
+
+} // namespace
+
+ep_status_t ep_row_tokens(const ep_routing_desc_t* routing, const ep_layout_t* layout, ep_buffer_mode_t mode,
+                          int32_t max_tokens_per_expert, int64_t num_rows, int32_t* row_token, ep_stream_t stream)
+{
+    CallRange range_("ep_row_tokens");
+    const ep_status_t st = check_row_args(routing, layout, mode, max_tokens_per_expert, num_rows);
+    if (st != EP_OK)
+        return st;
+    if (num_rows > 0 && (row_token == nullptr || !aligned(row_token, 4)))
+        return EP_ERR_INVALID_ARG;
+    ep::RowTokensLaunch a{tc_rows(routing, layout, mode, max_tokens_per_expert, num_rows), routing->num_tokens,
+                          row_token, ep::error_word(layout->workspace)};
+    return from_cuda(ep::launch_row_tokens(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_lora(const void* x, const void* base, const ep_routing_desc_t* routing, const ep_layout_t* layout,
+                    ep_buffer_mode_t mode, int32_t max_tokens_per_expert, int64_t num_rows, const int32_t* row_token,
+                    const ep_lora_desc_t* lora, void* out, float* h, ep_stream_t stream)
+{
+    CallRange range_("ep_lora");
+    const ep_status_t st = check_lora(routing, layout, mode, max_tokens_per_expert, num_rows, row_token, lora);
+    if (st != EP_OK)
+        return st;
+    if (!row_array(routing, num_rows, row_token, x) || !row_array(routing, num_rows, row_token, out) ||
+        !aligned(base, 16) || (num_rows > 0 && (h == nullptr || !aligned(h, 16))))
+        return EP_ERR_INVALID_ARG;
+    if (out != nullptr && out == x)
+        return EP_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const ep::LoraRows rows = lora_rows(routing, layout, mode, max_tokens_per_expert, num_rows, row_token);
+    ep::LoraShrinkLaunch down{rows, x, lora->a, lora->scales, lora->hidden_in, lora->rank, 0, h};
+    const cudaError_t e = ep::launch_lora_shrink(down, s);
+    if (e != cudaSuccess)
+        return EP_ERR_CUDA;
+    ep::LoraExpandLaunch up{rows, h, lora->b, base, out, lora->hidden_out, lora->rank, 0,
+                            row_token != nullptr && out != base ? layout->slot : nullptr};
+    return from_cuda(ep::launch_lora_expand(up, s));
+}
+
+ep_status_t ep_lora_backward(const void* dy, const void* x, const float* h, const void* dx_base,
+                             const ep_routing_desc_t* routing, const ep_layout_t* layout, ep_buffer_mode_t mode,
+                             int32_t max_tokens_per_expert, int64_t num_rows, const int32_t* row_token,
+                             const ep_lora_desc_t* lora, float* dh, void* dx, void* da, void* db, ep_stream_t stream)
+{
+    CallRange range_("ep_lora_backward");
+    const ep_status_t st = check_lora(routing, layout, mode, max_tokens_per_expert, num_rows, row_token, lora);
+    if (st != EP_OK)
+        return st;
+    if (!row_array(routing, num_rows, row_token, dy) || !aligned(dx_base, 16) || !aligned(dx, 16) ||
+        (num_rows > 0 && (dh == nullptr || !aligned(dh, 16))) || (da == nullptr) != (db == nullptr) ||
+        !aligned(da, 16) || !aligned(db, 16))
+        return EP_ERR_INVALID_ARG;
+    if (da != nullptr && (!row_array(routing, num_rows, row_token, x) ||
+                          (num_rows > 0 && (h == nullptr || !aligned(h, 16) || h == dh))))
+        return EP_ERR_INVALID_ARG;
+    if (dx != nullptr && (dx == dy || dx == x))
+        return EP_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const ep::LoraRows rows = lora_rows(routing, layout, mode, max_tokens_per_expert, num_rows, row_token);
+    ep::LoraShrinkLaunch down{rows, dy, lora->b, lora->scales, lora->hidden_out, lora->rank, 1, dh};
+    cudaError_t e = ep::launch_lora_shrink(down, s);
+    if (e == cudaSuccess && dx != nullptr) {
+        ep::LoraExpandLaunch up{rows, dh, lora->a, dx_base, dx, lora->hidden_in, lora->rank, 1,
+                                row_token != nullptr && dx != dx_base ? layout->slot : nullptr};
+        e = ep::launch_lora_expand(up, s);
+    }
+    if (e == cudaSuccess && da != nullptr) {
+        ep::LoraOuterLaunch o{rows, x, dh, da, dy, h, db, lora->hidden_in, lora->hidden_out, lora->rank};
+        e = ep::launch_lora_outer(o, s);
+    }
+    return from_cuda(e);
 }
 
 ep_status_t ep_get_device_error(const ep_layout_t* layout, uint32_t* flags, int clear, ep_stream_t stream)

@@ -1,0 +1,76 @@
+// ep_lora_launch.h -- launch interfaces of the low-rank adapter kernels
+// (ep_lora.cu), called by the C-ABI layer, which has checked the arguments.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "ep_internal.h"
+#include "ep_lora.h"
+
+namespace ep {
+
+constexpr int kLoraMaxRank = 128;
+constexpr int kLoraMaxAdapters = 1024;
+
+// The rows of every adapter, and where a row's data is.
+struct LoraRows {
+    const int32_t* offsets; // COMPACT: [E + 1]
+    const int32_t* counts;  // PADDED: [E]
+    int32_t mode, max_tokens, E;
+    int32_t num_rows;
+    int32_t pairs;            // T * K: no routing fills more rows
+    const int32_t* row_token; // [num_rows], or nullptr: row i is at row i
+    int32_t T;                // with row_token: rows of x, base and out
+    uint32_t* err;
+};
+
+struct RowTokensLaunch {
+    TcRows rows;
+    int32_t T;
+    int32_t* row_token;
+    uint32_t* err;
+};
+cudaError_t launch_row_tokens(const RowTokensLaunch& a, cudaStream_t stream);
+
+// u[row, j] = scales[e] * sum over k of x[row, k] * w_e(j, k); w_e is [rank, K]
+// (transposed 0) or [K, rank] (1).
+struct LoraShrinkLaunch {
+    LoraRows rows;
+    const void* x;
+    const void* w;
+    const float* scales; // or nullptr
+    int32_t K, rank, transposed;
+    float* u;
+};
+cudaError_t launch_lora_shrink(const LoraShrinkLaunch& a, cudaStream_t stream);
+
+// out[row, n] = base[row, n] + sum over j of u[row, j] * w_e(n, j); w_e is
+// [N, rank] (transposed 0) or [rank, N] (1).
+struct LoraExpandLaunch {
+    LoraRows rows;
+    const float* u;
+    const void* w;
+    const void* base; // or nullptr
+    void* out;
+    int32_t N, rank, transposed;
+    const int32_t* slot; // [T]: copy base to out for tokens with slot -1; or nullptr
+};
+cudaError_t launch_lora_expand(const LoraExpandLaunch& a, cudaStream_t stream);
+
+// da[e][j, n] = sum over e's rows of dh[row, j] * x[row, n]  and
+// db[e][n, j] = sum over e's rows of dy[row, n] * h[row, j]
+struct LoraOuterLaunch {
+    LoraRows rows;
+    const void* x;
+    const float* dh;
+    void* da;
+    const void* dy;
+    const float* h;
+    void* db;
+    int32_t hidden_in, hidden_out, rank;
+};
+cudaError_t launch_lora_outer(const LoraOuterLaunch& a, cudaStream_t stream);
+
+} // namespace ep

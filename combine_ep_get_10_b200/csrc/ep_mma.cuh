@@ -1,0 +1,72 @@
+// ep_mma.cuh -- device helpers of the kernels that multiply: asynchronous
+// 16-byte copies, ldmatrix and the warp matrix product, and the two-term bf16
+// form of an fp32 operand.
+#pragma once
+
+#include "ep_device.cuh"
+
+namespace ep {
+
+// 16 bytes global -> shared; `bytes` 0 writes zeros and reads nothing.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// d += a (16 x 16, rows) * b (16 x 8, columns), bf16 operands, fp32 sums.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An fp32 pair as bf16 pairs hi + lo: hi is the value rounded to bf16, lo what
+// is left, rounded again, so 16 bits of the value survive (2^-17 of it at
+// most is lost).  An infinite value leaves no rest (inf - inf).
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uint32_t& lo)
+{
+    hi = pack_bf16x2(a, b);
+    const float ra = a - bf16_lo(hi), rb = b - bf16_hi(hi);
+    lo = pack_bf16x2(ra == ra ? ra : 0.0f, rb == rb ? rb : 0.0f);
+}
+
+// Place of 16-byte chunk c of a row in a shared-memory tile of PC (a power of
+// two) chunks a row, so that 8 consecutive rows of one chunk lie in different
+// banks (what ldmatrix reads at once).
+template <int PC>
+__device__ __forceinline__ uint32_t swizzled(int row, int c)
+{
+    const int f = PC >= 8 ? row & 7 : (row / (8 / PC)) & (PC - 1);
+    return static_cast<uint32_t>(row * PC + (c ^ f)) * 16u;
+}
+
+} // namespace ep
