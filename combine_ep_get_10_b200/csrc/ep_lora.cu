@@ -16,6 +16,7 @@
 
 #include "ep_lora_launch.h"
 #include "ep_mma.cuh"
+#include "ep_tcgen05.cuh"
 
 namespace ep {
 
@@ -442,159 +443,193 @@ __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1) lora_expand_
 }
 
 // ------------------------------------------------------------------- outer
-constexpr int kOuterThreads = 128; // four warps, 32 columns each
+// dW of one adapter and 128 columns of x or dy: the columns are the product's
+// rows (M), the rank its columns (N), and the sum runs over the adapter's rows,
+// 64 at a time.  Both operands are MN-major: the row data as it lies in HBM,
+// and u, which the threads write as two bf16 tiles (hi, lo).  Sums stay in
+// tensor memory until the last row.
+constexpr int kOuterThreads = 128;
 constexpr int kOuterCols = 128;
-constexpr int kOuterStages = 3;
+constexpr int kOuterStages = 4;
+constexpr int kOuterAhead = kOuterStages - 2; // chunks in flight while one is multiplied
 
 template <int RP>
 struct OuterShape {
     static constexpr int kVBytes = kRowTile * kOuterCols * 2;
-    static constexpr int kUBytes = kRowTile * RP * 2;
-    static constexpr int kBytes = kOuterStages * kVBytes + 2 * kUBytes;
+    static constexpr int kUBytes = kRowTile * RP * 2; // one term
+    static constexpr int kStageBytes = kVBytes + 2 * kUBytes;
+    static constexpr int kBytes = kOuterStages * kStageBytes + 1024; // tiles start on 1024 bytes
+    static constexpr int kCols = RP < 32 ? 32 : RP;                  // tensor memory
+    static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
+    static constexpr int kUChunks = RP < 64 ? RP / 8 : 8; // 16-byte chunks a row of u's tile
 };
 
-// One adapter's rows against kOuterCols columns of x (IN: da, [rank, N]) or
-// of dy (!IN: db, [N, rank]).
-template <int RP, bool IN>
-__device__ __forceinline__ void outer_tile(const LoraOuterLaunch& a, int e, int n0, uint8_t* smem)
+// Place of columns 8c.. of `row` in a tile of 128-byte rows, 64 columns each.
+__device__ __forceinline__ uint32_t halves(int row, int c)
 {
-    using S = OuterShape<RP>;
-    constexpr int PC = RP / 8, VC = kOuterCols / 8;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int N = IN ? a.hidden_in : a.hidden_out;
-    const uint16_t* v = static_cast<const uint16_t*>(IN ? a.x : a.dy);
-    const float* u = IN ? a.dh : a.h;
-    const RowRange rows = group_rows(a.rows, e);
-    const uint32_t vs = smem_addr(smem), us = vs + kOuterStages * S::kVBytes;
-    const int n = (rows.end - rows.begin + kRowTile - 1) / kRowTile;
-
-    const auto load = [&](int step, int stage) {
-        const int c = tid % VC, col = n0 + c * 8;
-#pragma unroll
-        for (int i = 0; i < kRowTile / (kOuterThreads / VC); ++i) {
-            const int row = tid / VC + i * (kOuterThreads / VC);
-            const int at = row_at(a.rows, rows.begin + step * kRowTile + row, rows.end);
-            const bool on = at >= 0 && col < N;
-            cp_async16(vs + stage * S::kVBytes + swizzled<VC>(row, c), on ? v + static_cast<int64_t>(at) * N + col : v,
-                       on ? 16 : 0);
-        }
-    };
-
-    // IN: [RP / 16 tiles of j][4 tiles of n]; else [2 tiles of n][RP / 8 tiles of j]
-    float acc[RP / 4][4];
-#pragma unroll
-    for (int j = 0; j < RP / 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            acc[j][i] = 0.0f;
-
-#pragma unroll
-    for (int i = 0; i < kOuterStages - 1; ++i) {
-        if (i < n)
-            load(i, i);
-        cp_async_commit();
-    }
-    for (int i = 0; i < n; ++i) {
-        cp_async_wait<kOuterStages - 2>();
-        __syncthreads(); // the stage is there, and everybody is done with the one before
-        if (i + kOuterStages - 1 < n)
-            load(i + kOuterStages - 1, (i + kOuterStages - 1) % kOuterStages);
-        cp_async_commit();
-        // u of these rows, in two terms
-        for (int t = tid; t < kRowTile * PC; t += kOuterThreads) {
-            const int row = t / PC, c = t % PC;
-            const int r = rows.begin + i * kRowTile + row;
-            uint4 h4 = make_uint4(0u, 0u, 0u, 0u), l4 = h4;
-            if (c * 8 < a.rank && row_at(a.rows, r, rows.end) >= 0) {
-                const float4* p = reinterpret_cast<const float4*>(u + static_cast<int64_t>(r) * a.rank + c * 8);
-                const float4 p0 = __ldcg(p), p1 = __ldcg(p + 1);
-                split_bf16x2(p0.x, p0.y, h4.x, l4.x);
-                split_bf16x2(p0.z, p0.w, h4.y, l4.y);
-                split_bf16x2(p1.x, p1.y, h4.z, l4.z);
-                split_bf16x2(p1.z, p1.w, h4.w, l4.w);
-            }
-            *reinterpret_cast<uint4*>(smem + kOuterStages * S::kVBytes + swizzled<PC>(row, c)) = h4;
-            *reinterpret_cast<uint4*>(smem + kOuterStages * S::kVBytes + S::kUBytes + swizzled<PC>(row, c)) = l4;
-        }
-        __syncthreads();
-        const uint32_t vb = vs + (i % kOuterStages) * S::kVBytes;
-        // a fragment of the row (first) operand from a [rows of the sum, columns] tile, and of the column operand
-        const int a_row = (lane & 7) + ((lane >> 4) << 3), a_chunk = (lane >> 3) & 1;
-        const int b_row = (lane & 7) + (((lane >> 3) & 1) << 3), b_chunk = lane >> 4;
-#pragma unroll
-        for (int kk = 0; kk < kRowTile / 16; ++kk) {
-            if (IN) {
-                uint32_t b[2][4];
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    ldmatrix4_trans(b[c], vb + swizzled<VC>(kk * 16 + b_row, warp * 4 + c * 2 + b_chunk));
-#pragma unroll
-                for (int j = 0; j < RP / 16; ++j)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        uint32_t f[4];
-                        ldmatrix4_trans(f, us + t * S::kUBytes + swizzled<PC>(kk * 16 + a_row, j * 2 + a_chunk));
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            mma16816(acc[j * 4 + 2 * c], f, b[c][0], b[c][1]);
-                            mma16816(acc[j * 4 + 2 * c + 1], f, b[c][2], b[c][3]);
-                        }
-                    }
-            } else {
-                uint32_t f[2][4];
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    ldmatrix4_trans(f[c], vb + swizzled<VC>(kk * 16 + a_row, warp * 4 + c * 2 + a_chunk));
-#pragma unroll
-                for (int j = 0; j < RP / 16; ++j)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        uint32_t b[4];
-                        ldmatrix4_trans(b, us + t * S::kUBytes + swizzled<PC>(kk * 16 + b_row, j * 2 + b_chunk));
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            mma16816(acc[c * (RP / 8) + 2 * j], f[c], b[0], b[1]);
-                            mma16816(acc[c * (RP / 8) + 2 * j + 1], f[c], b[2], b[3]);
-                        }
-                    }
-            }
-        }
-        __syncthreads(); // u's tile is written again next time
-    }
-
-    const int g = lane >> 2, q = lane & 3;
-    uint16_t* out = static_cast<uint16_t*>(IN ? a.da : a.db) + static_cast<int64_t>(e) * a.rank * N;
-#pragma unroll
-    for (int t = 0; t < RP / 4; ++t) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t word = pack_bf16x2(acc[t][2 * h], acc[t][2 * h + 1]);
-            int j, col;
-            if (IN) {
-                j = (t / 4) * 16 + g + 8 * h;
-                col = n0 + warp * 32 + (t % 4) * 8 + 2 * q;
-                if (j < a.rank && col < N)
-                    *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(j) * N + col) = word;
-            } else {
-                j = (t % (RP / 8)) * 8 + 2 * q;
-                col = n0 + warp * 32 + (t / (RP / 8)) * 16 + g + 8 * h;
-                if (j < a.rank && col < N)
-                    *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(col) * a.rank + j) = word;
-            }
-        }
-    }
+    return static_cast<uint32_t>(c >> 3) * (kRowTile * 128u) + swizzled<8>(row, c & 7);
 }
 
 template <int RP>
 __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(LoraOuterLaunch a, int in_tiles, int out_tiles)
 {
-    extern __shared__ __align__(128) uint8_t smem[];
+    using S = OuterShape<RP>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t s_free[kOuterStages], s_done;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_at[2][kRowTile];
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int per = in_tiles + out_tiles;
-    const int e = blockIdx.x / per, i = blockIdx.x - e * per;
-    if (i < in_tiles)
-        outer_tile<RP, true>(a, e, i * kOuterCols, smem);
-    else
-        outer_tile<RP, false>(a, e, (i - in_tiles) * kOuterCols, smem);
+    const int e = blockIdx.x / per, i_tile = blockIdx.x - e * per;
+    const bool in = i_tile < in_tiles; // da, from x and dh; else db, from dy and h
+    const int N = in ? a.hidden_in : a.hidden_out;
+    const int n0 = (in ? i_tile : i_tile - in_tiles) * kOuterCols;
+    const uint16_t* v = static_cast<const uint16_t*>(in ? a.x : a.dy);
+    const float* u = in ? a.dh : a.h;
+    const RowRange rows = group_rows(a.rows, e);
+    const int n = (rows.end - rows.begin + kRowTile - 1) / kRowTile;
+    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t base = smem_addr(smem);
+
+    uint32_t tmem = 0;
+    if (n > 0) {
+        if (warp == 0)
+            tmem_alloc(&s_tmem, S::kCols);
+        if (tid == 0) {
+            for (int i = 0; i < kOuterStages; ++i)
+                mbar_init(&s_free[i], 1);
+            mbar_init(&s_done, 1);
+            fence_mbar_init();
+        }
+        // where the rows' data is: of chunk i in s_at[i % 2], of the one after in a register
+        const auto at_of = [&](int chunk) {
+            return tid < kRowTile ? row_at(a.rows, rows.begin + chunk * kRowTile + tid, rows.end) : -1;
+        };
+        if (tid < kRowTile)
+            s_at[0][tid] = at_of(0);
+        int next_at = at_of(1);
+        // u of the next chunk, in registers
+        constexpr int kVecs = RP / 16;
+        float4 un[kVecs][2];
+        const auto load_u = [&](int chunk) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int t = tid + i * kOuterThreads, row = rows.begin + chunk * kRowTile + t / (RP / 8), c = t % (RP / 8);
+                un[i][0] = un[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (row < rows.end && c * 8 < a.rank) {
+                    const float4* p = reinterpret_cast<const float4*>(u + static_cast<int64_t>(row) * a.rank + c * 8);
+                    un[i][0] = __ldcg(p);
+                    un[i][1] = __ldcg(p + 1);
+                }
+            }
+        };
+        load_u(0);
+        tc_fence_before_sync();
+        __syncthreads();
+        tc_fence_after_sync();
+        tmem = s_tmem;
+
+        bool alive = true; // false once a wait has run out
+        for (int it = 0; it < n + kOuterAhead; ++it) {
+            if (it < n) {
+                const int stage = it % kOuterStages;
+                if (it >= kOuterStages && alive)
+                    alive = mbar_wait_bounded(&s_free[stage], (it / kOuterStages - 1) & 1, a.rows.err);
+                const uint32_t vs = base + stage * S::kStageBytes;
+                const int* at = s_at[it & 1];
+                const int c = tid % 16, col = n0 + c * 8;
+#pragma unroll
+                for (int i = 0; i < kRowTile / 8; ++i) {
+                    const int row = tid / 16 + 8 * i, r = at[row];
+                    const bool on = r >= 0 && col < N;
+                    cp_async16(vs + halves(row, c), on ? v + static_cast<int64_t>(r) * N + col : v, on ? 16 : 0);
+                }
+                uint8_t* us = smem + stage * S::kStageBytes + S::kVBytes;
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) {
+                    const int t = tid + i * kOuterThreads, row = t / (RP / 8), cu = t % (RP / 8);
+                    uint4 h4 = make_uint4(0u, 0u, 0u, 0u), l4 = h4;
+                    if (at[row] >= 0) {
+                        split_bf16x2(un[i][0].x, un[i][0].y, h4.x, l4.x);
+                        split_bf16x2(un[i][0].z, un[i][0].w, h4.y, l4.y);
+                        split_bf16x2(un[i][1].x, un[i][1].y, h4.z, l4.z);
+                        split_bf16x2(un[i][1].z, un[i][1].w, h4.w, l4.w);
+                    }
+                    const uint32_t place = RP < 64 ? swizzled<S::kUChunks>(row, cu) : halves(row, cu);
+                    *reinterpret_cast<uint4*>(us + place) = h4;
+                    *reinterpret_cast<uint4*>(us + S::kUBytes + place) = l4;
+                }
+                load_u(it + 1);
+                if (tid < kRowTile)
+                    s_at[(it + 1) & 1][tid] = next_at;
+                next_at = at_of(it + 2);
+            }
+            cp_async_commit();
+            const int j = it - kOuterAhead;
+            cp_async_wait<kOuterAhead>();
+            fence_proxy_async_shared();
+            __syncthreads();
+            if (j >= 0 && tid == 0) {
+                tc_fence_after_sync();
+                const uint32_t vs = base + (j % kOuterStages) * S::kStageBytes, us = vs + S::kVBytes;
+                constexpr uint32_t desc = product_desc(kOuterCols, RP, true, true);
+                constexpr uint32_t group = S::kUChunks * 128u; // 8 rows of u
+#pragma unroll
+                for (int kk = 0; kk < kRowTile / 16; ++kk) {
+                    const uint64_t va = operand_desc(vs + kk * 2048u, Swizzle::k128, kRowTile * 128u, 1024u);
+                    tc_product(tmem, va, operand_desc(us + kk * 2 * group, S::kSwizzle, kRowTile * 128u, group), desc,
+                               j > 0 || kk > 0);
+                    tc_product(tmem, va,
+                               operand_desc(us + S::kUBytes + kk * 2 * group, S::kSwizzle, kRowTile * 128u, group), desc,
+                               true);
+                }
+                tc_commit(j == n - 1 ? &s_done : &s_free[j % kOuterStages]);
+            }
+        }
+        if (alive)
+            mbar_wait_bounded(&s_done, 0, a.rows.err);
+        tc_fence_after_sync();
+    }
+
+    // thread: column n0 + tid, every rank
+    const int col = n0 + tid;
+    uint16_t* out = static_cast<uint16_t*>(in ? a.da : a.db) + static_cast<int64_t>(e) * a.rank * N;
+#pragma unroll
+    for (int j0 = 0; j0 < RP; j0 += 16) {
+        if (j0 >= a.rank)
+            break;
+        float d[16];
+        if (n > 0) {
+            tmem_load16(d, tmem + (static_cast<uint32_t>(warp * 32) << 16) + j0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                d[i] = 0.0f;
+        }
+        if (col < N) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (j0 + 8 * h >= a.rank)
+                    break;
+                if (in) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        out[static_cast<int64_t>(j0 + 8 * h + i) * N + col] =
+                            static_cast<uint16_t>(pack_bf16x2(d[8 * h + i], 0.0f));
+                } else {
+                    st_v4(out + static_cast<int64_t>(col) * a.rank + j0 + 8 * h,
+                          make_uint4(pack_bf16x2(d[8 * h], d[8 * h + 1]), pack_bf16x2(d[8 * h + 2], d[8 * h + 3]),
+                                     pack_bf16x2(d[8 * h + 4], d[8 * h + 5]), pack_bf16x2(d[8 * h + 6], d[8 * h + 7])));
+                }
+            }
+        }
+    }
+    if (n > 0) {
+        tc_fence_before_sync();
+        __syncthreads();
+        if (warp == 0)
+            tmem_free(tmem, S::kCols);
+    }
 }
 
 // -------------------------------------------------------------- row tokens
