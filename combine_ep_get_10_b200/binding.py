@@ -196,8 +196,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current device's current stream, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -573,14 +573,14 @@ def ep_combine_peers(routing: Routing, layout: Layout, rank_layout: RankLayout, 
 
 
 # ------------------------------------------------------------------ router
-def _arg(name: str, t, dtype, shape, device=None):
+def _arg(name: str, t, dtype, shape: tuple, device=None):
     """Address of a dense tensor argument of the given type and shape (None
     stays None); `device`: the device it has to be on."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.shape != shape:
         raise TypeError("%s must be a %s tensor of shape %s, got %s %s"
-                        % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+                        % (name, dtype, shape, t.dtype, tuple(t.shape)))
     if not t.is_contiguous():
         raise ValueError("the C ABI takes dense row-major tensors; %s is a strided view" % name)
     if device is not None and t.device != device:
@@ -606,6 +606,7 @@ class Router:
         self._fields = (self.num_experts, self.num_topk, int(num_groups), int(topk_groups), int(group_top),
                         1 if normalize else 0, float(scale))
         self._score = int(score)
+        self._last = (None, None, None)  # the descriptor of the last number of tokens and type
 
     def desc(self, num_tokens: int, dtype) -> RouterDesc:
         return RouterDesc(self._score, EP_BF16 if dtype == torch.bfloat16 else EP_FP32, num_tokens, *self._fields)
@@ -619,7 +620,11 @@ class Router:
         if not logits.is_contiguous():
             raise ValueError("the C ABI takes dense row-major tensors; logits is a strided view")
         _on_current_device(logits.device)
-        return self.desc(logits.shape[0], logits.dtype)
+        T, dtype, d = self._last
+        if T != logits.shape[0] or dtype != logits.dtype:
+            d = self.desc(logits.shape[0], logits.dtype)
+            self._last = (logits.shape[0], logits.dtype, d)
+        return d
 
 
 def ep_router_topk(logits: torch.Tensor, router: Router, topk_idx: torch.Tensor, topk_weights: torch.Tensor, *,

@@ -1,9 +1,7 @@
 // ep_router.cu -- the token router, its balance losses and their gradient.
 //
 // All kernels give a token's row of E <= 1024 logits to one warp and keep it in
-// registers: lane L holds the NPL consecutive logits from e0(L) on, so that
-// lane order is expert order (a tie is settled by the lowest lane) and, with
-// groups, a group is a run of whole lanes.
+// registers, NPL of them a lane (RowMap).
 #include <algorithm>
 #include <cfloat>
 
@@ -18,23 +16,46 @@ constexpr int kTopkWarps = 4;
 constexpr float kNegInf = -INFINITY;
 
 // ------------------------------------------------------------------ rows
-// The lane's run of experts: [e0, e0 + n), n <= c <= NPL.  G (a power of two)
-// groups take 32 / G lanes each; G = 1 spreads the row over all lanes.
-struct LaneRun {
-    int e0, n;
+// Which experts a lane's NPL registers hold.
+//   without groups: vectors of kVec consecutive experts, vector after vector
+//     dealt to the lanes (one 16-byte load each), or single ones where E or
+//     the rows' alignment rules that out;
+//   with groups: 32 / G lanes hold a group, `c` consecutive experts each, so
+//     that a group is a run of whole lanes.
+template <int NPL, bool BF16, bool GROUPED>
+struct RowMap {
+    static constexpr int kFull = BF16 ? 8 : 4;
+    static constexpr int kVec = NPL < kFull ? NPL : kFull;
+    int e0, n, E;
+    bool vec; // 16-byte loads
+
+    __device__ __forceinline__ RowMap(const ep_router_desc_t& r, int lane, bool vec_) : E(r.num_experts), vec(vec_)
+    {
+        if (GROUPED) {
+            const int bits = 5 - (31 - __clz(r.num_groups)); // 2^bits lanes a group
+            const int per = E >> (5 - bits), c = (per + (1 << bits) - 1) >> bits;
+            const int q = lane & ((1 << bits) - 1);
+            e0 = (lane >> bits) * per + min(q * c, per);
+            n = max(0, min(c, per - q * c));
+        } else {
+            e0 = vec ? lane * kVec : lane;
+            n = E - e0;
+        }
+    }
+    // Register j holds expert e0 + offset(j), if holds(j).
+    __device__ __forceinline__ int offset(int j) const
+    {
+        if (GROUPED)
+            return j;
+        return vec ? (j / kVec) * (32 * kVec) + j % kVec : 32 * j;
+    }
+    __device__ __forceinline__ bool holds(int j) const { return offset(j) < n; }
 };
 
-__host__ __device__ __forceinline__ int run_length(int E, int G)
+int groups_run(const ep_router_desc_t& r) // c of RowMap
 {
-    const int lanes = 32 / G;
-    return (E / G + lanes - 1) / lanes;
-}
-
-__device__ __forceinline__ LaneRun lane_run(int E, int G, int lane)
-{
-    const int lanes = 32 / G, per = E / G, c = run_length(E, G);
-    const int g = lane / lanes, q = lane - g * lanes;
-    return {g * per + min(q * c, per), max(0, min(c, per - q * c))};
+    const int lanes = 32 / r.num_groups;
+    return (r.num_experts / r.num_groups + lanes - 1) / lanes;
 }
 
 // A logit as the operators take it: NaN closes the expert like -inf, values
@@ -53,36 +74,36 @@ __device__ __forceinline__ float load_logit(const void* logits, int64_t i)
     return __ldg(static_cast<const float*>(logits) + i);
 }
 
-// The lane's logits, closed ones and the places past its run as -inf.  vec:
-// every lane has NPL of them and the rows are aligned for vector loads.
-template <int NPL, bool BF16>
-__device__ __forceinline__ void load_row(float (&v)[NPL], const void* logits, int64_t row, int E, LaneRun r, bool vec)
+// The lane's logits, closed ones and registers that hold nothing as -inf.
+template <int NPL, bool BF16, bool GROUPED>
+__device__ __forceinline__ void load_row(float (&v)[NPL], const void* logits, int64_t row,
+                                         const RowMap<NPL, BF16, GROUPED>& map)
 {
-    const int64_t at = row * E + r.e0;
-    if (vec && !BF16 && NPL % 4 == 0) {
+    using Map = RowMap<NPL, BF16, GROUPED>;
+    const int64_t at = row * map.E + map.e0;
+    if (Map::kVec == Map::kFull && map.vec) {
 #pragma unroll
-        for (int j = 0; j < NPL / 4; ++j) {
-            const uint4 w = ld_nc_v4(static_cast<const float*>(logits) + at + 4 * j);
-            v[4 * j + 0] = __uint_as_float(w.x);
-            v[4 * j + 1] = __uint_as_float(w.y);
-            v[4 * j + 2] = __uint_as_float(w.z);
-            v[4 * j + 3] = __uint_as_float(w.w);
-        }
-    } else if (vec && BF16 && NPL % 8 == 0) {
-#pragma unroll
-        for (int j = 0; j < NPL / 8; ++j) {
-            const uint4 w = ld_nc_v4(static_cast<const uint16_t*>(logits) + at + 8 * j);
+        for (int j = 0; j < NPL; j += Map::kVec) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            const bool on = map.holds(j);
+            if (on)
+                w = BF16 ? ld_nc_v4(static_cast<const uint16_t*>(logits) + at + map.offset(j))
+                         : ld_nc_v4(static_cast<const float*>(logits) + at + map.offset(j));
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[8 * j + 2 * i] = bf16_lo(u[i]);
-                v[8 * j + 2 * i + 1] = bf16_hi(u[i]);
+                if (BF16) {
+                    v[(j + 2 * i) % NPL] = on ? bf16_lo(u[i]) : kNegInf;
+                    v[(j + 2 * i + 1) % NPL] = on ? bf16_hi(u[i]) : kNegInf;
+                } else {
+                    v[(j + i) % NPL] = on ? __uint_as_float(u[i]) : kNegInf;
+                }
             }
         }
     } else {
 #pragma unroll
         for (int j = 0; j < NPL; ++j)
-            v[j] = j < r.n ? load_logit<BF16>(logits, at + j) : kNegInf;
+            v[j] = map.holds(j) ? load_logit<BF16>(logits, at + map.offset(j)) : kNegInf;
     }
 #pragma unroll
     for (int j = 0; j < NPL; ++j)
@@ -123,6 +144,13 @@ __device__ __forceinline__ float row_max(const float (&v)[NPL])
 __device__ __forceinline__ float sigmoid(float l)
 {
     return 1.0f / (1.0f + expf(-l));
+}
+
+// exp and sigmoid for whole rows: ex2.approx of l * log2(e) (2 ulp, and the
+// product's half ulp, |l| * 2^-24 of the result) and a 2-ulp quotient.
+__device__ __forceinline__ float fast_sigmoid(float l)
+{
+    return __fdividef(1.0f, 1.0f + __expf(-l));
 }
 
 // Below this, sigmoid(l) = exp(l) to fp32 precision, and ratios of sigmoids are
@@ -238,27 +266,53 @@ __device__ __noinline__ int choose_wide(const RouterTopkLaunch& a, int64_t row, 
     return chosen;
 }
 
-// One warp a token.  Without bias and groups the choice is by the logits
-// themselves and exact.  Otherwise the fp32 values c carry an error of at most
-// err(c): half an ulp of the sum with the bias, and that of s,
-//   sigmoid: expf 2 ulp, the sum and the quotient half an ulp each, on s <= 1:
-//            6 * 2^-24 < 5e-7;
-//   softmax: l - max half an ulp of it (times p <= exp(l - max) / Z: at most
-//            0.37 / Z), expf 2 ulp, the sum of E terms NPL + 5 roundings and the
-//            same again inside, on p <= 1 / Z: less than 64 * 2^-24 / Z;
-// a row whose order those errors could change (adjacent chosen values, the last
-// chosen one and the next, the last group kept and the first one dropped) is
-// chosen again in fp64.  Values that are equal because logit and bias are
-// equal need no second look.
-template <int NPL, bool BF16>
+// Lane i of the first `count` gives its value and id: the lane's place in
+// descending order, equal values by id.
+template <typename T>
+__device__ __forceinline__ int place_in_order(T value, int e, int count)
+{
+    int place = 0;
+    for (int i = 0; i < count; ++i) {
+        const T o = __shfl_sync(kFullMask, value, i);
+        const int oe = __shfl_sync(kFullMask, e, i);
+        place += (o > value || (o == value && oe < e)) ? 1 : 0;
+    }
+    return place;
+}
+
+// One warp a token.
+//
+// Selection.  Let t be the K-th largest of the 32 lanes' largest values: K
+// values are at least t, so the K largest are among the values >= t, about a
+// dozen for K = 8 of 256.  They are gathered to one a lane and put in order by
+// counting, for each, those before it.  (If they are more than 32 - many equal
+// values, or K near 32 - the K largest are taken one by one instead.)
+//
+// Order.  Without bias and groups the choice is by the logits themselves and
+// exact.  Otherwise the fp32 values c carry an error of at most err(c): half
+// an ulp of the sum with the bias (twice, for the comparison's own rounding), and
+// that of s,
+//   sigmoid: 2 ulp of ex2 and |l| * 2^-24 on s (1 - s) <= 1/4 and |l| s (1 - s)
+//            <= 0.23, then the sum and the 2-ulp quotient: < 8 * 2^-24 < 5e-7;
+//   softmax: on p <= 1 / Z, l - max and its product with log2(e) half an ulp each
+//            (|l - max| exp(l - max) <= 0.37), 2 ulp of ex2, the sum of E terms
+//            NPL + 5 roundings and the same errors inside (the mean of |l -
+//            max| under p is at most log E <= 7), the quotient: < 64 * 2^-24 / Z;
+// a row whose order those errors could change is decided in fp64: the gathered
+// values alone where only their order is open, else (a value below t, or a
+// group, could come in) the whole row.  Values that are equal because logit
+// and bias are equal need no second look.
+template <int NPL, bool BF16, bool GROUPED>
 __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopkLaunch a, bool vec)
 {
     extern __shared__ double s_wide[];
+    __shared__ uint2 s_list[kTopkWarps][2][32]; // (key, expert): as gathered, in order
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTopkWarps + warp;
     if (t >= a.r.num_tokens)
         return;
-    const int E = a.r.num_experts, K = a.r.num_topk, G = a.r.num_groups;
+    const int E = a.r.num_experts, K = a.r.num_topk;
     int64_t* idx_out = a.topk_idx + t * K;
     float* w_out = a.topk_weights + t * K;
     if (a.token_mask != nullptr && __ldg(a.token_mask + t) == 0) {
@@ -269,10 +323,10 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
         return;
     }
     const bool softmax = a.r.score == EP_SCORE_SOFTMAX;
-    const bool by_logit = a.bias == nullptr && G == 1;
-    const LaneRun r = lane_run(E, G, lane);
+    const bool by_logit = !GROUPED && a.bias == nullptr;
+    const RowMap<NPL, BF16, GROUPED> map(a.r, lane, vec);
     float v[NPL];
-    load_row<NPL, BF16>(v, a.logits, t, E, r, vec);
+    load_row(v, a.logits, t, map);
 
     float m = 0.0f, z = 1.0f;
     if (softmax && (!by_logit || a.r.normalize == 0)) {
@@ -280,12 +334,12 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < NPL; ++j)
-            sum += v[j] > kNegInf ? expf(v[j] - m) : 0.0f;
+            sum += v[j] > kNegInf ? __expf(v[j] - m) : 0.0f;
         z = warp_sum(sum);
     }
     const float es = softmax ? 4e-6f / z : 5e-7f;
     const auto err = [es](float c) { return es + 1.3e-7f * fabsf(c); };
-    bool sure = true;
+    bool sure = true; // no group's place is open
     uint32_t key[NPL];
     if (by_logit) {
 #pragma unroll
@@ -293,23 +347,24 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
             key[j] = v[j] > kNegInf ? order_key(v[j]) : 0u;
     } else {
         float c[NPL];
+        const float inv_z = 1.0f / z;
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-            float s = softmax ? expf(v[j] - m) / z : sigmoid(v[j]);
-            if (a.bias != nullptr && j < r.n)
-                s += __ldg(a.bias + r.e0 + j);
+            float s = softmax ? __expf(v[j] - m) * inv_z : fast_sigmoid(v[j]);
+            if (a.bias != nullptr && map.holds(j))
+                s += __ldg(a.bias + map.e0 + map.offset(j));
             c[j] = v[j] > kNegInf && s > kNegInf ? s : kNegInf;
         }
         bool stay = true;
-        if (G > 1 && a.r.topk_groups < G) {
-            const int lanes = 32 / G, mine = lane / lanes;
+        if (GROUPED && a.r.topk_groups < a.r.num_groups) {
+            const int G = a.r.num_groups, bits = 5 - (31 - __clz(G)), mine = lane >> bits;
             float t1 = kNegInf, t2 = kNegInf;
 #pragma unroll
             for (int j = 0; j < NPL; ++j) {
                 t2 = fmaxf(t2, fminf(t1, c[j]));
                 t1 = fmaxf(t1, c[j]);
             }
-            for (int d = lanes >> 1; d >= 1; d >>= 1) {
+            for (int d = (1 << bits) >> 1; d >= 1; d >>= 1) {
                 const float o1 = __shfl_xor_sync(kFullMask, t1, d), o2 = __shfl_xor_sync(kFullMask, t2, d);
                 t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
                 t1 = fmaxf(t1, o1);
@@ -319,7 +374,7 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
             const float ge = err(t1) + (two ? err(t2) : 0.0f) + 1.3e-7f * fabsf(value);
             int before = 0;
             for (int g = 0; g < G; ++g) {
-                const float o = __shfl_sync(kFullMask, value, g * lanes);
+                const float o = __shfl_sync(kFullMask, value, g << bits);
                 before += (o > value || (o == value && g < mine)) ? 1 : 0;
             }
             stay = before < a.r.topk_groups;
@@ -332,62 +387,124 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
             key[j] = stay && c[j] > kNegInf ? order_key(c[j]) : 0u;
     }
 
-    // the K largest, in order, one a step: lane k keeps the k-th; the check
-    // needs the one after them too
-    int my_idx = -1, next_idx = -1;
-    uint32_t my_key = 0u, next_key = 0u;
-    const int steps = by_logit ? K : K + 1;
-    for (int k = 0; k < steps; ++k) {
-        uint32_t best = 0u;
-        int bj = 0;
+    // lane k: the k-th chosen, and those after it as far as they are known
+    int my_idx = -1;
+    uint32_t my_key = 0u;
+    uint32_t best = key[0];
 #pragma unroll
-        for (int j = 0; j < NPL; ++j)
-            if (key[j] > best) {
-                best = key[j];
-                bj = j;
-            }
-        const uint32_t top = __reduce_max_sync(kFullMask, best);
-        if (top == 0u)
+    for (int j = 1; j < NPL; ++j)
+        best = max(best, key[j]);
+    // (two values more where the order has to be checked: what comes after the
+    // K-th is then known, and what is not gathered is well below it)
+    uint32_t least = 0u;
+    const int values = by_logit ? K : K + 2;
+    for (int k = 0; k < values; ++k) {
+        least = __reduce_max_sync(kFullMask, best);
+        if (least == 0u)
             break;
-        const int from = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
-        const int e = __shfl_sync(kFullMask, r.e0 + bj, from);
-        if (lane == from) {
+        if (best == least)
+            best = 0u;
+    }
+    const bool all = least == 0u; // everything that can be chosen is gathered
+    least = max(least, 1u);
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+        const bool in = key[j] >= least;
+        const uint32_t who = __ballot_sync(kFullMask, in);
+        const int at = count + __popc(who & ((1u << lane) - 1u));
+        if (in && at < 32)
+            s_list[warp][0][at] = make_uint2(key[j], static_cast<uint32_t>(map.e0 + map.offset(j)));
+        count += __popc(who);
+    }
+    __syncwarp();
+    uint32_t after = 0u; // one by one: the (K + 1)-th value
+    if (count <= 32) {
+        uint2 mine = make_uint2(0u, 0u);
+        if (lane < count)
+            mine = s_list[warp][0][lane];
+        int place = 0;
+        for (int i = 0; i < count; ++i) {
+            const uint2 o = s_list[warp][0][i];
+            place += (o.x > mine.x || (o.x == mine.x && o.y < mine.y)) ? 1 : 0;
+        }
+        if (lane < count)
+            s_list[warp][1][place] = mine;
+        __syncwarp();
+        if (lane < count) {
+            mine = s_list[warp][1][lane];
+            my_key = mine.x;
+            my_idx = static_cast<int>(mine.y);
+        }
+    } else {
+        for (int k = 0; k <= K; ++k) {
+            uint32_t top = 0u;
+            int e = E;
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
-                if (j == bj)
+                if (key[j] > top) {
+                    top = key[j];
+                    e = map.e0 + map.offset(j);
+                }
+            after = __reduce_max_sync(kFullMask, top);
+            if (after == 0u)
+                break;
+            const int first = static_cast<int>(__reduce_min_sync(kFullMask, static_cast<uint32_t>(top == after ? e : E)));
+#pragma unroll
+            for (int j = 0; j < NPL; ++j)
+                if (map.e0 + map.offset(j) == first)
                     key[j] = 0u;
-        }
-        if (lane == k) {
-            my_idx = e;
-            my_key = top;
-        }
-        if (k == K) {
-            next_idx = e;
-            next_key = top;
-        }
-    }
-    if (!by_logit && sure) {
-        const float l = my_idx >= 0 ? clean_logit(load_logit<BF16>(a.logits, t * E + my_idx)) : 0.0f;
-        const float b = my_idx >= 0 && a.bias != nullptr ? __ldg(a.bias + my_idx) : 0.0f;
-        uint32_t nk = __shfl_down_sync(kFullMask, my_key, 1);
-        float nl = __shfl_down_sync(kFullMask, l, 1), nb = __shfl_down_sync(kFullMask, b, 1);
-        if (lane == K - 1) {
-            nk = next_key;
-            if (next_idx >= 0) {
-                nl = clean_logit(load_logit<BF16>(a.logits, t * E + next_idx));
-                nb = a.bias != nullptr ? __ldg(a.bias + next_idx) : 0.0f;
+            if (lane == k && k < K) {
+                my_idx = first;
+                my_key = after;
             }
         }
-        bool apart = true;
-        if (lane < K && nk != 0u) {
-            const float c = key_value(my_key), n = key_value(nk);
-            apart = c - err(c) > n + err(n) || (l == nl && b == nb);
-        }
-        sure = __all_sync(kFullMask, apart);
     }
-    if (!sure)
-        my_idx = choose_wide<BF16>(a, t, s_wide + static_cast<size_t>(warp) * E, lane);
-    else if (lane >= K)
+    if (!by_logit) {
+        const float l = my_idx >= 0 ? clean_logit(load_logit<BF16>(a.logits, t * E + my_idx)) : 0.0f;
+        const float b = my_idx >= 0 && a.bias != nullptr ? __ldg(a.bias + my_idx) : 0.0f;
+        uint32_t next = __shfl_down_sync(kFullMask, my_key, 1);
+        const float nl = __shfl_down_sync(kFullMask, l, 1), nb = __shfl_down_sync(kFullMask, b, 1);
+        const uint32_t last = __shfl_sync(kFullMask, my_key, K - 1); // 0: fewer than K
+        const float c = key_value(my_key);
+        // the order of the chosen, and of what is equal to the last of them
+        bool like = l == nl && b == nb, open = lane < K || my_key == last;
+        if (lane == 31)
+            next = 0u;
+        if (count > 32 && lane == K - 1) {
+            next = after; // more of these values may follow: equal ones settle nothing
+            like = false;
+        }
+        const float n = key_value(next);
+        const bool order = __all_sync(kFullMask, !open || my_key == 0u || next == 0u || like || c - err(c) > n + err(n));
+        // what was not gathered is below `least`
+        const float k_th = key_value(last), rest = key_value(least);
+        const bool closed = all || count > 32 || k_th - err(k_th) > rest + err(rest);
+        if (!sure || !closed || (!order && count > 32)) {
+            my_idx = choose_wide<BF16>(a, t, s_wide + static_cast<size_t>(warp) * E, lane);
+        } else if (!order) {
+            double sum = 1.0;
+            if (softmax) {
+                sum = 0.0;
+#pragma unroll 1
+                for (int e = lane; e < E; e += 32) {
+                    const float o = clean_logit(load_logit<BF16>(a.logits, t * E + e));
+                    sum += o > kNegInf ? exp(static_cast<double>(o) - m) : 0.0;
+                }
+                for (int d = 16; d >= 1; d >>= 1)
+                    sum += __shfl_xor_sync(kFullMask, sum, d);
+            }
+            const double l64 = l;
+            const double c64 = (softmax ? exp(l64 - m) / sum : 1.0 / (1.0 + exp(-l64))) + b;
+            const int place = place_in_order(c64, my_idx, count);
+            if (lane < count)
+                s_list[warp][0][place].y = static_cast<uint32_t>(my_idx);
+            __syncwarp();
+            if (lane < count)
+                my_idx = static_cast<int>(s_list[warp][0][lane].y);
+        }
+    }
+    if (lane >= K)
         my_idx = -1;
 
     const bool got = my_idx >= 0;
@@ -409,31 +526,41 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
 }
 
 // ------------------------------------------------------------ balance loss
-// Tokens are dealt out in chunks of at most kChunk tokens of one sequence,
-// sequence after sequence: a CTA sums one chunk into its own partial row, and
-// a second kernel sums each sequence's partial rows in order (fixed order, no
-// floating-point atomics).
-constexpr int kChunk = 64;
-constexpr int kBalanceWarps = 8;
+// Tokens are dealt out in chunks of at most `chunk` tokens of one sequence,
+// sequence after sequence.  A CTA sums a chunk; where that is the whole
+// sequence it writes the results, else it leaves its sums in the workspace and
+// a CTA of the second kernel adds the sequence's up in chunk order (fixed
+// order, no floating-point atomics, nothing that one call leaves for the next).
+constexpr int kBalanceWarps = 16;
+constexpr int kBalanceThreads = kBalanceWarps * 32;
+constexpr int kBalanceCtas = 148; // chunks of a long batch: one a CTA and SM
 
-__host__ __device__ __forceinline__ int64_t balance_items(int64_t T, int64_t S)
+// Tokens a chunk, a multiple of the warps.
+__host__ __device__ __forceinline__ int chunk_tokens(int64_t T)
 {
-    return (T + kChunk - 1) / kChunk + S; // at most one part chunk a sequence
+    const int64_t each = (T + kBalanceCtas - 1) / kBalanceCtas;
+    return static_cast<int>((each + kBalanceWarps - 1) / kBalanceWarps * kBalanceWarps);
 }
 
-struct BalancePartials {
-    float* q;     // [items, E]
-    int32_t* cnt; // [items, E]
-    float* z;     // [items]
-    int32_t* n;   // [items]
+// Most chunks that T tokens in S sequences make (at most one part one a
+// sequence); grows with T.
+__host__ __device__ __forceinline__ int64_t most_chunks(int64_t T, int64_t S)
+{
+    const int64_t full = (T + kBalanceWarps - 1) / kBalanceWarps;
+    return (full < kBalanceCtas ? full : kBalanceCtas) + S;
+}
+
+// Workspace: each chunk's sums (score, count) per expert, then its (sum of
+// lse^2, tokens).
+struct BalanceSums {
+    int2* sums;  // [chunks, E]: bits of the fp32 sum, count
+    int2* tails; // [chunks]: bits of the fp32 sum, tokens
 };
 
-__host__ __device__ __forceinline__ BalancePartials balance_partials(void* workspace, int64_t items, int64_t E)
+__device__ __forceinline__ BalanceSums balance_sums(void* workspace, int64_t chunks, int E)
 {
-    float* q = static_cast<float*>(workspace);
-    int32_t* cnt = reinterpret_cast<int32_t*>(q + items * E);
-    float* z = reinterpret_cast<float*>(cnt + items * E);
-    return {q, cnt, z, reinterpret_cast<int32_t*>(z + items)};
+    int2* sums = static_cast<int2*>(workspace);
+    return {sums, sums + chunks * E};
 }
 
 struct TokenRange {
@@ -449,31 +576,23 @@ __device__ __forceinline__ TokenRange seq_range(const int32_t* offsets, int T, i
     return {b, min(max(__ldg(offsets + s + 1), b), T)};
 }
 
-// Chunks of the sequences before s, for s = S all of them; one warp, lanes agree.
-__device__ __forceinline__ int64_t chunks_before(const int32_t* offsets, int T, int s, int lane)
-{
-    int64_t total = 0;
-    for (int base = 0; base < s; base += 32) {
-        int n = 0;
-        if (base + lane < s) {
-            const TokenRange r = seq_range(offsets, T, base + lane);
-            n = (r.end - r.begin + kChunk - 1) / kChunk;
-        }
-        total += __reduce_add_sync(kFullMask, n);
-    }
-    return total;
-}
+struct Chunk {
+    int64_t first, index; // the sequence's first chunk, this one
+    int seq, of;          // the sequence, its number of chunks
+    TokenRange tokens;
+};
 
-// The sequence and chunk of item i; false when there are fewer items.
-__device__ __forceinline__ bool find_chunk(const int32_t* offsets, int T, int S, int64_t i, int lane, int& seq,
-                                           TokenRange& tokens)
+// Chunk i, and the number of chunks in all (the return value); i past them
+// leaves `c` as it was.  One warp; lanes agree.
+__device__ __forceinline__ int64_t find_chunk(const int32_t* offsets, int T, int S, int chunk, int64_t i, int lane,
+                                              Chunk& c)
 {
     int64_t before = 0;
     for (int base = 0; base < S; base += 32) {
         int n = 0;
         if (base + lane < S) {
             const TokenRange r = seq_range(offsets, T, base + lane);
-            n = (r.end - r.begin + kChunk - 1) / kChunk;
+            n = (r.end - r.begin + chunk - 1) / chunk;
         }
         int inc = n;
 #pragma unroll
@@ -482,65 +601,141 @@ __device__ __forceinline__ bool find_chunk(const int32_t* offsets, int T, int S,
             if (lane >= d)
                 inc += o;
         }
-        const uint32_t past = __ballot_sync(kFullMask, before + inc > i);
-        if (past != 0u) {
-            const int l = __ffs(past) - 1;
-            const int64_t first = before + __shfl_sync(kFullMask, inc - n, l);
-            seq = base + l;
-            const TokenRange r = seq_range(offsets, T, seq);
-            tokens.begin = r.begin + static_cast<int>(i - first) * kChunk;
-            tokens.end = min(r.end, tokens.begin + kChunk);
-            return true;
+        const int l = __ffs(__ballot_sync(kFullMask, before <= i && before + inc > i)) - 1;
+        if (l >= 0) {
+            c.of = __shfl_sync(kFullMask, n, l);
+            c.first = before + __shfl_sync(kFullMask, inc, l) - c.of;
+            c.index = i;
+            c.seq = base + l;
+            const TokenRange r = seq_range(offsets, T, c.seq);
+            c.tokens.begin = r.begin + static_cast<int>(i - c.first) * chunk;
+            c.tokens.end = min(r.end, c.tokens.begin + chunk);
         }
         before += __shfl_sync(kFullMask, inc, 31);
     }
-    return false;
+    return before;
+}
+
+struct SeqChunks {
+    int64_t first, total; // the sequence's first chunk; the chunks of all
+    int of;               // the sequence's chunks
+};
+
+__device__ __forceinline__ SeqChunks find_seq_chunks(const int32_t* offsets, int T, int S, int chunk, int s, int lane)
+{
+    int64_t before = 0, total = 0;
+    int of = 0;
+    for (int i = lane; i < S; i += 32) {
+        const TokenRange r = seq_range(offsets, T, i);
+        const int n = (r.end - r.begin + chunk - 1) / chunk;
+        total += n;
+        before += i < s ? n : 0;
+        of = i == s ? n : of;
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+        before += __shfl_xor_sync(kFullMask, before, d);
+        total += __shfl_xor_sync(kFullMask, total, d);
+        of = max(of, __shfl_xor_sync(kFullMask, of, d));
+    }
+    return {before, total, of};
+}
+
+// The results of sequence s from its sums: thread e < E holds expert e's.  All
+// threads of the CTA; red: kBalanceWarps floats of shared memory.
+__device__ __forceinline__ void write_balance(const BalanceLaunch& a, int s, int tokens, float lse2, const float* q,
+                                              const int* cnt, float* red)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.r.num_experts;
+    const float n = static_cast<float>(tokens);
+    float fp = 0.0f;
+    for (int e = tid; e < E; e += kBalanceThreads) {
+        const float mean = tokens > 0 ? q[e] / n : 0.0f;
+        const int64_t at = static_cast<int64_t>(s) * E + e;
+        a.counts[at] = tokens > 0 ? cnt[e] : 0;
+        if (a.mean_scores != nullptr)
+            a.mean_scores[at] = mean;
+        fp += static_cast<float>(cnt[e]) * mean;
+    }
+    fp = warp_sum(fp);
+    if (lane == 0)
+        red[warp] = fp;
+    __syncthreads();
+    if (tid == 0) {
+        float sum = 0.0f;
+        for (int w = 0; w < kBalanceWarps; ++w)
+            sum += red[w];
+        const float scale = static_cast<float>(E) / (static_cast<float>(a.r.num_topk) * n);
+        a.losses[2 * s] = tokens > 0 ? sum * scale : 0.0f;
+        a.losses[2 * s + 1] = tokens > 0 ? lse2 / n : 0.0f;
+        a.seq_tokens[s] = tokens;
+    }
 }
 
 template <int NPL, bool BF16>
-__global__ void __launch_bounds__(kBalanceWarps * 32) balance_chunk_kernel(BalanceLaunch a, bool vec)
+__global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch a, int chunk, bool vec)
 {
-    extern __shared__ float s_q[]; // [kBalanceWarps, E] sums, then [E] counts
-    __shared__ float s_z[kBalanceWarps];
+    // [2 * kBalanceWarps, E] floats at most: each warp's sums, then the experts'
+    extern __shared__ float s_q[];
+    __shared__ float s_z[kBalanceWarps], s_red[kBalanceWarps];
     __shared__ int s_n[kBalanceWarps];
+    pdl_wait();
+    pdl_launch_dependents(); // balance_finish_kernel, which waits for this grid
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int E = a.r.num_experts, K = a.r.num_topk, T = a.r.num_tokens;
-    int32_t* s_cnt = reinterpret_cast<int32_t*>(s_q + kBalanceWarps * E);
-    int seq;
-    TokenRange tokens;
-    if (!find_chunk(a.seq_offsets, T, a.num_seqs, blockIdx.x, lane, seq, tokens))
-        return; // the whole CTA: every warp sees the same answer
-    for (int e = tid; e < E; e += blockDim.x)
+    const int E = a.r.num_experts, K = a.r.num_topk, T = a.r.num_tokens, S = a.num_seqs;
+    int* s_cnt = reinterpret_cast<int*>(s_q + kBalanceWarps * E);
+    const int64_t chunks = most_chunks(T, S);
+    const BalanceSums part = balance_sums(a.workspace, chunks, E);
+    Chunk c{};
+    const int64_t total = find_chunk(a.seq_offsets, T, S, chunk, blockIdx.x, lane, c);
+    const bool sound = total <= chunks; // else the offsets are not sorted: no sequence has tokens
+    for (int64_t s = blockIdx.x; s < S; s += gridDim.x) { // sequences without tokens
+        const TokenRange r = seq_range(a.seq_offsets, T, static_cast<int>(s));
+        if (sound && r.begin < r.end)
+            continue;
+        for (int e = tid; e < E; e += kBalanceThreads) {
+            a.counts[s * E + e] = 0;
+            if (a.mean_scores != nullptr)
+                a.mean_scores[s * E + e] = 0.0f;
+        }
+        if (tid == 0) {
+            a.losses[2 * s] = a.losses[2 * s + 1] = 0.0f;
+            a.seq_tokens[s] = 0;
+        }
+    }
+    if (!sound || static_cast<int64_t>(blockIdx.x) >= total)
+        return;
+    for (int e = tid; e < E; e += kBalanceThreads)
         s_cnt[e] = 0;
     __syncthreads();
 
     const bool softmax = a.r.score == EP_SCORE_SOFTMAX;
-    const LaneRun r = lane_run(E, 1, lane);
+    const RowMap<NPL, BF16, false> map(a.r, lane, vec);
     float acc[NPL];
 #pragma unroll
     for (int j = 0; j < NPL; ++j)
         acc[j] = 0.0f;
     float zz = 0.0f;
     int live = 0;
-    for (int t = tokens.begin + warp; t < tokens.end; t += kBalanceWarps) {
+    for (int t = c.tokens.begin + warp; t < c.tokens.end; t += kBalanceWarps) {
         if (a.token_mask != nullptr && __ldg(a.token_mask + t) == 0)
             continue;
         float v[NPL];
-        load_row<NPL, BF16>(v, a.logits, t, E, r, vec);
+        load_row(v, a.logits, t, map);
+        int64_t e = -1;
+        if (lane < K)
+            e = __ldg(a.topk_idx + static_cast<int64_t>(t) * K + lane);
         const float m = row_max(v);
         if (!(m > kNegInf))
             continue; // every expert closed
-        if (lane < K) {
-            const int64_t e = __ldg(a.topk_idx + static_cast<int64_t>(t) * K + lane);
-            if (e >= 0 && e < E)
-                atomicAdd(s_cnt + e, 1);
-        }
+        if (e >= 0 && e < E)
+            atomicAdd(s_cnt + e, 1);
         ++live;
         float sum = 0.0f;
         float p[NPL];
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-            p[j] = v[j] > kNegInf ? expf(v[j] - m) : 0.0f;
+            p[j] = v[j] > kNegInf ? __expf(v[j] - m) : 0.0f;
             sum += p[j];
         }
         sum = warp_sum(sum);
@@ -550,7 +745,7 @@ __global__ void __launch_bounds__(kBalanceWarps * 32) balance_chunk_kernel(Balan
             sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < NPL; ++j) {
-                p[j] = v[j] > kNegInf ? sigmoid(v[j]) : 0.0f;
+                p[j] = v[j] > kNegInf ? fast_sigmoid(v[j]) : 0.0f;
                 sum += p[j];
             }
             sum = warp_sum(sum);
@@ -562,109 +757,100 @@ __global__ void __launch_bounds__(kBalanceWarps * 32) balance_chunk_kernel(Balan
     }
 #pragma unroll
     for (int j = 0; j < NPL; ++j)
-        if (j < r.n)
-            s_q[warp * E + r.e0 + j] = acc[j];
+        if (map.holds(j))
+            s_q[warp * E + map.e0 + map.offset(j)] = acc[j];
     if (lane == 0) {
         s_z[warp] = zz;
         s_n[warp] = live;
     }
     __syncthreads();
-    const BalancePartials part = balance_partials(a.workspace, balance_items(T, a.num_seqs), E);
-    const int64_t item = blockIdx.x;
-    for (int e = tid; e < E; e += blockDim.x) {
+    for (int e = tid; e < E; e += kBalanceThreads) {
         float sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kBalanceWarps; ++w)
             sum += s_q[w * E + e];
-        part.q[item * E + e] = sum;
-        part.cnt[item * E + e] = s_cnt[e];
+        s_q[e] = sum; // only this thread reads the column again
+        if (c.of > 1)
+            part.sums[c.index * E + e] = make_int2(__float_as_int(sum), s_cnt[e]);
     }
-    if (tid == 0) {
-        float z = 0.0f;
-        int n = 0;
-        for (int w = 0; w < kBalanceWarps; ++w) {
-            z += s_z[w];
-            n += s_n[w];
-        }
-        part.z[item] = z;
-        part.n[item] = n;
+    float z = 0.0f;
+    int n = 0;
+    for (int w = 0; w < kBalanceWarps; ++w) {
+        z += s_z[w];
+        n += s_n[w];
     }
+    if (c.of == 1) {
+        write_balance(a, c.seq, n, z, s_q, s_cnt, s_red);
+        return;
+    }
+    if (tid == 0)
+        part.tails[c.index] = make_int2(__float_as_int(z), n);
 }
 
-// One CTA a sequence: its chunks' partial rows summed, then the losses.  The
-// CTA's threads are `slices` runs of E (rounded up to whole warps); each run
-// sums every slices-th chunk, and the runs are added in order.
-constexpr int kFinishThreads = 1024;
-
-__global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(BalanceLaunch a)
+// One CTA a sequence: the results of those that are made of several chunks.
+__global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(BalanceLaunch a, int chunk)
 {
-    __shared__ float s_sum[kFinishThreads];
-    __shared__ int s_cnt[kFinishThreads];
-    __shared__ float s_red[kFinishThreads / 32];
-    __shared__ int s_tokens;
-    __shared__ float s_zsum;
+    extern __shared__ float s_q[]; // [2 * kBalanceWarps, E] floats at most, as above
+    __shared__ float s_z, s_red[kBalanceWarps];
+    __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int E = a.r.num_experts, T = a.r.num_tokens, s = blockIdx.x;
-    const int64_t items = balance_items(T, a.num_seqs);
-    const BalancePartials part = balance_partials(a.workspace, items, E);
-    const int64_t i0 = min(items, chunks_before(a.seq_offsets, T, s, lane));
-    const TokenRange tokens = seq_range(a.seq_offsets, T, s);
-    const int64_t i1 = min(items, i0 + (tokens.end - tokens.begin + kChunk - 1) / kChunk);
+    const int E = a.r.num_experts, T = a.r.num_tokens, S = a.num_seqs, s = blockIdx.x;
+    int* s_cnt = reinterpret_cast<int*>(s_q + kBalanceWarps * E);
+    const int64_t chunks = most_chunks(T, S);
+    const BalanceSums part = balance_sums(a.workspace, chunks, E);
+    // (what it reads before the wait is older than the kernel that it waits for)
+    const SeqChunks c = find_seq_chunks(a.seq_offsets, T, S, chunk, s, lane);
+    pdl_wait();
+    if (c.of <= 1 || c.total > chunks)
+        return;
+    // the chunks in order: each run of `width` threads takes every runs-th one
+    const int width = (E + 31) / 32 * 32, runs = max(1, kBalanceThreads / width);
+    const int run = tid / width;
+    for (int e = tid % width; e < E && run < runs; e += kBalanceThreads) {
+        float q = 0.0f;
+        int cnt = 0;
+#pragma unroll 16
+        for (int i = run; i < c.of; i += runs) {
+            const int2 o = __ldcg(part.sums + (c.first + i) * E + e);
+            q += __int_as_float(o.x);
+            cnt += o.y;
+        }
+        s_q[run * E + e] = q;
+        s_cnt[run * E + e] = cnt;
+    }
     if (warp == 0) {
-        int n = 0;
         float z = 0.0f;
-        for (int64_t i = i0 + lane; i < i1; i += 32) {
-            n += part.n[i];
-            z += part.z[i];
+        int n = 0;
+        for (int i = lane; i < c.of; i += 32) {
+            const int2 o = __ldcg(part.tails + c.first + i);
+            z += __int_as_float(o.x);
+            n += o.y;
         }
-        n = __reduce_add_sync(kFullMask, n);
         z = warp_sum(z);
+        n = __reduce_add_sync(kFullMask, n);
         if (lane == 0) {
-            s_tokens = n;
-            s_zsum = z;
+            s_z = z;
+            s_n = n;
         }
     }
-    const int width = (E + 31) / 32 * 32;
-    const int slices = kFinishThreads / width;
-    const int e = tid % width, slice = tid / width;
-    float q = 0.0f;
-    int cnt = 0;
-    if (e < E && slice < slices) {
-#pragma unroll 8
-        for (int64_t i = i0 + slice; i < i1; i += slices) {
-            q += part.q[i * E + e];
-            cnt += part.cnt[i * E + e];
-        }
-    }
-    s_sum[tid] = q;
-    s_cnt[tid] = cnt;
     __syncthreads();
-    const int n = s_tokens;
-    float fp = 0.0f;
-    if (tid < E) {
-        for (int i = 1; i < slices; ++i) {
-            q += s_sum[i * width + tid];
-            cnt += s_cnt[i * width + tid];
+    if (runs > 1) {
+        float q = 0.0f;
+        int cnt = 0;
+        if (tid < E) {
+            for (int i = 0; i < runs; ++i) {
+                q += s_q[i * E + tid];
+                cnt += s_cnt[i * E + tid];
+            }
         }
-        const float mean = n > 0 ? q / static_cast<float>(n) : 0.0f;
-        a.counts[static_cast<int64_t>(s) * E + tid] = cnt;
-        if (a.mean_scores != nullptr)
-            a.mean_scores[static_cast<int64_t>(s) * E + tid] = mean;
-        fp = static_cast<float>(cnt) * mean;
-    }
-    fp = warp_sum(fp);
-    if (lane == 0)
-        s_red[warp] = fp;
-    __syncthreads();
-    if (warp == 0) {
-        fp = warp_sum(s_red[lane]);
-        if (lane == 0) {
-            const float nf = static_cast<float>(n);
-            a.losses[2 * s] = n > 0 ? fp * (static_cast<float>(E) / (static_cast<float>(a.r.num_topk) * nf)) : 0.0f;
-            a.losses[2 * s + 1] = n > 0 ? s_zsum / nf : 0.0f;
-            a.seq_tokens[s] = n;
+        __syncthreads();
+        if (tid < E) {
+            s_q[tid] = q;
+            s_cnt[tid] = cnt;
         }
+        __syncthreads();
     }
+    write_balance(a, s, s_n, s_z, s_q, s_cnt, s_red);
 }
 
 // ---------------------------------------------------------------- backward
@@ -696,12 +882,14 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(Ro
 {
     extern __shared__ float s_add[]; // [kBackwardWarps, E]: the chosen experts' part
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kBackwardWarps + warp;
     if (t >= a.r.num_tokens)
         return;
     const int E = a.r.num_experts, K = a.r.num_topk;
     const bool softmax = a.r.score == EP_SCORE_SOFTMAX;
-    const LaneRun r = lane_run(E, 1, lane);
+    const RowMap<NPL, BF16, false> map(a.r, lane, vec);
+    using Map = RowMap<NPL, BF16, false>;
     float* add = s_add + static_cast<size_t>(warp) * E;
 
     float d[NPL];
@@ -712,7 +900,7 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(Ro
     float v[NPL];
     float m = kNegInf;
     if (on) {
-        load_row<NPL, BF16>(v, a.logits, t, E, r, vec);
+        load_row(v, a.logits, t, map);
         m = row_max(v);
     }
     if (m > kNegInf) {
@@ -721,7 +909,7 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(Ro
         float z = 0.0f;
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-            p[j] = v[j] > kNegInf ? expf(v[j] - m) : 0.0f;
+            p[j] = v[j] > kNegInf ? __expf(v[j] - m) : 0.0f;
             z += p[j];
         }
         z = warp_sum(z);
@@ -762,8 +950,8 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(Ro
             }
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
-                if (j < r.n)
-                    add[r.e0 + j] = 0.0f;
+                if (map.holds(j))
+                    add[map.e0 + map.offset(j)] = 0.0f;
             __syncwarp();
             // slots of one expert (a caller's own ids) are added in slot order
             const uint32_t same = __match_any_sync(kFullMask, got ? static_cast<int>(e) : -1 - lane);
@@ -780,8 +968,8 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(Ro
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
-                if (j < r.n)
-                    d[j] = add[r.e0 + j] - p[j] * through;
+                if (map.holds(j))
+                    d[j] = add[map.e0 + map.offset(j)] - p[j] * through;
         }
 
         if (a.d_losses != nullptr) {
@@ -791,12 +979,16 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(Ro
                 const float nf = static_cast<float>(n);
                 const float gb = __ldg(a.d_losses + 2 * s) * (static_cast<float>(E) / (static_cast<float>(K) * nf)) / nf;
                 const float gz = __ldg(a.d_losses + 2 * s + 1) * 2.0f * (m + logf(z)) / nf;
-                const int32_t* cnt = a.counts + static_cast<int64_t>(s) * E + r.e0;
+                const int32_t* cnt = a.counts + static_cast<int64_t>(s) * E + map.e0;
                 float c[NPL], q[NPL];
 #pragma unroll
                 for (int j = 0; j < NPL; ++j)
-                    c[j] = j < r.n ? static_cast<float>(__ldg(cnt + j)) : 0.0f;
-                if (softmax || m < kSigmoidTail) {
+                    c[j] = map.holds(j) ? static_cast<float>(__ldg(cnt + map.offset(j))) : 0.0f;
+                float rest[NPL]; // ds / dl = s * rest
+#pragma unroll
+                for (int j = 0; j < NPL; ++j)
+                    rest[j] = 1.0f;
+                if (softmax || m < kSigmoidTail) { // there 1 - s is 1 too
 #pragma unroll
                     for (int j = 0; j < NPL; ++j)
                         q[j] = p[j];
@@ -804,7 +996,8 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(Ro
                     float total = 0.0f;
 #pragma unroll
                     for (int j = 0; j < NPL; ++j) {
-                        q[j] = v[j] > kNegInf ? sigmoid(v[j]) : 0.0f;
+                        q[j] = v[j] > kNegInf ? fast_sigmoid(v[j]) : 0.0f;
+                        rest[j] = fast_sigmoid(-v[j]);
                         total += q[j];
                     }
                     const float inv = 1.0f / warp_sum(total);
@@ -818,59 +1011,84 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(Ro
                     mean += c[j] * q[j];
                 mean = warp_sum(mean);
 #pragma unroll
-                for (int j = 0; j < NPL; ++j) {
-                    const float rest = softmax ? 1.0f : 1.0f / (1.0f + expf(v[j])); // ds/dl = s (1 - s)
-                    d[j] += gb * q[j] * rest * (c[j] - mean) + gz * p[j];
-                }
+                for (int j = 0; j < NPL; ++j)
+                    d[j] += gb * q[j] * rest[j] * (c[j] - mean) + gz * p[j];
             }
         }
     }
-    const int64_t at = t * E + r.e0;
-    if (BF16) {
-        uint16_t* out = static_cast<uint16_t*>(a.d_logits) + at;
-        if (vec && NPL % 8 == 0) {
+    const int64_t at = t * E + map.e0;
+    if (Map::kVec == Map::kFull && vec) {
 #pragma unroll
-            for (int j = 0; j < NPL / 8; ++j)
-                st_v4(out + 8 * j, make_uint4(pack_bf16x2(d[8 * j], d[8 * j + 1]), pack_bf16x2(d[8 * j + 2], d[8 * j + 3]),
-                                              pack_bf16x2(d[8 * j + 4], d[8 * j + 5]),
-                                              pack_bf16x2(d[8 * j + 6], d[8 * j + 7])));
-        } else {
-#pragma unroll
-            for (int j = 0; j < NPL; ++j)
-                if (j < r.n)
-                    out[j] = static_cast<uint16_t>(pack_bf16x2(d[j], 0.0f));
+        for (int j = 0; j < NPL; j += Map::kVec) {
+            if (!map.holds(j))
+                continue;
+            uint4 w;
+            if (BF16) {
+                w = make_uint4(pack_bf16x2(d[j], d[(j + 1) % NPL]), pack_bf16x2(d[(j + 2) % NPL], d[(j + 3) % NPL]),
+                               pack_bf16x2(d[(j + 4) % NPL], d[(j + 5) % NPL]),
+                               pack_bf16x2(d[(j + 6) % NPL], d[(j + 7) % NPL]));
+                st_v4(static_cast<uint16_t*>(a.d_logits) + at + map.offset(j), w);
+            } else {
+                w = make_uint4(__float_as_uint(d[j]), __float_as_uint(d[(j + 1) % NPL]),
+                               __float_as_uint(d[(j + 2) % NPL]), __float_as_uint(d[(j + 3) % NPL]));
+                st_v4(static_cast<float*>(a.d_logits) + at + map.offset(j), w);
+            }
         }
     } else {
-        float* out = static_cast<float*>(a.d_logits) + at;
-        if (vec && NPL % 4 == 0) {
 #pragma unroll
-            for (int j = 0; j < NPL / 4; ++j)
-                st_v4(out + 4 * j, make_uint4(__float_as_uint(d[4 * j]), __float_as_uint(d[4 * j + 1]),
-                                              __float_as_uint(d[4 * j + 2]), __float_as_uint(d[4 * j + 3])));
-        } else {
-#pragma unroll
-            for (int j = 0; j < NPL; ++j)
-                if (j < r.n)
-                    out[j] = d[j];
+        for (int j = 0; j < NPL; ++j) {
+            if (!map.holds(j))
+                continue;
+            if (BF16)
+                static_cast<uint16_t*>(a.d_logits)[at + map.offset(j)] = static_cast<uint16_t>(pack_bf16x2(d[j], 0.0f));
+            else
+                static_cast<float*>(a.d_logits)[at + map.offset(j)] = d[j];
         }
     }
 }
 
 // ----------------------------------------------------------------- launches
-// Calls f<NPL, BF16>(vec) for the smallest NPL that holds a lane's run of
-// logits.  vec: every lane has NPL logits and every run starts on 16 bytes.
-template <typename F>
-cudaError_t with_row_shape(const ep_router_desc_t& r, int groups, const void* in, const void* out, F&& f)
+// <<<grid, block, smem, stream>>> as a programmatic dependent: the launch is
+// ready when the kernel before it ends, and every kernel here waits (pdl_wait)
+// before it reads what that one may have written.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                         Args... args)
 {
-    const int c = run_length(r.num_experts, groups);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Calls f<NPL, BF16>(vec) for the smallest NPL that holds a lane's logits; vec:
+// by 16-byte loads, where E is a multiple of that many logits and both arrays
+// start on 16 bytes.
+template <typename F>
+cudaError_t with_row_shape(const ep_router_desc_t& r, const void* in, const void* out, F&& f)
+{
     const bool bf16 = r.logits_dtype == EP_BF16;
-    const int size = bf16 ? 2 : 4;
-    const bool vec = r.num_experts == 32 * c && (c * size) % 16 == 0 &&
-                     ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+    const int full = bf16 ? 8 : 4;
+    const bool fits = ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+    int need = (r.num_experts + 31) / 32;
+    bool vec = fits && r.num_experts % full == 0;
+    if (r.num_groups > 1) { // runs of c, each of whole vectors
+        need = groups_run(r);
+        vec = vec && need >= full && (need & (need - 1)) == 0 && r.num_experts == 32 * need;
+    } else if (vec) {
+        need = (r.num_experts / full + 31) / 32 * full;
+    }
 #define EP_ROW_SHAPE(N)                                                                                               \
-    if (c <= N)                                                                                                       \
-        return bf16 ? f(std::integral_constant<int, N>{}, std::true_type{}, vec && c == N)                            \
-                    : f(std::integral_constant<int, N>{}, std::false_type{}, vec && c == N)
+    if (need <= N)                                                                                                    \
+        return bf16 ? f(std::integral_constant<int, N>{}, std::true_type{}, vec)                                      \
+                    : f(std::integral_constant<int, N>{}, std::false_type{}, vec)
     EP_ROW_SHAPE(1);
     EP_ROW_SHAPE(2);
     EP_ROW_SHAPE(4);
@@ -887,47 +1105,57 @@ cudaError_t launch_router_topk(const RouterTopkLaunch& a, cudaStream_t stream)
 {
     if (a.r.num_tokens == 0)
         return cudaSuccess;
-    return with_row_shape(a.r, a.r.num_groups, a.logits, nullptr, [&](auto npl, auto bf16, bool vec) {
-        const bool wide = a.bias != nullptr || a.r.num_groups > 1;
-        const size_t smem = wide ? sizeof(double) * kTopkWarps * a.r.num_experts : 0;
+    return with_row_shape(a.r, a.logits, nullptr, [&](auto npl, auto bf16, bool vec) {
+        const bool grouped = a.r.num_groups > 1;
+        const size_t smem = grouped || a.bias != nullptr ? sizeof(double) * kTopkWarps * a.r.num_experts : 0;
         const unsigned grid = (a.r.num_tokens + kTopkWarps - 1) / kTopkWarps;
-        router_topk_kernel<npl(), bf16()><<<grid, kTopkWarps * 32, smem, stream>>>(a, vec);
-        return cudaGetLastError();
+        return launch_after(grouped ? router_topk_kernel<npl(), bf16(), true> : router_topk_kernel<npl(), bf16(), false>,
+                            grid, kTopkWarps * 32, smem, stream, a, vec);
     });
 }
 
 size_t balance_workspace_bytes(int64_t T, int64_t E, int64_t S)
 {
-    const size_t bytes = static_cast<size_t>(balance_items(T, S)) * (8 * E + 8);
+    const size_t bytes = static_cast<size_t>(most_chunks(T, S)) * (8 * E + 8);
     return (bytes + 255) / 256 * 256;
 }
 
 cudaError_t launch_balance_loss(const BalanceLaunch& a, cudaStream_t stream)
 {
-    cudaError_t e = cudaSuccess;
-    if (a.r.num_tokens > 0) {
-        e = with_row_shape(a.r, 1, a.logits, nullptr, [&](auto npl, auto bf16, bool vec) {
-            const size_t smem = sizeof(float) * (kBalanceWarps + 1) * a.r.num_experts;
-            const unsigned grid = static_cast<unsigned>(balance_items(a.r.num_tokens, a.num_seqs));
-            balance_chunk_kernel<npl(), bf16()><<<grid, kBalanceWarps * 32, smem, stream>>>(a, vec);
-            return cudaGetLastError();
-        });
-    }
-    if (e != cudaSuccess)
-        return e;
-    balance_finish_kernel<<<a.num_seqs, kFinishThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    ep_router_desc_t r = a.r;
+    r.num_groups = 1; // the groups are the choice's alone
+    return with_row_shape(r, a.logits, nullptr, [&](auto npl, auto bf16, bool vec) {
+        const auto kernel = balance_kernel<npl(), bf16()>;
+        const size_t smem = sizeof(float) * 2 * kBalanceWarps * a.r.num_experts;
+        if (smem > 48 * 1024) {
+            cudaError_t e =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(balance_finish_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+            if (e != cudaSuccess)
+                return e;
+        }
+        const int T = a.r.num_tokens, chunk = chunk_tokens(std::max(T, 1));
+        const unsigned grid = static_cast<unsigned>(most_chunks(T, a.num_seqs));
+        const cudaError_t e = launch_after(kernel, grid, kBalanceThreads, smem, stream, a, chunk, vec);
+        if (e != cudaSuccess || T <= chunk) // no sequence has a second chunk
+            return e;
+        return launch_after(balance_finish_kernel, static_cast<unsigned>(a.num_seqs), kBalanceThreads, smem, stream, a,
+                            chunk);
+    });
 }
 
 cudaError_t launch_router_backward(const RouterBackwardLaunch& a, cudaStream_t stream)
 {
     if (a.r.num_tokens == 0)
         return cudaSuccess;
-    return with_row_shape(a.r, 1, a.logits, a.d_logits, [&](auto npl, auto bf16, bool vec) {
+    ep_router_desc_t r = a.r;
+    r.num_groups = 1;
+    return with_row_shape(r, a.logits, a.d_logits, [&](auto npl, auto bf16, bool vec) {
         const size_t smem = sizeof(float) * kBackwardWarps * a.r.num_experts;
         const unsigned grid = (a.r.num_tokens + kBackwardWarps - 1) / kBackwardWarps;
-        router_backward_kernel<npl(), bf16()><<<grid, kBackwardWarps * 32, smem, stream>>>(a, vec);
-        return cudaGetLastError();
+        return launch_after(router_backward_kernel<npl(), bf16()>, grid, kBackwardWarps * 32, smem, stream, a, vec);
     });
 }
 
