@@ -1120,12 +1120,12 @@ ep_status_t ep_lora(const void* x, const void* base, const ep_routing_desc_t* ro
         return EP_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const ep::LoraRows rows = lora_rows(routing, layout, mode, max_tokens_per_expert, num_rows, row_token);
-    ep::LoraShrinkLaunch down{rows, x, lora->a, lora->scales, lora->hidden_in, lora->rank, 0, h};
+    ep::LoraShrinkLaunch down{rows, x, lora->a, lora->scales, lora->hidden_in, lora->rank, 0, h, 1};
     const cudaError_t e = ep::launch_lora_shrink(down, s);
     if (e != cudaSuccess)
         return EP_ERR_CUDA;
     ep::LoraExpandLaunch up{rows, h, lora->b, base, out, lora->hidden_out, lora->rank, 0,
-                            row_token != nullptr && out != base ? layout->slot : nullptr};
+                            row_token != nullptr && out != base ? layout->slot : nullptr, rows.pairs > 0 ? 1 : 0};
     return from_cuda(ep::launch_lora_expand(up, s));
 }
 
@@ -1149,16 +1149,19 @@ ep_status_t ep_lora_backward(const void* dy, const void* x, const float* h, cons
         return EP_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const ep::LoraRows rows = lora_rows(routing, layout, mode, max_tokens_per_expert, num_rows, row_token);
-    ep::LoraShrinkLaunch down{rows, dy, lora->b, lora->scales, lora->hidden_out, lora->rank, 1, dh};
+    ep::LoraShrinkLaunch down{rows, dy, lora->b, lora->scales, lora->hidden_out, lora->rank, 1, dh,
+                              da != nullptr || dx != nullptr ? 1 : 0};
     cudaError_t e = ep::launch_lora_shrink(down, s);
+    if (e == cudaSuccess && da != nullptr) { // before dx: dy, just read, may still be in L2
+        ep::LoraOuterLaunch o{rows, x, dh, da, dy, h, db, lora->hidden_in, lora->hidden_out, lora->rank,
+                              dx != nullptr ? 1 : 0};
+        e = ep::launch_lora_outer(o, s);
+    }
     if (e == cudaSuccess && dx != nullptr) {
         ep::LoraExpandLaunch up{rows, dh, lora->a, dx_base, dx, lora->hidden_in, lora->rank, 1,
-                                row_token != nullptr && dx != dx_base ? layout->slot : nullptr};
+                                row_token != nullptr && dx != dx_base ? layout->slot : nullptr,
+                                rows.pairs == 0 ? 0 : (da != nullptr ? 2 : 1)};
         e = ep::launch_lora_expand(up, s);
-    }
-    if (e == cudaSuccess && da != nullptr) {
-        ep::LoraOuterLaunch o{rows, x, dh, da, dy, h, db, lora->hidden_in, lora->hidden_out, lora->rank};
-        e = ep::launch_lora_outer(o, s);
     }
     return from_cuda(e);
 }

@@ -66,6 +66,11 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
                  : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity)
 {
     uint32_t done;
@@ -79,20 +84,23 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity)
     return done != 0u;
 }
 
-// Wait for phase `parity` of `bar` to complete, for at most kWaitLimitNs.
+// Wait for phase `parity` of `bar` to complete, for at most kWaitLimitNs from
+// the 256th look on (most waits end before, and never read the timer).
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint32_t* err)
 {
-    if (mbar_try_wait(bar, parity))
-        return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if ((i & 63u) == 0u && global_timer_ns() - t0 > kWaitLimitNs) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 255u) != 0u)
+            continue;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0)
+            t0 = now;
+        if (now - t0 > kWaitLimitNs) {
             flag_error(err, EP_DEVERR_TIMEOUT);
             return false;
         }
     }
+    return true;
 }
 
 // ------------------------------------------------------ bulk (TMA) copies
@@ -248,6 +256,21 @@ __device__ __forceinline__ uint32_t pack_e2m1x2(float lo, float hi)
 __device__ __forceinline__ void sts_v2(void* p, uint2 v)
 {
     asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(smem_addr(p)), "r"(v.x), "r"(v.y) : "memory");
+}
+
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void st_u32(void* p, uint32_t v)

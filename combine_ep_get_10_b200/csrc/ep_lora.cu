@@ -17,6 +17,7 @@
 #include "ep_lora_launch.h"
 #include "ep_mma.cuh"
 #include "ep_tcgen05.cuh"
+#include "ep_tma.cuh"
 
 namespace ep {
 
@@ -24,7 +25,7 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kRowTile = 64;
+constexpr int kRowTile = 64; // rows without an adapter that a CTA copies
 
 // ------------------------------------------------------------------- rows
 struct RowRange {
@@ -47,8 +48,9 @@ __device__ __forceinline__ RowRange group_rows(const LoraRows& g, int e)
     return {static_cast<int>(b), static_cast<int>(b + n)};
 }
 
-// Tiles of kRowTile rows are numbered adapter after adapter: the adapter and rows of
+// Tiles of TILE rows are numbered adapter after adapter: the adapter and rows of
 // tile i; false when there are fewer.  One warp; all lanes get the answer.
+template <int TILE>
 __device__ __forceinline__ bool find_tile(const LoraRows& g, int i, int lane, int& e, RowRange& rows)
 {
     const int per = (g.E + 31) / 32; // adapters a lane, consecutive
@@ -57,7 +59,7 @@ __device__ __forceinline__ bool find_tile(const LoraRows& g, int i, int lane, in
 #pragma unroll 8
     for (int j = e0; j < e1; ++j) {
         const RowRange r = group_rows(g, j);
-        n += (r.end - r.begin + kRowTile - 1) / kRowTile;
+        n += (r.end - r.begin + TILE - 1) / TILE;
     }
     int inc = n;
 #pragma unroll
@@ -75,11 +77,11 @@ __device__ __forceinline__ bool find_tile(const LoraRows& g, int i, int lane, in
         int left = i - (inc - n);
         for (int j = e0; j < e1; ++j) {
             const RowRange r = group_rows(g, j);
-            const int tiles = (r.end - r.begin + kRowTile - 1) / kRowTile;
+            const int tiles = (r.end - r.begin + TILE - 1) / TILE;
             if (left < tiles) {
                 found = j;
-                b = r.begin + left * kRowTile;
-                end = min(r.end, b + kRowTile);
+                b = r.begin + left * TILE;
+                end = min(r.end, b + TILE);
                 break;
             }
             left -= tiles;
@@ -106,160 +108,217 @@ __device__ __forceinline__ void report_overflow(const LoraRows& g, int lane)
         flag_error(g.err, EP_DEVERR_OVERFLOW);
 }
 
-// Most tiles that the rows can make: a full one for every kRowTile rows and a part
-// one for every adapter in use.
-int most_tiles(const LoraRows& g)
+// A call without row buffer: what there is to say about its rows.
+__global__ void overflow_kernel(LoraRows g)
 {
-    const int rows = std::min(g.pairs, g.num_rows);
-    return rows / kRowTile + std::min(g.E, rows);
+    pdl_wait();
+    report_overflow(g, threadIdx.x & 31);
 }
 
-// Where the data of `row` is: its row index in x, base or out; -1 when the
-// row is past the group's end or its token is out of range.
-__device__ __forceinline__ int row_at(const LoraRows& g, int row, int end)
+// Most tiles that the rows can make: a full one for every `tile` rows and a part
+// one for every adapter in use.
+int most_tiles(const LoraRows& g, int tile)
+{
+    const int rows = std::min(g.pairs, g.num_rows);
+    return rows / tile + std::min(g.E, rows);
+}
+
+// Where the data of `row` is, in two steps so that the table's entry can be on
+// its way while other work is done: the entry (-1 past the group's end), and the
+// row index in x, base or out (-1 for an entry that is none).
+__device__ __forceinline__ int row_entry(const LoraRows& g, int row, int end)
 {
     if (row >= end)
         return -1;
-    if (g.row_token == nullptr)
-        return row;
-    const int t = __ldg(g.row_token + row);
-    if (t < 0 || t >= g.T) {
+    return g.row_token == nullptr ? row : __ldg(g.row_token + row);
+}
+
+__device__ __forceinline__ int row_index(const LoraRows& g, int entry, int row, int end)
+{
+    if (row >= end || g.row_token == nullptr)
+        return entry;
+    if (entry < 0 || entry >= g.T) {
         flag_error(g.err, EP_DEVERR_BAD_INDEX);
         return -1;
     }
-    return t;
+    return entry;
+}
+
+__device__ __forceinline__ int row_at(const LoraRows& g, int row, int end)
+{
+    return row_index(g, row_entry(g, row, end), row, end);
 }
 
 // ------------------------------------------------------------------ shrink
-constexpr int kShrinkThreads = 128; // four warps, 16 rows each
-constexpr int kDepth = 64;          // hidden channels a stage
+constexpr int kShrinkThreads = 160; // four warps that load x and store, one that loads w and multiplies
+constexpr int kShrinkTile = 64; // rows
+constexpr int kDepth = 64;      // hidden channels a stage
 
 template <int RP>
 struct ShrinkShape {
-    static constexpr int kStages = RP <= 64 ? 4 : 3;
-    static constexpr int kXBytes = kRowTile * kDepth * 2;
+    static constexpr int kStages = RP <= 32 ? 8 : (RP == 64 ? 6 : 4); // 96 KB: two CTAs an SM
+    static constexpr int kXBytes = kShrinkTile * kDepth * 2;
     static constexpr int kWBytes = RP * kDepth * 2;
     static constexpr int kStageBytes = kXBytes + kWBytes;
     static constexpr int kPitch = RP + 4; // floats a row of the partial sums
-    static constexpr int kSumBytes = kRowTile * kPitch * 4;
-    static constexpr int kBytes = kStages * kStageBytes > kSumBytes ? kStages * kStageBytes : kSumBytes;
+    static constexpr int kSumBytes = kShrinkTile * kPitch * 4;
+    // tiles start on 1024 bytes; a product reads 128 rows from a stage's first on
+    static constexpr int kBytes = (kStages - 1) * kStageBytes + 128 * kDepth * 2 + kWBytes + 1024;
+    static_assert(kSumBytes <= kStages * kStageBytes, "the sums take the stages' place");
+    static constexpr int kCols = RP < 32 ? 32 : RP; // tensor memory
+    static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
+    static constexpr int kWBox = RP < 64 ? RP : 64; // ranks a box of w [K, rank]
 };
 
 // A cluster has one tile of rows; its CTAs split the hidden width, and each
 // adds up its share of the tile's rows over the cluster, in CTA order (the
-// same sum every time, no atomics, no partial sums in HBM).
+// same sum every time, no atomics, no partial sums in HBM).  Four warps copy
+// the rows of x from where they are, one thread brings the factor's slice and
+// multiplies from shared memory into tensor memory: what is in flight is
+// bounded by the stages alone.  The product has 128 rows: what lies behind a
+// stage's 64 gives sums that nobody reads.
 template <int RP, bool TRANS>
-__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(LoraShrinkLaunch a)
+__global__ void __launch_bounds__(kShrinkThreads)
+    lora_shrink_kernel(const __grid_constant__ CUtensorMap w_map, LoraShrinkLaunch a)
 {
     using S = ShrinkShape<RP>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t s_full[S::kStages], s_free[S::kStages], s_done;
+    __shared__ uint32_t s_tmem;
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = static_cast<int>(cluster.num_blocks()), part = static_cast<int>(cluster.block_rank());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t base = smem_addr(smem);
+    if (tid == 0) {
+        prefetch_map(&w_map);
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&s_full[i], 129);
+            mbar_init(&s_free[i], 1);
+        }
+        mbar_init(&s_done, 1);
+        fence_mbar_init();
+    }
+    pdl_wait();
+    if (a.trigger_dependents != 0)
+        pdl_launch_dependents();
     if (blockIdx.x == 0 && warp == 0)
         report_overflow(a.rows, lane);
     int e;
     RowRange rows;
-    if (!find_tile(a.rows, blockIdx.x / parts, lane, e, rows))
+    if (!find_tile<kShrinkTile>(a.rows, blockIdx.x / parts, lane, e, rows))
         return; // the whole cluster has the same tile
+    const int live = rows.end - rows.begin;
     const int steps = (a.K + kDepth - 1) / kDepth;
-    const int per = (steps + parts - 1) / parts;
-    const int s0 = min(part * per, steps), n = min(per, steps - s0);
-    const uint32_t base = smem_addr(smem);
+    const int n = (steps - part + parts - 1) / parts; // steps part, part + parts, ..: the cluster reads along the rows
+    if (warp == 4)
+        tmem_alloc(&s_tmem, S::kCols);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = s_tmem;
 
-    // this thread's copies: chunk tid % 8 of rows tid / 8 + 16 i of x
-    const uint16_t* x_row[4];
-    bool x_on[4];
+    if (warp < 4) {
+        // chunk tid % 8 of rows tid / 8 + 16 i; rows past the group's end are
+        // left out (what their rows of the product hold is not used)
+        const int c = tid % 8;
+        const uint16_t* x_row[4];
+        uint32_t on = 0u, none = 0u; // rows with data; rows that count as zeros
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = row_at(a.rows, rows.begin + tid / 8 + 16 * i, rows.end);
-        x_on[i] = at >= 0;
-        x_row[i] = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(max(at, 0)) * a.K;
-    }
-    const uint16_t* w = static_cast<const uint16_t*>(a.w) + static_cast<int64_t>(e) * a.rank * a.K;
-
-    const auto load = [&](int step, int stage) {
-        const uint32_t xs = base + stage * S::kStageBytes, ws = xs + S::kXBytes;
-        const int k0 = step * kDepth;
-        const int c = tid % 8, k = k0 + c * 8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            cp_async16(xs + swizzled<8>(tid / 8 + 16 * i, c), x_row[i] + (k < a.K ? k : 0),
-                       x_on[i] && k < a.K ? 16 : 0);
-        if (!TRANS) {
-#pragma unroll
-            for (int j = tid / 8; j < RP; j += 16) {
-                const bool on = j < a.rank && k < a.K;
-                cp_async16(ws + swizzled<8>(j, c), on ? w + static_cast<int64_t>(j) * a.K + k : w, on ? 16 : 0);
-            }
-        } else {
-            constexpr int PC = RP / 8;
-#pragma unroll
-            for (int i = tid; i < kDepth * PC; i += kShrinkThreads) {
-                const int row = i / PC, cc = i % PC;
-                const bool on = cc * 8 < a.rank && k0 + row < a.K;
-                cp_async16(ws + swizzled<PC>(row, cc), on ? w + static_cast<int64_t>(k0 + row) * a.rank + cc * 8 : w,
-                           on ? 16 : 0);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int row = rows.begin + tid / 8 + 16 * i;
+            const int at = row_at(a.rows, row, rows.end);
+            on |= (at >= 0 ? 1u : 0u) << i;
+            none |= (at < 0 && row < rows.end ? 1u : 0u) << i;
+            x_row[i] = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(max(at, 0)) * a.K + c * 8;
         }
-    };
-
-    float acc[RP / 8][4];
+        bool alive = true;
+        for (int i = 0; i < n; ++i) {
+            const int stage = i % S::kStages, k = (part + i * parts) * kDepth;
+            if (i >= S::kStages && alive)
+                alive = mbar_wait_bounded(&s_free[stage], (i / S::kStages - 1) & 1, a.rows.err);
+            const uint32_t xs = base + stage * S::kStageBytes;
+            const bool in = k + c * 8 < a.K;
 #pragma unroll
-    for (int j = 0; j < RP / 8; ++j)
+            for (int j = 0; j < 4; ++j)
+                if (((on | none) >> j & 1u) != 0u)
+                    cp_async16(xs + swizzled<8>(tid / 8 + 16 * j, c), in ? x_row[j] + k : a.x,
+                               in && (on >> j & 1u) != 0u ? 16 : 0);
+            cp_async_arrive(&s_full[stage]);
+        }
+        cp_async_wait_all();
+    } else if (lane == 0) {
+        constexpr uint32_t desc = product_desc(128, RP, false, TRANS);
+        const auto load_w = [&](int i) {
+            uint64_t* full = &s_full[i % S::kStages];
+            const uint32_t ws = base + i % S::kStages * S::kStageBytes + S::kXBytes;
+            const int k0 = (part + i * parts) * kDepth;
+            mbar_arrive_expect_tx(full, S::kWBytes);
+            if (!TRANS) {
+                tma_load3(ws, &w_map, k0, 0, e, full);
+            } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            acc[j][i] = 0.0f;
-    const bool busy = rows.begin + warp * 16 < rows.end; // this warp has rows
-
+                for (int j = 0; j < RP; j += S::kWBox)
+                    tma_load3(ws + j * kDepth * 2, &w_map, j, k0, e, full);
+            }
+        };
+        for (int i = 0; i < min(n, S::kStages); ++i)
+            load_w(i);
+        for (int i = 0; i < n; ++i) {
+            const int stage = i % S::kStages;
+            if (!mbar_wait_bounded(&s_full[stage], (i / S::kStages) & 1, a.rows.err))
+                break;
+            fence_proxy_async_shared(); // the copies were the other threads'
+            tc_fence_after_sync();
+            const uint32_t xs = base + stage * S::kStageBytes, ws = xs + S::kXBytes;
 #pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) {
-        if (i < n)
-            load(s0 + i, i);
-        cp_async_commit();
-    }
-    for (int i = 0; i < n; ++i) {
-        cp_async_wait<S::kStages - 2>();
-        __syncthreads();
-        if (i + S::kStages - 1 < n)
-            load(s0 + i + S::kStages - 1, (i + S::kStages - 1) % S::kStages);
-        cp_async_commit();
-        if (!busy)
-            continue;
-        const uint32_t xs = base + (i % S::kStages) * S::kStageBytes, ws = xs + S::kXBytes;
-#pragma unroll
-        for (int kk = 0; kk < kDepth / 16; ++kk) {
-            uint32_t x4[4];
-            ldmatrix4(x4, xs + swizzled<8>(warp * 16 + (lane & 15), kk * 2 + (lane >> 4)));
-#pragma unroll
-            for (int j = 0; j < RP / 16; ++j) {
-                uint32_t b[4];
-                if (!TRANS)
-                    ldmatrix4(b, ws + swizzled<8>(j * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
-                else
-                    ldmatrix4_trans(b, ws + swizzled<RP / 8>(kk * 16 + (lane & 7) + (((lane >> 3) & 1) << 3),
-                                                             j * 2 + (lane >> 4)));
-                mma16816(acc[2 * j], x4, b[0], b[1]);
-                mma16816(acc[2 * j + 1], x4, b[2], b[3]);
+            for (int kk = 0; kk < kDepth / 16; ++kk) {
+                const uint64_t xd = operand_desc(xs + kk * 32, Swizzle::k128, 0, 1024);
+                const uint64_t wd = TRANS ? operand_desc(ws + kk * 2 * S::kWBox * 16, S::kSwizzle, kDepth * S::kWBox * 2,
+                                                         S::kWBox * 16)
+                                          : operand_desc(ws + kk * 32, Swizzle::k128, 0, 1024);
+                tc_product(tmem, xd, wd, desc, i > 0 || kk > 0);
+            }
+            tc_commit(i == n - 1 ? &s_done : &s_free[stage]);
+            // the stage before this one is (nearly) free: its next slice
+            if (i >= 1 && i - 1 + S::kStages < n) {
+                if (!mbar_wait_bounded(&s_free[(i - 1) % S::kStages], ((i - 1) / S::kStages) & 1, a.rows.err))
+                    break;
+                load_w(i - 1 + S::kStages);
             }
         }
     }
-    cp_async_wait<0>();
+    __syncwarp();
+    if (n > 0)
+        mbar_wait_bounded(&s_done, 0, a.rows.err);
+    tc_fence_after_sync();
     __syncthreads();
 
     // the tile's partial sums to shared memory, then the cluster's sums of them
     float* sums = reinterpret_cast<float*>(smem);
-    const int g = lane >> 2, q = lane & 3;
+    if (warp < 2) {
 #pragma unroll
-    for (int j = 0; j < RP / 8; ++j) {
-        float* p = sums + (warp * 16 + g) * S::kPitch + j * 8 + 2 * q;
-        *reinterpret_cast<float2*>(p) = make_float2(acc[j][0], acc[j][1]);
-        *reinterpret_cast<float2*>(p + 8 * S::kPitch) = make_float2(acc[j][2], acc[j][3]);
+        for (int j = 0; j < RP; j += 16) {
+            float d[16];
+            if (n > 0) {
+                tmem_load16(d, tmem + (static_cast<uint32_t>(warp * 32) << 16) + j);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    d[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(sums + tid * S::kPitch + j + i) =
+                    make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+        }
+        tc_fence_before_sync();
     }
     cluster.sync();
+    if (warp == 4)
+        tmem_free(tmem, S::kCols);
     const float scale = a.scales != nullptr ? __ldg(a.scales + e) : 1.0f;
     const int vecs = a.rank / 4;
-    const int live = rows.end - rows.begin;
     for (int i = part * kShrinkThreads + tid; i < live * vecs; i += parts * kShrinkThreads) {
         const int row = i / vecs, v = i - row * vecs;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -277,358 +336,528 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(LoraShrinkL
 }
 
 // ------------------------------------------------------------------ expand
-constexpr int kExpandThreads = 256; // warps: 4 of 16 rows x 2 of 128 columns
-constexpr int kColTile = 256;
+constexpr int kExpandThreads = 256; // (a ninth warp would leave 96 registers a thread, which spill)
+constexpr int kExpandTile = 128;    // rows: the product's M
+constexpr int kExpandCols = 128;    // columns a step: the product's N
+#ifndef EP_EXPAND_CTAS
+#define EP_EXPAND_CTAS 2
+#endif
 
-// Word i of lane q of each quad <-> word q of lane i.
-__device__ __forceinline__ void transpose_quad(uint32_t (&w)[4], int q)
-{
-    const bool up2 = (q & 2) != 0, up1 = (q & 1) != 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t r = __shfl_xor_sync(kFullMask, up2 ? w[i] : w[i + 2], 2);
-        if (up2)
-            w[i] = r;
-        else
-            w[i + 2] = r;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-        const uint32_t r = __shfl_xor_sync(kFullMask, up1 ? w[i] : w[i + 1], 1);
-        if (up1)
-            w[i] = r;
-        else
-            w[i + 1] = r;
-    }
-}
+template <int RP>
+struct ExpandShape {
+    static constexpr int kTermBytes = kExpandTile * RP * 2; // one bf16 tile of u
+    static constexpr int kWBytes = kExpandCols * RP * 2;
+    static constexpr int kWStages = RP == 16 ? 6 : 2;
+    static constexpr int kPitch = 144;                      // bytes a row of a warp's tile of base: 32 x 64 columns
+    static constexpr int kTileBytes = 8 * 32 * kPitch;
+    static constexpr int kTilesAt = 2 * kTermBytes + kWStages * kWBytes;
+    static constexpr int kBytes = kTilesAt + 2 * kTileBytes + 1024; // operands start on 1024 bytes
+    static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
+    static constexpr int kBox = RP < 64 ? RP : 64; // ranks a row of u's tiles, and of a box of w [N, rank]
+};
 
 __device__ __forceinline__ uint32_t add_to_bf16x2(uint32_t base, float a, float b)
 {
     return pack_bf16x2(bf16_lo(base) + a, bf16_hi(base) + b);
 }
 
-// Each thread ends with 8 consecutive columns of a row (one 16-byte load and
-// store): for w [N, rank] the columns of w's tile are laid out in shared memory
-// in the order in which the product's fragments hand them out; for w [rank, N]
-// the quad's four lanes exchange words.
+// A CTA has one tile of rows and every parts-th column tile.  u stays in shared
+// memory as two bf16 tiles (hi, lo).  While one thread, another warp's each
+// time, has the factor's next column tile multiplied into one of two places in
+// tensor memory, eight warps take the other one (32 rows and 64 columns each):
+// a thread adds a row's sums to base in shared memory, then the warp stores its
+// rows from there, four lanes 32 columns, and asks for base's tile after next.
 template <int RP, bool TRANS>
-__global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1) lora_expand_kernel(LoraExpandLaunch a, int tiles,
-                                                                                         int col_tiles)
+__global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
+    lora_expand_kernel(const __grid_constant__ CUtensorMap w_map, LoraExpandLaunch a, int tiles, int parts)
 {
-    extern __shared__ __align__(128) uint8_t smem[];
+    using S = ExpandShape<RP>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t s_w[S::kWStages], s_free[S::kWStages], s_sums[2], s_taken[2];
+    __shared__ uint32_t s_tmem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int tile = blockIdx.x / col_tiles;
-    if (blockIdx.x >= static_cast<unsigned>(tiles) * col_tiles) { // tokens without an adapter: out = base
-        const int t0 = (blockIdx.x - tiles * col_tiles) * kRowTile;
-        for (int i = warp; i < kRowTile; i += kExpandThreads / 32) {
-            const int t = t0 + i;
-            if (t >= a.rows.T || __ldg(a.slot + t) >= 0)
-                continue;
-            const int64_t at = static_cast<int64_t>(t) * a.N;
+    if (a.after_u == 0)
+        pdl_wait();
+    const int tile = blockIdx.x / parts;
+    if (blockIdx.x >= static_cast<unsigned>(tiles) * parts) { // tokens without an adapter: out = base
+        const int t0 = (blockIdx.x - tiles * parts) * kRowTile;
+        const int mine = t0 + (lane & 7) * 8 + warp;
+        uint32_t todo =
+            __ballot_sync(kFullMask, lane < 8 && mine < a.rows.T && __ldg(a.slot + mine) < 0);
+        for (; todo != 0u; todo &= todo - 1u) {
+            const int64_t at = static_cast<int64_t>(t0 + (__ffs(todo) - 1) * 8 + warp) * a.N;
+#pragma unroll 4
             for (int c = lane * 8; c < a.N; c += 256) {
                 const uint4 v = a.base != nullptr ? ld_nc_v4(static_cast<const uint16_t*>(a.base) + at + c)
                                                   : make_uint4(0u, 0u, 0u, 0u);
                 st_v4(static_cast<uint16_t*>(a.out) + at + c, v);
             }
         }
+        pdl_wait();
         return;
+    }
+    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t us = smem_addr(smem), ws0 = us + 2 * S::kTermBytes;
+    if (tid == 0) {
+        prefetch_map(&w_map);
+        for (int i = 0; i < S::kWStages; ++i) {
+            mbar_init(&s_w[i], 1);
+            mbar_init(&s_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_sums[i], 1);
+            mbar_init(&s_taken[i], 8);
+        }
+        fence_mbar_init();
     }
     int e;
     RowRange rows;
-    if (!find_tile(a.rows, tile, lane, e, rows))
+    if (!find_tile<kExpandTile>(a.rows, tile, lane, e, rows)) {
+        pdl_wait();
         return;
-    const int n0 = (blockIdx.x - tile * col_tiles) * kColTile;
-    const uint32_t ws = smem_addr(smem);
-    const uint16_t* w = static_cast<const uint16_t*>(a.w) + static_cast<int64_t>(e) * a.rank * a.N;
-    constexpr int PC = RP / 8;
-    if (!TRANS) {
-#pragma unroll 4
-        for (int i = tid; i < kColTile * PC; i += kExpandThreads) {
-            const int col = i / PC, c = i % PC;
-            // column 8a + 2j + b of 32 at place 8j + 2a + b
-            const int place = (col & ~31) | ((col & 6) << 2) | ((col & 24) >> 2) | (col & 1);
-            const bool on = c * 8 < a.rank && n0 + col < a.N;
-            cp_async16(ws + swizzled<PC>(place, c), on ? w + static_cast<int64_t>(n0 + col) * a.rank + c * 8 : w,
-                       on ? 16 : 0);
-        }
-    } else {
-#pragma unroll 4
-        for (int i = tid; i < RP * (kColTile / 8); i += kExpandThreads) {
-            const int row = i / (kColTile / 8), c = i % (kColTile / 8);
-            const bool on = row < a.rank && n0 + c * 8 < a.N;
-            cp_async16(ws + swizzled<kColTile / 8>(row, c), on ? w + static_cast<int64_t>(row) * a.N + n0 + c * 8 : w,
-                       on ? 16 : 0);
-        }
     }
-    cp_async_commit();
+    const int steps = (a.N + kExpandCols - 1) / kExpandCols;
+    const int part = blockIdx.x - tile * parts;
+    const int n = (steps - part + parts - 1) / parts; // steps part, part + parts, ..
 
-    const int g = lane >> 2, q = lane & 3;
-    const int wm = warp & 3, wn = warp >> 2; // rows 16 wm.., columns 128 wn..
-    const int row0 = rows.begin + wm * 16 + g;
-    const int at0 = row_at(a.rows, row0, rows.end), at1 = row_at(a.rows, row0 + 8, rows.end);
-    const int64_t o0 = static_cast<int64_t>(max(at0, 0)) * a.N, o1 = static_cast<int64_t>(max(at1, 0)) * a.N;
-    // base, all of it at once: 4 x 32 columns of two rows
-    uint4 base[4][2];
+    const auto load_w = [&](int i) {
+        uint64_t* bar = &s_w[i % S::kWStages];
+        const uint32_t ws = ws0 + i % S::kWStages * S::kWBytes;
+        const int n0 = (part + i * parts) * kExpandCols;
+        mbar_arrive_expect_tx(bar, S::kWBytes);
+        if (!TRANS) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int col = n0 + wn * 128 + c * 32 + q * 8;
-        const bool on = a.base != nullptr && col < a.N;
-        const uint16_t* b = static_cast<const uint16_t*>(a.base);
-        base[c][0] = on && at0 >= 0 ? ld_nc_v4(b + o0 + col) : make_uint4(0u, 0u, 0u, 0u);
-        base[c][1] = on && at1 >= 0 ? ld_nc_v4(b + o1 + col) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    // u of this thread's rows, in two terms
-    uint32_t hi[RP / 16][4], lo[RP / 16][4];
-    const float* u0 = a.u + static_cast<int64_t>(row0) * a.rank;
-    const float* u1 = u0 + static_cast<int64_t>(8) * a.rank;
+            for (int j = 0; j < RP; j += S::kBox)
+                tma_load3(ws + j * kExpandCols * 2, &w_map, j, n0, e, bar);
+        } else {
 #pragma unroll
-    for (int ks = 0; ks < RP / 16; ++ks) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int j = ks * 16 + h * 8 + 2 * q;
-            const float2 zero = make_float2(0.0f, 0.0f);
-            const float2 v0 = at0 >= 0 && j < a.rank ? __ldcg(reinterpret_cast<const float2*>(u0 + j)) : zero;
-            const float2 v1 = at1 >= 0 && j < a.rank ? __ldcg(reinterpret_cast<const float2*>(u1 + j)) : zero;
-            split_bf16x2(v0.x, v0.y, hi[ks][2 * h], lo[ks][2 * h]);
-            split_bf16x2(v1.x, v1.y, hi[ks][2 * h + 1], lo[ks][2 * h + 1]);
+            for (int h = 0; h < kExpandCols / 64; ++h)
+                tma_load3(ws + h * RP * 128, &w_map, n0 + h * 64, 0, e, bar);
         }
-    }
-    cp_async_wait<0>();
-    __syncthreads();
-    if (rows.begin + wm * 16 >= rows.end)
-        return; // no rows in this warp
+    };
+    if (tid == 0)
+        for (int i = 0; i < min(n, S::kWStages); ++i)
+            load_w(i);
 
+    // warps 0 .. 7: rows 32 (warp % 4).., columns 64 (warp / 4)..; lane: rows
+    // lane / 4 + 8 r of them, 8 columns from 8 (lane % 4) on of each 32
+    const int q = warp & 3, ch = (warp >> 2) * 64;
+    const bool busy = rows.begin + 32 * q < rows.end;
+    int at[4];
+    const uint32_t mine = us + S::kTilesAt + warp * 32 * S::kPitch;
+    const uint32_t quad = mine + (lane / 4) * S::kPitch + (lane & 3) * 16; // + 8 kPitch r + 64 p
+    const auto load_base = [&](int i) {
+        const int col = (part + i * parts) * kExpandCols + ch + (lane & 3) * 8;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        float acc[4][4];
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[j][i] = 0.0f;
-        const int place = wn * 128 + c * 32;
-#pragma unroll
-        for (int ks = 0; ks < RP / 16; ++ks) {
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                uint32_t b[4];
-                if (!TRANS)
-                    ldmatrix4(b, ws + swizzled<PC>(place + j * 8 + (lane & 7) + ((lane >> 4) << 3),
-                                                   ks * 2 + ((lane >> 3) & 1)));
-                else
-                    ldmatrix4_trans(b, ws + swizzled<kColTile / 8>(ks * 16 + (lane & 7) + (((lane >> 3) & 1) << 3),
-                                                                   place / 8 + j + (lane >> 4)));
-                mma16816(acc[j], hi[ks], b[0], b[1]);
-                mma16816(acc[j + 1], hi[ks], b[2], b[3]);
-                mma16816(acc[j], lo[ks], b[0], b[1]);
-                mma16816(acc[j + 1], lo[ks], b[2], b[3]);
+            for (int r = 0; r < 4; ++r) {
+                const bool on = a.base != nullptr && at[r] >= 0 && col + p * 32 < a.N;
+                const uint16_t* from = static_cast<const uint16_t*>(a.base) + static_cast<int64_t>(at[r]) * a.N + col + p * 32;
+                if (at[r] >= 0)
+                    cp_async16(quad + (i & 1) * S::kTileBytes + r * 8 * S::kPitch + p * 64, on ? from : a.w, on ? 16 : 0);
             }
-        }
-        const int col = n0 + place + q * 8;
-        uint16_t* out = static_cast<uint16_t*>(a.out);
+    };
+    if (busy) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            uint32_t v[4] = {base[c][r].x, base[c][r].y, base[c][r].z, base[c][r].w};
-            if (TRANS)
-                transpose_quad(v, q);
+        for (int r = 0; r < 4; ++r)
+            at[r] = row_at(a.rows, rows.begin + 32 * q + lane / 4 + 8 * r, rows.end);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = add_to_bf16x2(v[j], acc[j][2 * r], acc[j][2 * r + 1]);
-            if (TRANS)
-                transpose_quad(v, q);
-            if ((r == 0 ? at0 : at1) >= 0 && col < a.N)
-                st_v4(out + (r == 0 ? o0 : o1) + col, make_uint4(v[0], v[1], v[2], v[3]));
+        for (int i = 0; i < 2; ++i) {
+            if (i < n)
+                load_base(i);
+            cp_async_commit();
         }
     }
+    if (a.after_u == 1)
+        pdl_wait();
+
+    // u in two terms; rows past the group's end give sums that nobody reads
+    const int live = rows.end - rows.begin;
+    {
+        const float* u = a.u + static_cast<int64_t>(rows.begin) * a.rank;
+#pragma unroll 4
+        for (int t = tid; t < live * (RP / 8); t += 256) {
+            const int row = t / (RP / 8), c = t % (RP / 8);
+            uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
+            if (c * 8 < a.rank) {
+                const float4* f = reinterpret_cast<const float4*>(u + static_cast<int64_t>(row) * a.rank + c * 8);
+                const float4 f0 = __ldcg(f), f1 = __ldcg(f + 1);
+                split_bf16x2(f0.x, f0.y, h.x, l.x);
+                split_bf16x2(f0.z, f0.w, h.y, l.y);
+                split_bf16x2(f1.x, f1.y, h.z, l.z);
+                split_bf16x2(f1.z, f1.w, h.w, l.w);
+            }
+            const uint32_t place = (c >> 3) * (kExpandTile * 128u) + swizzled<S::kBox / 8>(row, c & 7);
+            *reinterpret_cast<uint4*>(smem + place) = h;
+            *reinterpret_cast<uint4*>(smem + S::kTermBytes + place) = l;
+        }
+        fence_proxy_async_shared();
+    }
+    if (warp == 0)
+        tmem_alloc(&s_tmem, 2 * kExpandCols);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = s_tmem;
+
+    const auto multiply = [&](int i) {
+        constexpr uint32_t desc = product_desc(128, kExpandCols, false, TRANS);
+        constexpr uint32_t group = S::kBox * 16; // 8 rows of u's tiles
+        const int stage = i % S::kWStages;
+        bool ok = mbar_wait_bounded(&s_w[stage], (i / S::kWStages) & 1, a.rows.err);
+        if (i >= 2 && ok)
+            ok = mbar_wait_bounded(&s_taken[i & 1], (i / 2 - 1) & 1, a.rows.err);
+        if (!ok)
+            return false;
+        tc_fence_after_sync();
+        const uint32_t ws = ws0 + stage * S::kWBytes;
+#pragma unroll
+        for (int kk = 0; kk < RP / 16; ++kk) {
+            const uint32_t k_at = kk / 4 * kExpandTile * 128 + kk % 4 * 32;
+            const uint64_t hi = operand_desc(us + k_at, S::kSwizzle, 0, group);
+            const uint64_t lo = operand_desc(us + S::kTermBytes + k_at, S::kSwizzle, 0, group);
+            const uint64_t w = TRANS ? operand_desc(ws + kk * 2048, Swizzle::k128, RP * 128, 1024)
+                                     : operand_desc(ws + kk / 4 * kExpandCols * 128 + kk % 4 * 32, S::kSwizzle, 0, group);
+            tc_product(tmem + (i & 1) * kExpandCols, hi, w, desc, kk > 0);
+            tc_product(tmem + (i & 1) * kExpandCols, lo, w, desc, true);
+        }
+        tc_commit(&s_free[stage]);
+        tc_commit(&s_sums[i & 1]);
+        return true;
+    };
+    {
+        bool alive = true; // no wait has run out
+        if (tid == 0)
+            alive = multiply(0);
+        __syncwarp();
+        uint16_t* out = static_cast<uint16_t*>(a.out);
+        for (int i = 0; i < n; ++i) {
+            if (lane == 0 && warp == (i & 7) && alive) { // each warp in its turn
+                if (i >= 1 && i - 1 + S::kWStages < n) { // (before the product: with two stages it is the one it needs)
+                    alive = mbar_wait_bounded(&s_free[(i - 1) % S::kWStages], ((i - 1) / S::kWStages) & 1, a.rows.err);
+                    if (alive)
+                        load_w(i - 1 + S::kWStages);
+                }
+                if (i + 1 < n && alive)
+                    alive = multiply(i + 1);
+            }
+            __syncwarp();
+            if (alive)
+                alive = mbar_wait_bounded(&s_sums[i & 1], (i / 2) & 1, a.rows.err);
+            tc_fence_after_sync();
+            if (busy) {
+                const uint32_t from = tmem + (static_cast<uint32_t>(q * 32) << 16) + (i & 1) * kExpandCols + ch;
+                const uint32_t tile = (i & 1) * S::kTileBytes, row = mine + tile + lane * S::kPitch;
+                cp_async_wait<1>();
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < 64; h += 16) {
+                    float d[16];
+                    tmem_load16(d, from + h);
+                    uint4 v0 = lds_v4(row + h * 2), v1 = lds_v4(row + h * 2 + 16);
+                    v0 = make_uint4(add_to_bf16x2(v0.x, d[0], d[1]), add_to_bf16x2(v0.y, d[2], d[3]),
+                                    add_to_bf16x2(v0.z, d[4], d[5]), add_to_bf16x2(v0.w, d[6], d[7]));
+                    v1 = make_uint4(add_to_bf16x2(v1.x, d[8], d[9]), add_to_bf16x2(v1.y, d[10], d[11]),
+                                    add_to_bf16x2(v1.z, d[12], d[13]), add_to_bf16x2(v1.w, d[14], d[15]));
+                    sts_v4(row + h * 2, v0);
+                    sts_v4(row + h * 2 + 16, v1);
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                const int col = (part + i * parts) * kExpandCols + ch + (lane & 3) * 8;
+                uint4 v[2][4];
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        v[p][r] = lds_v4(quad + tile + r * 8 * S::kPitch + p * 64);
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (at[r] >= 0 && col + p * 32 < a.N)
+                            st_v4(out + static_cast<int64_t>(at[r]) * a.N + col + p * 32, v[p][r]);
+                __syncwarp();
+                if (i + 2 < n)
+                    load_base(i + 2);
+                cp_async_commit();
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&s_taken[i & 1]);
+        }
+    }
+    __syncthreads();
+    if (warp == 0)
+        tmem_free(tmem, 2 * kExpandCols);
+    if (a.after_u == 2)
+        pdl_wait(); // this grid ends after the one before it
 }
 
 // ------------------------------------------------------------------- outer
-// dW of one adapter and 128 columns of x or dy: the columns are the product's
-// rows (M), the rank its columns (N), and the sum runs over the adapter's rows,
-// 64 at a time.  Both operands are MN-major: the row data as it lies in HBM,
-// and u, which the threads write as two bf16 tiles (hi, lo).  Sums stay in
-// tensor memory until the last row.
-constexpr int kOuterThreads = 128;
-constexpr int kOuterCols = 128;
-constexpr int kOuterStages = 4;
-constexpr int kOuterAhead = kOuterStages - 2; // chunks in flight while one is multiplied
+#ifndef EP_OUTER_COLS
+#define EP_OUTER_COLS 128
+#endif
+#ifndef EP_OUTER_STAGE_KB
+#define EP_OUTER_STAGE_KB 100
+#endif
+constexpr int kOuterThreads = 288; // four warps that load, four that split u and store, one that multiplies
+constexpr int kOuterRows = 64;     // rows a stage
 
 template <int RP>
 struct OuterShape {
-    static constexpr int kVBytes = kRowTile * kOuterCols * 2;
-    static constexpr int kUBytes = kRowTile * RP * 2; // one term
-    static constexpr int kStageBytes = kVBytes + 2 * kUBytes;
-    static constexpr int kBytes = kOuterStages * kStageBytes + 1024; // tiles start on 1024 bytes
-    static constexpr int kCols = RP < 32 ? 32 : RP;                  // tensor memory
+    static constexpr int kCols = EP_OUTER_COLS;            // columns of x or dy: kCols / 128 products
+    static constexpr int kHalfBytes = kOuterRows * 128;    // 64 columns of x or dy, or of u's terms
+    static constexpr int kVBytes = kOuterRows * kCols * 2;
+    static constexpr int kUBytes = kOuterRows * RP * 4;    // u as it is in HBM, then its two terms
+    static constexpr int kTermBytes = kUBytes / 2;
+    static constexpr int kStageBytes = kVBytes + kUBytes;
+    static constexpr int kStages = EP_OUTER_STAGE_KB * 1024 / kStageBytes < 2 ? 2 : EP_OUTER_STAGE_KB * 1024 / kStageBytes;
+    static constexpr int kBytes = kStages * kStageBytes + 1024; // tiles start on 1024 bytes
+    static constexpr int kTmem = kCols / 128 * RP < 32 ? 32 : kCols / 128 * RP;
     static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
-    static constexpr int kUChunks = RP < 64 ? RP / 8 : 8; // 16-byte chunks a row of u's tile
+    static constexpr int kUChunks = RP < 64 ? RP / 8 : 8; // 16-byte chunks a row of u's terms
 };
 
 // Place of columns 8c.. of `row` in a tile of 128-byte rows, 64 columns each.
-__device__ __forceinline__ uint32_t halves(int row, int c)
+__device__ __forceinline__ uint32_t in_halves(int row, int c)
 {
-    return static_cast<uint32_t>(c >> 3) * (kRowTile * 128u) + swizzled<8>(row, c & 7);
+    return static_cast<uint32_t>(c >> 3) * (kOuterRows * 128u) + swizzled<8>(row, c & 7);
 }
 
+// The adapter that is i-th by rows, most first (E <= 32; else the i-th), so
+// that the CTAs that run longest start first.  One warp.
+__device__ __forceinline__ int by_rows(const LoraRows& g, int i, int lane)
+{
+    if (g.E > 32)
+        return i;
+    int n = -1;
+    if (lane < g.E) {
+        const RowRange r = group_rows(g, lane);
+        n = r.end - r.begin;
+    }
+    int before = 0;
+    for (int j = 0; j < g.E; ++j) {
+        const int o = __shfl_sync(kFullMask, n, j);
+        before += o > n || (o == n && j < lane) ? 1 : 0;
+    }
+    return __ffs(__ballot_sync(kFullMask, lane < g.E && before == i)) - 1;
+}
+
+// dW of one adapter and kCols columns of x or dy: the columns are the
+// products' rows (M = 128 each), the rank their columns (N), and the sum runs
+// over the adapter's rows, kOuterRows a stage.  Both operands are MN-major: the
+// row data as it lies in HBM, and u, copied as fp32 and turned in place into
+// two bf16 tiles (hi, lo).  Sums stay in tensor memory
+// until the last row.
 template <int RP>
-__global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(LoraOuterLaunch a, int in_tiles, int out_tiles)
+__global__ void __launch_bounds__(kOuterThreads)
+    lora_outer_kernel(LoraOuterLaunch a, int in_tiles, int out_tiles)
 {
     using S = OuterShape<RP>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t s_free[kOuterStages], s_done;
-    __shared__ uint32_t s_tmem;
-    __shared__ int s_at[2][kRowTile];
-    const int tid = threadIdx.x, warp = tid >> 5;
-    const int per = in_tiles + out_tiles;
-    const int e = blockIdx.x / per, i_tile = blockIdx.x - e * per;
-    const bool in = i_tile < in_tiles; // da, from x and dh; else db, from dy and h
-    const int N = in ? a.hidden_in : a.hidden_out;
-    const int n0 = (in ? i_tile : i_tile - in_tiles) * kOuterCols;
-    const uint16_t* v = static_cast<const uint16_t*>(in ? a.x : a.dy);
-    const float* u = in ? a.dh : a.h;
-    const RowRange rows = group_rows(a.rows, e);
-    const int n = (rows.end - rows.begin + kRowTile - 1) / kRowTile;
+    __shared__ uint64_t s_v[S::kStages], s_u[S::kStages], s_split[S::kStages], s_free[S::kStages], s_done;
+    __shared__ uint32_t s_tmem, s_on[2][2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = smem_addr(smem);
-
+    if (tid == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&s_v[i], 128);
+            mbar_init(&s_u[i], 1);
+            mbar_init(&s_split[i], 128);
+            mbar_init(&s_free[i], 1);
+        }
+        mbar_init(&s_done, 1);
+        fence_mbar_init();
+    }
+    const int per = in_tiles + out_tiles;
+    const int i_adapter = blockIdx.x / per, i_tile = blockIdx.x - i_adapter * per;
+    const bool in = i_tile >= out_tiles; // da, from x and dh; else db, from dy and h
+    const int N = in ? a.hidden_in : a.hidden_out;
+    const int n0 = (in ? i_tile - out_tiles : i_tile) * S::kCols;
+    const float* u = in ? a.dh : a.h;
+    const uint16_t* v = static_cast<const uint16_t*>(in ? a.x : a.dy);
+    pdl_wait();
+    if (a.trigger_dependents != 0)
+        pdl_launch_dependents(); // what comes next needs dh, which is there
+    const int e = by_rows(a.rows, i_adapter, lane);
+    const RowRange rows = group_rows(a.rows, e);
+    const int live = rows.end - rows.begin;
+    const int n = (live + kOuterRows - 1) / kOuterRows;
     uint32_t tmem = 0;
     if (n > 0) {
-        if (warp == 0)
-            tmem_alloc(&s_tmem, S::kCols);
-        if (tid == 0) {
-            for (int i = 0; i < kOuterStages; ++i)
-                mbar_init(&s_free[i], 1);
-            mbar_init(&s_done, 1);
-            fence_mbar_init();
-        }
-        // where the rows' data is: of chunk i in s_at[i % 2], of the one after in a register
-        const auto at_of = [&](int chunk) {
-            return tid < kRowTile ? row_at(a.rows, rows.begin + chunk * kRowTile + tid, rows.end) : -1;
-        };
-        if (tid < kRowTile)
-            s_at[0][tid] = at_of(0);
-        int next_at = at_of(1);
-        // u of the next chunk, in registers
-        constexpr int kVecs = RP / 16;
-        float4 un[kVecs][2];
-        const auto load_u = [&](int chunk) {
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const int t = tid + i * kOuterThreads, row = rows.begin + chunk * kRowTile + t / (RP / 8), c = t % (RP / 8);
-                un[i][0] = un[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (row < rows.end && c * 8 < a.rank) {
-                    const float4* p = reinterpret_cast<const float4*>(u + static_cast<int64_t>(row) * a.rank + c * 8);
-                    un[i][0] = __ldcg(p);
-                    un[i][1] = __ldcg(p + 1);
-                }
-            }
-        };
-        load_u(0);
+        if (warp == 8)
+            tmem_alloc(&s_tmem, S::kTmem);
         tc_fence_before_sync();
         __syncthreads();
         tc_fence_after_sync();
         tmem = s_tmem;
+    }
 
-        bool alive = true; // false once a wait has run out
-        for (int it = 0; it < n + kOuterAhead; ++it) {
-            if (it < n) {
-                const int stage = it % kOuterStages;
-                if (it >= kOuterStages && alive)
-                    alive = mbar_wait_bounded(&s_free[stage], (it / kOuterStages - 1) & 1, a.rows.err);
+    if (warp < 4) {
+        // chunk t % VC of rows t / VC + kStep j
+        constexpr int VC = S::kCols / 8, kStep = 128 / VC, kCopies = kOuterRows / kStep;
+        const int c = tid % VC, r0 = tid / VC;
+        const bool in_col = n0 + c * 8 < N;
+        int entry[kCopies]; // of the next stage's rows
+        const auto find = [&](int i) {
+#pragma unroll
+            for (int j = 0; j < kCopies; ++j)
+                entry[j] = row_entry(a.rows, rows.begin + i * kOuterRows + r0 + kStep * j, rows.end);
+        };
+        bool alive = true; // no wait has run out
+        if (n > 0)
+            find(0);
+        for (int i = 0; i < n; ++i) {
+            {
+                const int stage = i % S::kStages;
+                if (i >= S::kStages && alive)
+                    alive = mbar_wait_bounded(&s_free[stage], (i / S::kStages - 1) & 1, a.rows.err);
+                const int first = rows.begin + i * kOuterRows, here = min(kOuterRows, rows.end - first);
                 const uint32_t vs = base + stage * S::kStageBytes;
-                const int* at = s_at[it & 1];
-                const int c = tid % 16, col = n0 + c * 8;
-#pragma unroll
-                for (int i = 0; i < kRowTile / 8; ++i) {
-                    const int row = tid / 16 + 8 * i, r = at[row];
-                    const bool on = r >= 0 && col < N;
-                    cp_async16(vs + halves(row, c), on ? v + static_cast<int64_t>(r) * N + col : v, on ? 16 : 0);
+                if (tid == 0) {
+                    const uint32_t u_bytes = static_cast<uint32_t>(here) * a.rank * 4;
+                    mbar_arrive_expect_tx(&s_u[stage], u_bytes);
+                    bulk_load_g2s(smem + stage * S::kStageBytes + S::kVBytes, u + static_cast<int64_t>(first) * a.rank,
+                                  u_bytes, &s_u[stage]);
                 }
-                uint8_t* us = smem + stage * S::kStageBytes + S::kVBytes;
+                const int used = (here + 15) & ~15; // whole steps of the sum; rows past the end are zeros
 #pragma unroll
-                for (int i = 0; i < kVecs; ++i) {
-                    const int t = tid + i * kOuterThreads, row = t / (RP / 8), cu = t % (RP / 8);
-                    uint4 h4 = make_uint4(0u, 0u, 0u, 0u), l4 = h4;
-                    if (at[row] >= 0) {
-                        split_bf16x2(un[i][0].x, un[i][0].y, h4.x, l4.x);
-                        split_bf16x2(un[i][0].z, un[i][0].w, h4.y, l4.y);
-                        split_bf16x2(un[i][1].x, un[i][1].y, h4.z, l4.z);
-                        split_bf16x2(un[i][1].z, un[i][1].w, h4.w, l4.w);
-                    }
-                    const uint32_t place = RP < 64 ? swizzled<S::kUChunks>(row, cu) : halves(row, cu);
-                    *reinterpret_cast<uint4*>(us + place) = h4;
-                    *reinterpret_cast<uint4*>(us + S::kUBytes + place) = l4;
+                for (int j = 0; j < kCopies; ++j) {
+                    const int row = r0 + kStep * j, at = row_index(a.rows, entry[j], first + row, rows.end);
+                    const bool on = at >= 0 && in_col;
+                    if (row < used)
+                        cp_async16(vs + in_halves(row, c), on ? v + static_cast<int64_t>(at) * N + n0 + c * 8 : v,
+                                   on ? 16 : 0);
                 }
-                load_u(it + 1);
-                if (tid < kRowTile)
-                    s_at[(it + 1) & 1][tid] = next_at;
-                next_at = at_of(it + 2);
-            }
-            cp_async_commit();
-            const int j = it - kOuterAhead;
-            cp_async_wait<kOuterAhead>();
-            fence_proxy_async_shared();
-            __syncthreads();
-            if (j >= 0 && tid == 0) {
-                tc_fence_after_sync();
-                const uint32_t vs = base + (j % kOuterStages) * S::kStageBytes, us = vs + S::kVBytes;
-                constexpr uint32_t desc = product_desc(kOuterCols, RP, true, true);
-                constexpr uint32_t group = S::kUChunks * 128u; // 8 rows of u
-#pragma unroll
-                for (int kk = 0; kk < kRowTile / 16; ++kk) {
-                    const uint64_t va = operand_desc(vs + kk * 2048u, Swizzle::k128, kRowTile * 128u, 1024u);
-                    tc_product(tmem, va, operand_desc(us + kk * 2 * group, S::kSwizzle, kRowTile * 128u, group), desc,
-                               j > 0 || kk > 0);
-                    tc_product(tmem, va,
-                               operand_desc(us + S::kUBytes + kk * 2 * group, S::kSwizzle, kRowTile * 128u, group), desc,
-                               true);
-                }
-                tc_commit(j == n - 1 ? &s_done : &s_free[j % kOuterStages]);
+                cp_async_arrive(&s_v[stage]);
+                if (i + 1 < n)
+                    find(i + 1);
             }
         }
-        if (alive)
+        cp_async_wait_all();
+    } else if (warp == 8) {
+        if (lane == 0) {
+            constexpr uint32_t desc = product_desc(128, RP, true, true);
+            constexpr uint32_t group = S::kUChunks * 128u; // 8 rows of u's terms
+            for (int i = 0; i < n; ++i) {
+                const int stage = i % S::kStages;
+                const uint32_t parity = (i / S::kStages) & 1;
+                if (!mbar_wait_bounded(&s_v[stage], parity, a.rows.err) ||
+                    !mbar_wait_bounded(&s_split[stage], parity, a.rows.err))
+                    break;
+                fence_proxy_async_shared(); // the copies were the other threads'
+                tc_fence_after_sync();
+                const int steps = (min(kOuterRows, live - i * kOuterRows) + 15) / 16;
+                const uint32_t vs = base + stage * S::kStageBytes;
+                for (int kk = 0; kk < steps; ++kk) {
+                    const uint32_t us = vs + S::kVBytes + kk * 2 * group;
+                    const uint64_t hi = operand_desc(us, S::kSwizzle, S::kHalfBytes, group);
+                    const uint64_t lo = operand_desc(us + S::kTermBytes, S::kSwizzle, S::kHalfBytes, group);
+#pragma unroll
+                    for (int m = 0; m < S::kCols / 128; ++m) {
+                        const uint64_t v = operand_desc(vs + m * 2 * S::kHalfBytes + kk * 2048u, Swizzle::k128, S::kHalfBytes,
+                                                        1024u);
+                        tc_product(tmem + m * RP, v, hi, desc, i > 0 || kk > 0);
+                        tc_product(tmem + m * RP, v, lo, desc, true);
+                    }
+                }
+                tc_commit(i == n - 1 ? &s_done : &s_free[stage]);
+            }
+        }
+    } else {
+        constexpr int kVecs = RP / 8; // float4 a thread and stage
+        const int st = tid - 128;
+        // one thread a row: is it one of the group's, with data?
+        const auto find = [&](int i) {
+            return st < kOuterRows ? row_entry(a.rows, rows.begin + i * kOuterRows + st, rows.end) : -1;
+        };
+        int entry = n > 0 ? find(0) : -1;
+        bool alive = true; // no wait has run out
+        for (int i = 0; i < n; ++i) {
+            const int stage = i % S::kStages;
+            const uint32_t who = __ballot_sync(
+                kFullMask,
+                st < kOuterRows && row_index(a.rows, entry, rows.begin + i * kOuterRows + st, rows.end) >= 0);
+            if (warp < 6 && lane == 0)
+                s_on[i & 1][warp - 4] = who;
+            if (i + 1 < n)
+                entry = find(i + 1);
+            if (alive)
+                alive = mbar_wait_bounded(&s_u[stage], (i / S::kStages) & 1, a.rows.err);
+            uint8_t* us = smem + stage * S::kStageBytes + S::kVBytes;
+            float4 f[kVecs];
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int t = st + j * 128, row = t / (RP / 4), q = t % (RP / 4);
+                f[j] = q * 4 < a.rank ? *reinterpret_cast<const float4*>(us + (row * a.rank + q * 4) * 4)
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory"); // u is read (and s_on written) before its terms take its place
+            const uint2 rows_on = make_uint2(s_on[i & 1][0], s_on[i & 1][1]);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int t = st + j * 128, row = t / (RP / 4), q = t % (RP / 4);
+                uint2 h = make_uint2(0u, 0u), l = h;
+                if (((row < 32 ? rows_on.x : rows_on.y) >> (row & 31) & 1u) != 0u) {
+                    split_bf16x2(f[j].x, f[j].y, h.x, l.x);
+                    split_bf16x2(f[j].z, f[j].w, h.y, l.y);
+                }
+                const uint32_t place = (RP < 64 ? swizzled<S::kUChunks>(row, q / 2) : in_halves(row, q / 2)) + 8 * (q & 1);
+                *reinterpret_cast<uint2*>(us + place) = h;
+                *reinterpret_cast<uint2*>(us + S::kTermBytes + place) = l;
+            }
+            fence_proxy_async_shared();
+            mbar_arrive(&s_split[stage]);
+        }
+        if (n > 0)
             mbar_wait_bounded(&s_done, 0, a.rows.err);
         tc_fence_after_sync();
-    }
-
-    // thread: column n0 + tid, every rank
-    const int col = n0 + tid;
-    uint16_t* out = static_cast<uint16_t*>(in ? a.da : a.db) + static_cast<int64_t>(e) * a.rank * N;
+        // thread: column n0 + 128 m + st, every rank
+        uint16_t* out = static_cast<uint16_t*>(in ? a.da : a.db) + static_cast<int64_t>(e) * a.rank * N;
 #pragma unroll
-    for (int j0 = 0; j0 < RP; j0 += 16) {
-        if (j0 >= a.rank)
-            break;
-        float d[16];
-        if (n > 0) {
-            tmem_load16(d, tmem + (static_cast<uint32_t>(warp * 32) << 16) + j0);
-        } else {
+        for (int m = 0; m < S::kCols / 128; ++m) {
+            const int col = n0 + m * 128 + st;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                d[i] = 0.0f;
-        }
-        if (col < N) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (j0 + 8 * h >= a.rank)
+            for (int j0 = 0; j0 < RP; j0 += 16) {
+                if (j0 >= a.rank)
                     break;
-                if (in) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        out[static_cast<int64_t>(j0 + 8 * h + i) * N + col] =
-                            static_cast<uint16_t>(pack_bf16x2(d[8 * h + i], 0.0f));
+                float d[16];
+                if (n > 0) {
+                    tmem_load16(d, tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + m * RP + j0);
                 } else {
-                    st_v4(out + static_cast<int64_t>(col) * a.rank + j0 + 8 * h,
-                          make_uint4(pack_bf16x2(d[8 * h], d[8 * h + 1]), pack_bf16x2(d[8 * h + 2], d[8 * h + 3]),
-                                     pack_bf16x2(d[8 * h + 4], d[8 * h + 5]), pack_bf16x2(d[8 * h + 6], d[8 * h + 7])));
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        d[i] = 0.0f;
+                }
+                if (col < N) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (j0 + 8 * h >= a.rank)
+                            break;
+                        if (in) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                out[static_cast<int64_t>(j0 + 8 * h + i) * N + col] =
+                                    static_cast<uint16_t>(pack_bf16x2(d[8 * h + i], 0.0f));
+                        } else {
+                            st_v4(out + static_cast<int64_t>(col) * a.rank + j0 + 8 * h,
+                                  make_uint4(pack_bf16x2(d[8 * h], d[8 * h + 1]), pack_bf16x2(d[8 * h + 2], d[8 * h + 3]),
+                                             pack_bf16x2(d[8 * h + 4], d[8 * h + 5]),
+                                             pack_bf16x2(d[8 * h + 6], d[8 * h + 7])));
+                        }
+                    }
                 }
             }
         }
+        tc_fence_before_sync();
     }
     if (n > 0) {
-        tc_fence_before_sync();
         __syncthreads();
-        if (warp == 0)
-            tmem_free(tmem, S::kCols);
+        if (warp == 8)
+            tmem_free(tmem, S::kTmem);
     }
 }
 
@@ -672,12 +901,30 @@ cudaError_t with_rank(int rank, F&& f)
     return f(std::integral_constant<int, 128>{});
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes)
+// A launch as a programmatic dependent, in clusters of `cluster`: every kernel
+// here waits (pdl_wait) before it reads what the kernel before may have written.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(void (*kernel)(KArgs...), unsigned grid, unsigned block, int smem, int cluster,
+                         cudaStream_t stream, const Args&... args)
 {
-    if (bytes <= 48 * 1024)
-        return cudaSuccess;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 } // namespace
@@ -698,66 +945,57 @@ cudaError_t launch_lora_shrink(const LoraShrinkLaunch& a, cudaStream_t stream)
 {
     if (a.rows.pairs == 0)
         return cudaSuccess;
-    const int tiles = std::max(1, most_tiles(a.rows)); // one at least: it reports rows past the buffer
+    if (a.rows.num_rows == 0)
+        return launch_after(overflow_kernel, 1, 32, 0, 1, stream, a.rows);
+    const int tiles = most_tiles(a.rows, kShrinkTile);
     return with_rank(a.rank, [&](auto rp) {
         constexpr int RP = decltype(rp)::value;
-        const auto kernel = a.transposed ? lora_shrink_kernel<RP, true> : lora_shrink_kernel<RP, false>;
-        const int smem = ShrinkShape<RP>::kBytes;
-        cudaError_t e = allow_smem(kernel, smem);
-        if (e != cudaSuccess)
-            return e;
+        using S = ShrinkShape<RP>;
+        CUtensorMap w_map;
+        const cudaError_t st = a.transposed ? encode_map(&w_map, a.w, a.rank, a.K, a.rows.E, S::kWBox, kDepth)
+                                            : encode_map(&w_map, a.w, a.K, a.rank, a.rows.E, kDepth, RP);
+        if (st != cudaSuccess)
+            return st;
         const int steps = (a.K + kDepth - 1) / kDepth;
         int parts = 1;
-        while (parts < 8 && tiles * parts < 3 * 148 && steps >= 8 * parts)
+        while (parts < 8 && tiles * parts <= 148 && steps >= 8 * parts)
             parts *= 2;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(static_cast<unsigned>(tiles) * parts);
-        cfg.blockDim = dim3(kShrinkThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim = {static_cast<unsigned>(parts), 1, 1};
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, kernel, a);
+        return launch_after(a.transposed ? lora_shrink_kernel<RP, true> : lora_shrink_kernel<RP, false>,
+                            static_cast<unsigned>(tiles) * parts, kShrinkThreads, S::kBytes, parts, stream, w_map, a);
     });
 }
 
 cudaError_t launch_lora_expand(const LoraExpandLaunch& a, cudaStream_t stream)
 {
-    const int tiles = most_tiles(a.rows);
-    const int col_tiles = (a.N + kColTile - 1) / kColTile;
-    const int64_t grid = static_cast<int64_t>(tiles) * col_tiles +
+    const int tiles = most_tiles(a.rows, kExpandTile);
+    const int steps = (a.N + kExpandCols - 1) / kExpandCols;
+    const int parts = std::min(steps, std::max(1, EP_EXPAND_CTAS * 148 / std::max(tiles, 1)));
+    const int64_t grid = static_cast<int64_t>(tiles) * parts +
                          (a.slot != nullptr ? (a.rows.T + kRowTile - 1) / kRowTile : 0);
     if (grid == 0)
         return cudaSuccess;
     return with_rank(a.rank, [&](auto rp) {
         constexpr int RP = decltype(rp)::value;
-        const auto kernel = a.transposed ? lora_expand_kernel<RP, true> : lora_expand_kernel<RP, false>;
-        const int smem = RP * kColTile * 2;
-        const cudaError_t e = allow_smem(kernel, smem);
+        using S = ExpandShape<RP>;
+        CUtensorMap w_map;
+        const cudaError_t e = a.transposed ? encode_map(&w_map, a.w, a.N, a.rank, a.rows.E, 64, RP)
+                                           : encode_map(&w_map, a.w, a.rank, a.N, a.rows.E, S::kBox, kExpandCols);
         if (e != cudaSuccess)
             return e;
-        kernel<<<static_cast<unsigned>(grid), kExpandThreads, smem, stream>>>(a, tiles, col_tiles);
-        return cudaGetLastError();
+        return launch_after(a.transposed ? lora_expand_kernel<RP, true> : lora_expand_kernel<RP, false>,
+                            static_cast<unsigned>(grid), kExpandThreads, S::kBytes, 1, stream, w_map, a, tiles, parts);
     });
 }
 
 cudaError_t launch_lora_outer(const LoraOuterLaunch& a, cudaStream_t stream)
 {
-    const int in_tiles = (a.hidden_in + kOuterCols - 1) / kOuterCols;
-    const int out_tiles = (a.hidden_out + kOuterCols - 1) / kOuterCols;
     return with_rank(a.rank, [&](auto rp) {
         constexpr int RP = decltype(rp)::value;
-        const auto kernel = lora_outer_kernel<RP>;
-        const int smem = OuterShape<RP>::kBytes;
-        const cudaError_t e = allow_smem(kernel, smem);
-        if (e != cudaSuccess)
-            return e;
+        using S = OuterShape<RP>;
+        const int in_tiles = (a.hidden_in + S::kCols - 1) / S::kCols, out_tiles = (a.hidden_out + S::kCols - 1) / S::kCols;
         const int64_t grid = static_cast<int64_t>(a.rows.E) * (in_tiles + out_tiles);
-        kernel<<<static_cast<unsigned>(grid), kOuterThreads, smem, stream>>>(a, in_tiles, out_tiles);
-        return cudaGetLastError();
+        return launch_after(lora_outer_kernel<RP>, static_cast<unsigned>(grid), kOuterThreads, S::kBytes, 1, stream, a,
+                            in_tiles, out_tiles);
     });
 }
 

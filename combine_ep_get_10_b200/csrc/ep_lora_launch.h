@@ -43,6 +43,7 @@ struct LoraShrinkLaunch {
     const float* scales; // or nullptr
     int32_t K, rank, transposed;
     float* u;
+    int32_t trigger_dependents; // the kernel launched next is one of the same call
 };
 cudaError_t launch_lora_shrink(const LoraShrinkLaunch& a, cudaStream_t stream);
 
@@ -56,6 +57,9 @@ struct LoraExpandLaunch {
     void* out;
     int32_t N, rank, transposed;
     const int32_t* slot; // [T]: copy base to out for tokens with slot -1; or nullptr
+    // 0: the kernel before may have written anything; 1: it is the one that
+    // writes u; 2: u was complete before that one let its dependents start
+    int32_t after_u;
 };
 cudaError_t launch_lora_expand(const LoraExpandLaunch& a, cudaStream_t stream);
 
@@ -70,6 +74,7 @@ struct LoraOuterLaunch {
     const float* h;
     void* db;
     int32_t hidden_in, hidden_out, rank;
+    int32_t trigger_dependents; // as for LoraShrinkLaunch
 };
 cudaError_t launch_lora_outer(const LoraOuterLaunch& a, cudaStream_t stream);
 

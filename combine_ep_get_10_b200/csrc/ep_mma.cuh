@@ -1,6 +1,6 @@
 // ep_mma.cuh -- device helpers of the kernels that multiply: asynchronous
-// 16-byte copies, ldmatrix and the warp matrix product, and the two-term bf16
-// form of an fp32 operand.
+// 16-byte copies, the two-term bf16 form of an fp32 operand, and the places of
+// 16-byte chunks in operand tiles.
 #pragma once
 
 #include "ep_device.cuh"
@@ -11,6 +11,15 @@ namespace ep {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Arrives on `bar` when this thread's copies so far are done, without waiting
+// for them.  Whoever waits on `bar` fences before the tensor core reads: a
+// proxy fence of this thread's would wait for every copy it has in flight, the
+// later stages' too.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 __device__ __forceinline__ void cp_async_commit()
@@ -24,29 +33,9 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
+__device__ __forceinline__ void cp_async_wait_all()
 {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
-// d += a (16 x 16, rows) * b (16 x 8, columns), bf16 operands, fp32 sums.
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // An fp32 pair as bf16 pairs hi + lo: hi is the value rounded to bf16, lo what
@@ -61,7 +50,8 @@ __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uin
 
 // Place of 16-byte chunk c of a row in a shared-memory tile of PC (a power of
 // two) chunks a row, so that 8 consecutive rows of one chunk lie in different
-// banks (what ldmatrix reads at once).
+// banks: what the 32-, 64- and 128-byte swizzles of tensor maps and of operand
+// descriptors give.
 template <int PC>
 __device__ __forceinline__ uint32_t swizzled(int row, int c)
 {

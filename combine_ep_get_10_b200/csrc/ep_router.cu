@@ -673,14 +673,15 @@ __device__ __forceinline__ void write_balance(const BalanceLaunch& a, int s, int
 }
 
 template <int NPL, bool BF16>
-__global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch a, int chunk, bool vec)
+__global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch a, int chunk, bool vec, bool finish)
 {
     // [2 * kBalanceWarps, E] floats at most: each warp's sums, then the experts'
     extern __shared__ float s_q[];
     __shared__ float s_z[kBalanceWarps], s_red[kBalanceWarps];
     __shared__ int s_n[kBalanceWarps];
     pdl_wait();
-    pdl_launch_dependents(); // balance_finish_kernel, which waits for this grid
+    if (finish)
+        pdl_launch_dependents(); // balance_finish_kernel, which waits for this grid
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int E = a.r.num_experts, K = a.r.num_topk, T = a.r.num_tokens, S = a.num_seqs;
     int* s_cnt = reinterpret_cast<int*>(s_q + kBalanceWarps * E);
@@ -1138,8 +1139,9 @@ cudaError_t launch_balance_loss(const BalanceLaunch& a, cudaStream_t stream)
         }
         const int T = a.r.num_tokens, chunk = chunk_tokens(std::max(T, 1));
         const unsigned grid = static_cast<unsigned>(most_chunks(T, a.num_seqs));
-        const cudaError_t e = launch_after(kernel, grid, kBalanceThreads, smem, stream, a, chunk, vec);
-        if (e != cudaSuccess || T <= chunk) // no sequence has a second chunk
+        const bool finish = T > chunk; // else no sequence has a second chunk
+        const cudaError_t e = launch_after(kernel, grid, kBalanceThreads, smem, stream, a, chunk, vec, finish);
+        if (e != cudaSuccess || !finish)
             return e;
         return launch_after(balance_finish_kernel, static_cast<unsigned>(a.num_seqs), kBalanceThreads, smem, stream, a,
                             chunk);

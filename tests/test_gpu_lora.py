@@ -378,3 +378,15 @@ def test_large_row_offsets():
     B.ep_lora_backward(dy, None, None, routing, layout, lora, dh, dx=dx, dx_base=dx, row_token=row_token)
     (rdx, _, _), (sdx, _, _) = ref.backward(dyf, few, torch.zeros((5, 16)), few, torch.zeros((5, hin)))
     close(dx[at.cuda()], rdx, sdx, hout + 16, True, "dx")
+
+
+@pytest.mark.parametrize("rank", [16, 24, 64, 72, 128])
+def test_long_runs_of_stages(rank):
+    """More steps a CTA than it has stages, for each of the three products:
+    many adapters (no tile's columns or hidden width is split), then long groups."""
+    c = Case(ids(340, 300, 27), 300, rank, 1160, 1096, 28)
+    c.check_forward()
+    c.check_backward(want=("dx",))
+    c = Case(ids(1500, 2, 29), 2, rank, 136, 264, 30)
+    c.check_forward()
+    c.check_backward()
