@@ -128,9 +128,13 @@ int most_tiles(const LoraRows& g, int tile)
 // row index in x, base or out (-1 for an entry that is none).
 __device__ __forceinline__ int row_entry(const LoraRows& g, int row, int end)
 {
-    if (row >= end)
-        return -1;
-    return g.row_token == nullptr ? row : __ldg(g.row_token + row);
+    int entry = row < end ? row : -1;
+    // predicated, into entry itself: a load in a branch would be copied at the
+    // branch's end, and the copy would wait for it
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
+                 : "+r"(entry)
+                 : "l"(g.row_token + row), "r"(g.row_token != nullptr && row < end ? 1u : 0u));
+    return entry;
 }
 
 __device__ __forceinline__ int row_index(const LoraRows& g, int entry, int row, int end)
@@ -150,20 +154,22 @@ __device__ __forceinline__ int row_at(const LoraRows& g, int row, int end)
 }
 
 // ------------------------------------------------------------------ shrink
-constexpr int kShrinkThreads = 160; // four warps that load x and store, one that loads w and multiplies
+constexpr int kShrinkThreads = 192; // four warps that load x and store, one that multiplies, one that loads w
 constexpr int kShrinkTile = 64; // rows
-constexpr int kDepth = 64;      // hidden channels a stage
+constexpr int kDepth = 128;     // hidden channels a stage, in tiles of 64
 
 template <int RP>
 struct ShrinkShape {
-    static constexpr int kStages = RP <= 32 ? 8 : (RP == 64 ? 6 : 4); // 96 KB: two CTAs an SM
+    static constexpr int kStages = RP <= 32 ? 4 : (RP == 64 ? 3 : 2); // 96 KB: two CTAs an SM
+    static constexpr int kHalfBytes = kShrinkTile * 128; // 64 channels of x
     static constexpr int kXBytes = kShrinkTile * kDepth * 2;
     static constexpr int kWBytes = RP * kDepth * 2;
     static constexpr int kStageBytes = kXBytes + kWBytes;
     static constexpr int kPitch = RP + 4; // floats a row of the partial sums
     static constexpr int kSumBytes = kShrinkTile * kPitch * 4;
     // tiles start on 1024 bytes; a product reads 128 rows from a stage's first on
-    static constexpr int kBytes = (kStages - 1) * kStageBytes + 128 * kDepth * 2 + kWBytes + 1024;
+    static constexpr int kBehind = kHalfBytes - kWBytes; // past the last stage
+    static constexpr int kBytes = kStages * kStageBytes + (kBehind > 0 ? kBehind : 0) + 1024;
     static_assert(kSumBytes <= kStages * kStageBytes, "the sums take the stages' place");
     static constexpr int kCols = RP < 32 ? 32 : RP; // tensor memory
     static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
@@ -173,9 +179,9 @@ struct ShrinkShape {
 // A cluster has one tile of rows; its CTAs split the hidden width, and each
 // adds up its share of the tile's rows over the cluster, in CTA order (the
 // same sum every time, no atomics, no partial sums in HBM).  Four warps copy
-// the rows of x from where they are, one thread brings the factor's slice and
-// multiplies from shared memory into tensor memory: what is in flight is
-// bounded by the stages alone.  The product has 128 rows: what lies behind a
+// the rows of x from where they are, a thread brings the factor's slice, and
+// another multiplies from shared memory into tensor memory: what
+// is in flight is bounded by the stages alone.  The product has 128 rows: what lies behind a
 // stage's 64 gives sums that nobody reads.
 template <int RP, bool TRANS>
 __global__ void __launch_bounds__(kShrinkThreads)
@@ -219,20 +225,25 @@ __global__ void __launch_bounds__(kShrinkThreads)
     const uint32_t tmem = s_tmem;
 
     if (warp < 4) {
-        // chunk tid % 8 of rows tid / 8 + 16 i; rows past the group's end are
-        // left out (what their rows of the product hold is not used)
-        const int c = tid % 8;
-        const uint16_t* x_row[4];
+        // 16-byte chunk tid % 16 of rows tid / 16 + 8 i; rows past the group's
+        // end are left out (what their rows of the product hold is not used)
+        const int c = tid % 16;
+        const uint16_t* x_row[8];
         uint32_t on = 0u, none = 0u; // rows with data; rows that count as zeros
+        int entry[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = rows.begin + tid / 8 + 16 * i;
-            const int at = row_at(a.rows, row, rows.end);
+        for (int i = 0; i < 8; ++i)
+            entry[i] = row_entry(a.rows, rows.begin + tid / 16 + 8 * i, rows.end);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = rows.begin + tid / 16 + 8 * i;
+            const int at = row_index(a.rows, entry[i], row, rows.end);
             on |= (at >= 0 ? 1u : 0u) << i;
             none |= (at < 0 && row < rows.end ? 1u : 0u) << i;
             x_row[i] = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(max(at, 0)) * a.K + c * 8;
         }
-        bool alive = true;
+        const uint32_t to = (c >> 3) * S::kHalfBytes + swizzled<8>(tid / 16, c & 7); // + 1024 j
+        bool alive = true; // no wait has run out
         for (int i = 0; i < n; ++i) {
             const int stage = i % S::kStages, k = (part + i * parts) * kDepth;
             if (i >= S::kStages && alive)
@@ -240,30 +251,30 @@ __global__ void __launch_bounds__(kShrinkThreads)
             const uint32_t xs = base + stage * S::kStageBytes;
             const bool in = k + c * 8 < a.K;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 8; ++j)
                 if (((on | none) >> j & 1u) != 0u)
-                    cp_async16(xs + swizzled<8>(tid / 8 + 16 * j, c), in ? x_row[j] + k : a.x,
-                               in && (on >> j & 1u) != 0u ? 16 : 0);
+                    cp_async16(xs + to + 1024u * j, in ? x_row[j] + k : a.x, in && (on >> j & 1u) != 0u ? 16 : 0);
             cp_async_arrive(&s_full[stage]);
         }
         cp_async_wait_all();
-    } else if (lane == 0) {
-        constexpr uint32_t desc = product_desc(128, RP, false, TRANS);
-        const auto load_w = [&](int i) {
-            uint64_t* full = &s_full[i % S::kStages];
-            const uint32_t ws = base + i % S::kStages * S::kStageBytes + S::kXBytes;
-            const int k0 = (part + i * parts) * kDepth;
-            mbar_arrive_expect_tx(full, S::kWBytes);
+    } else if (warp == 5) {
+        for (int i = 0; lane == 0 && i < n; ++i) {
+            const int stage = i % S::kStages, k = (part + i * parts) * kDepth;
+            if (i >= S::kStages && !mbar_wait_bounded(&s_free[stage], (i / S::kStages - 1) & 1, a.rows.err))
+                break;
+            const uint32_t ws = base + stage * S::kStageBytes + S::kXBytes;
+            mbar_arrive_expect_tx(&s_full[stage], S::kWBytes);
             if (!TRANS) {
-                tma_load3(ws, &w_map, k0, 0, e, full);
+                tma_load3(ws, &w_map, k, 0, e, &s_full[stage]);
+                tma_load3(ws + RP * 128, &w_map, k + 64, 0, e, &s_full[stage]);
             } else {
 #pragma unroll
                 for (int j = 0; j < RP; j += S::kWBox)
-                    tma_load3(ws + j * kDepth * 2, &w_map, j, k0, e, full);
+                    tma_load3(ws + j * kDepth * 2, &w_map, j, k, e, &s_full[stage]);
             }
-        };
-        for (int i = 0; i < min(n, S::kStages); ++i)
-            load_w(i);
+        }
+    } else if (lane == 0) {
+        constexpr uint32_t desc = product_desc(128, RP, false, TRANS);
         for (int i = 0; i < n; ++i) {
             const int stage = i % S::kStages;
             if (!mbar_wait_bounded(&s_full[stage], (i / S::kStages) & 1, a.rows.err))
@@ -273,19 +284,13 @@ __global__ void __launch_bounds__(kShrinkThreads)
             const uint32_t xs = base + stage * S::kStageBytes, ws = xs + S::kXBytes;
 #pragma unroll
             for (int kk = 0; kk < kDepth / 16; ++kk) {
-                const uint64_t xd = operand_desc(xs + kk * 32, Swizzle::k128, 0, 1024);
+                const uint64_t xd = operand_desc(xs + kk / 4 * S::kHalfBytes + kk % 4 * 32, Swizzle::k128, 0, 1024);
                 const uint64_t wd = TRANS ? operand_desc(ws + kk * 2 * S::kWBox * 16, S::kSwizzle, kDepth * S::kWBox * 2,
                                                          S::kWBox * 16)
-                                          : operand_desc(ws + kk * 32, Swizzle::k128, 0, 1024);
+                                          : operand_desc(ws + kk / 4 * RP * 128 + kk % 4 * 32, Swizzle::k128, 0, 1024);
                 tc_product(tmem, xd, wd, desc, i > 0 || kk > 0);
             }
             tc_commit(i == n - 1 ? &s_done : &s_free[stage]);
-            // the stage before this one is (nearly) free: its next slice
-            if (i >= 1 && i - 1 + S::kStages < n) {
-                if (!mbar_wait_bounded(&s_free[(i - 1) % S::kStages], ((i - 1) / S::kStages) & 1, a.rows.err))
-                    break;
-                load_w(i - 1 + S::kStages);
-            }
         }
     }
     __syncwarp();
@@ -602,7 +607,7 @@ __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
 #ifndef EP_OUTER_STAGE_KB
 #define EP_OUTER_STAGE_KB 100
 #endif
-constexpr int kOuterThreads = 288; // four warps that load, four that split u and store, one that multiplies
+constexpr int kOuterThreads = 320; // four warps that load x or dy, four that split u and store, one that multiplies, one that loads u
 constexpr int kOuterRows = 64;     // rows a stage
 
 template <int RP>
@@ -615,7 +620,7 @@ struct OuterShape {
     static constexpr int kStageBytes = kVBytes + kUBytes;
     static constexpr int kStages = EP_OUTER_STAGE_KB * 1024 / kStageBytes < 2 ? 2 : EP_OUTER_STAGE_KB * 1024 / kStageBytes;
     static constexpr int kBytes = kStages * kStageBytes + 1024; // tiles start on 1024 bytes
-    static constexpr int kTmem = kCols / 128 * RP < 32 ? 32 : kCols / 128 * RP;
+    static constexpr int kTmem = kCols / 128 * 2 * RP; // both terms' sums
     static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
     static constexpr int kUChunks = RP < 64 ? RP / 8 : 8; // 16-byte chunks a row of u's terms
 };
@@ -649,8 +654,8 @@ __device__ __forceinline__ int by_rows(const LoraRows& g, int i, int lane)
 // products' rows (M = 128 each), the rank their columns (N), and the sum runs
 // over the adapter's rows, kOuterRows a stage.  Both operands are MN-major: the
 // row data as it lies in HBM, and u, copied as fp32 and turned in place into
-// two bf16 tiles (hi, lo).  Sums stay in tensor memory
-// until the last row.
+// two bf16 tiles (hi, lo) that one product takes side by side.  Sums stay in
+// tensor memory until the last row; there the two terms' are added.
 template <int RP>
 __global__ void __launch_bounds__(kOuterThreads)
     lora_outer_kernel(LoraOuterLaunch a, int in_tiles, int out_tiles)
@@ -697,50 +702,59 @@ __global__ void __launch_bounds__(kOuterThreads)
     }
 
     if (warp < 4) {
-        // chunk t % VC of rows t / VC + kStep j
-        constexpr int VC = S::kCols / 8, kStep = 128 / VC, kCopies = kOuterRows / kStep;
+        // 16-byte chunk tid % VC of rows r0 + kStep j; lane l looks up the row of
+        // the warp's copy l / kLanes for its lanes of number l % kLanes
+        constexpr int VC = S::kCols / 8, kStep = 128 / VC, kCopies = kOuterRows / kStep, kLanes = kStep / 4;
+        static_assert(kCopies * kLanes <= 32 && kStep % 8 == 0, "a lane has one row to look up, a thread's rows one swizzle");
         const int c = tid % VC, r0 = tid / VC;
+        const uint32_t to = (c >> 3) * S::kHalfBytes + swizzled<8>(r0 & 7, c & 7) + (r0 & ~7) * 128u; // + 128 kStep j
         const bool in_col = n0 + c * 8 < N;
-        int entry[kCopies]; // of the next stage's rows
+        const uint16_t* from = in_col ? v + n0 + c * 8 : v;
+        const int mine = warp * kLanes + lane % kLanes + kStep * (lane / kLanes);
         const auto find = [&](int i) {
-#pragma unroll
-            for (int j = 0; j < kCopies; ++j)
-                entry[j] = row_entry(a.rows, rows.begin + i * kOuterRows + r0 + kStep * j, rows.end);
+            return row_entry(a.rows, rows.begin + i * kOuterRows + mine, lane < kCopies * kLanes ? rows.end : 0);
         };
         bool alive = true; // no wait has run out
-        if (n > 0)
-            find(0);
-        for (int i = 0; i < n; ++i) {
-            {
-                const int stage = i % S::kStages;
-                if (i >= S::kStages && alive)
-                    alive = mbar_wait_bounded(&s_free[stage], (i / S::kStages - 1) & 1, a.rows.err);
-                const int first = rows.begin + i * kOuterRows, here = min(kOuterRows, rows.end - first);
-                const uint32_t vs = base + stage * S::kStageBytes;
-                if (tid == 0) {
-                    const uint32_t u_bytes = static_cast<uint32_t>(here) * a.rank * 4;
-                    mbar_arrive_expect_tx(&s_u[stage], u_bytes);
-                    bulk_load_g2s(smem + stage * S::kStageBytes + S::kVBytes, u + static_cast<int64_t>(first) * a.rank,
-                                  u_bytes, &s_u[stage]);
-                }
-                const int used = (here + 15) & ~15; // whole steps of the sum; rows past the end are zeros
+        const auto load = [&](int i, int& entry) {
+            const int stage = i % S::kStages;
+            const int first = rows.begin + i * kOuterRows;
+            const int index = row_index(a.rows, entry, first + mine, lane < kCopies * kLanes ? rows.end : 0);
+            entry = find(i + 2);
+            if (i >= S::kStages && alive)
+                alive = mbar_wait_bounded(&s_free[stage], (i / S::kStages - 1) & 1, a.rows.err);
+            int at[kCopies];
 #pragma unroll
-                for (int j = 0; j < kCopies; ++j) {
-                    const int row = r0 + kStep * j, at = row_index(a.rows, entry[j], first + row, rows.end);
-                    const bool on = at >= 0 && in_col;
-                    if (row < used)
-                        cp_async16(vs + in_halves(row, c), on ? v + static_cast<int64_t>(at) * N + n0 + c * 8 : v,
-                                   on ? 16 : 0);
-                }
-                cp_async_arrive(&s_v[stage]);
-                if (i + 1 < n)
-                    find(i + 1);
-            }
+            for (int j = 0; j < kCopies; ++j)
+                at[j] = __shfl_sync(kFullMask, index, j * kLanes + r0 % kLanes);
+            const uint32_t vs = base + stage * S::kStageBytes + to;
+#pragma unroll
+            for (int j = 0; j < kCopies; ++j) // rows that are none, and columns past the last, are zeros
+                cp_async16(vs + 128u * kStep * j, from + static_cast<int64_t>(max(at[j], 0)) * N,
+                           at[j] >= 0 && in_col ? 16 : 0);
+            cp_async_arrive(&s_v[stage]);
+        };
+        int even = find(0), odd = find(1); // entries of the stage at hand and of the next one
+        for (int i = 0; i < n; i += 2) {
+            load(i, even);
+            if (i + 1 < n)
+                load(i + 1, odd);
         }
         cp_async_wait_all();
+    } else if (warp == 9) {
+        for (int i = 0; lane == 0 && i < n; ++i) {
+            const int stage = i % S::kStages;
+            if (i >= S::kStages && !mbar_wait_bounded(&s_free[stage], (i / S::kStages - 1) & 1, a.rows.err))
+                break;
+            const int first = rows.begin + i * kOuterRows;
+            const uint32_t bytes = static_cast<uint32_t>(min(kOuterRows, rows.end - first)) * a.rank * 4;
+            mbar_arrive_expect_tx(&s_u[stage], bytes);
+            bulk_load_g2s(smem + stage * S::kStageBytes + S::kVBytes, u + static_cast<int64_t>(first) * a.rank, bytes,
+                          &s_u[stage]);
+        }
     } else if (warp == 8) {
         if (lane == 0) {
-            constexpr uint32_t desc = product_desc(128, RP, true, true);
+            constexpr uint32_t desc = product_desc(128, 2 * RP, true, true);
+            constexpr uint32_t next = RP < 64 ? S::kTermBytes : S::kHalfBytes; // the following columns of u's terms
             constexpr uint32_t group = S::kUChunks * 128u; // 8 rows of u's terms
             for (int i = 0; i < n; ++i) {
                 const int stage = i % S::kStages;
@@ -754,63 +768,70 @@ __global__ void __launch_bounds__(kOuterThreads)
                 const uint32_t vs = base + stage * S::kStageBytes;
                 for (int kk = 0; kk < steps; ++kk) {
                     const uint32_t us = vs + S::kVBytes + kk * 2 * group;
-                    const uint64_t hi = operand_desc(us, S::kSwizzle, S::kHalfBytes, group);
-                    const uint64_t lo = operand_desc(us + S::kTermBytes, S::kSwizzle, S::kHalfBytes, group);
+                    const uint64_t ud = operand_desc(us, S::kSwizzle, next, group);
 #pragma unroll
-                    for (int m = 0; m < S::kCols / 128; ++m) {
-                        const uint64_t v = operand_desc(vs + m * 2 * S::kHalfBytes + kk * 2048u, Swizzle::k128, S::kHalfBytes,
-                                                        1024u);
-                        tc_product(tmem + m * RP, v, hi, desc, i > 0 || kk > 0);
-                        tc_product(tmem + m * RP, v, lo, desc, true);
-                    }
+                    for (int m = 0; m < S::kCols / 128; ++m)
+                        tc_product(tmem + m * 2 * RP,
+                                   operand_desc(vs + m * 2 * S::kHalfBytes + kk * 2048u, Swizzle::k128, S::kHalfBytes, 1024u),
+                                   ud, desc, i > 0 || kk > 0);
                 }
                 tc_commit(i == n - 1 ? &s_done : &s_free[stage]);
             }
         }
     } else {
-        constexpr int kVecs = RP / 8; // float4 a thread and stage
+        constexpr int kVecs = RP / 16; // pieces of 8 ranks a thread and stage
         const int st = tid - 128;
         // one thread a row: is it one of the group's, with data?
         const auto find = [&](int i) {
-            return st < kOuterRows ? row_entry(a.rows, rows.begin + i * kOuterRows + st, rows.end) : -1;
+            return row_entry(a.rows, rows.begin + i * kOuterRows + st, st < kOuterRows ? rows.end : 0);
         };
-        int entry = n > 0 ? find(0) : -1;
+        int even = find(0), odd = find(1);
         bool alive = true; // no wait has run out
-        for (int i = 0; i < n; ++i) {
+        const auto split = [&](int i, int& entry) {
             const int stage = i % S::kStages;
             const uint32_t who = __ballot_sync(
                 kFullMask,
                 st < kOuterRows && row_index(a.rows, entry, rows.begin + i * kOuterRows + st, rows.end) >= 0);
             if (warp < 6 && lane == 0)
                 s_on[i & 1][warp - 4] = who;
-            if (i + 1 < n)
-                entry = find(i + 1);
+            entry = find(i + 2);
             if (alive)
                 alive = mbar_wait_bounded(&s_u[stage], (i / S::kStages) & 1, a.rows.err);
             uint8_t* us = smem + stage * S::kStageBytes + S::kVBytes;
-            float4 f[kVecs];
+            float4 f[kVecs][2];
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
-                const int t = st + j * 128, row = t / (RP / 4), q = t % (RP / 4);
-                f[j] = q * 4 < a.rank ? *reinterpret_cast<const float4*>(us + (row * a.rank + q * 4) * 4)
-                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const int t = st + j * 128, row = t / (RP / 8), c = t % (RP / 8);
+                const float4* from = reinterpret_cast<const float4*>(us + (row * a.rank + c * 8) * 4);
+                f[j][0] = f[j][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (c * 8 < a.rank) {
+                    f[j][0] = from[0];
+                    f[j][1] = from[1];
+                }
             }
             asm volatile("bar.sync 1, 128;" ::: "memory"); // u is read (and s_on written) before its terms take its place
             const uint2 rows_on = make_uint2(s_on[i & 1][0], s_on[i & 1][1]);
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
-                const int t = st + j * 128, row = t / (RP / 4), q = t % (RP / 4);
-                uint2 h = make_uint2(0u, 0u), l = h;
+                const int t = st + j * 128, row = t / (RP / 8), c = t % (RP / 8);
+                uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
                 if (((row < 32 ? rows_on.x : rows_on.y) >> (row & 31) & 1u) != 0u) {
-                    split_bf16x2(f[j].x, f[j].y, h.x, l.x);
-                    split_bf16x2(f[j].z, f[j].w, h.y, l.y);
+                    split_bf16x2(f[j][0].x, f[j][0].y, h.x, l.x);
+                    split_bf16x2(f[j][0].z, f[j][0].w, h.y, l.y);
+                    split_bf16x2(f[j][1].x, f[j][1].y, h.z, l.z);
+                    split_bf16x2(f[j][1].z, f[j][1].w, h.w, l.w);
                 }
-                const uint32_t place = (RP < 64 ? swizzled<S::kUChunks>(row, q / 2) : in_halves(row, q / 2)) + 8 * (q & 1);
-                *reinterpret_cast<uint2*>(us + place) = h;
-                *reinterpret_cast<uint2*>(us + S::kTermBytes + place) = l;
+                const uint32_t place = RP < 64 ? swizzled<S::kUChunks>(row, c) : in_halves(row, c);
+                *reinterpret_cast<uint4*>(us + place) = h;
+                *reinterpret_cast<uint4*>(us + S::kTermBytes + place) = l;
             }
             fence_proxy_async_shared();
             mbar_arrive(&s_split[stage]);
+        };
+        for (int i = 0; i < n; i += 2) {
+            split(i, even);
+            if (i + 1 < n)
+                split(i + 1, odd);
         }
         if (n > 0)
             mbar_wait_bounded(&s_done, 0, a.rows.err);
@@ -826,7 +847,13 @@ __global__ void __launch_bounds__(kOuterThreads)
                     break;
                 float d[16];
                 if (n > 0) {
-                    tmem_load16(d, tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + m * RP + j0);
+                    const uint32_t from = tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + m * 2 * RP + j0;
+                    float lo[16];
+                    tmem_load16(d, from);
+                    tmem_load16(lo, from + RP);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        d[i] += lo[i];
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -953,12 +980,12 @@ cudaError_t launch_lora_shrink(const LoraShrinkLaunch& a, cudaStream_t stream)
         using S = ShrinkShape<RP>;
         CUtensorMap w_map;
         const cudaError_t st = a.transposed ? encode_map(&w_map, a.w, a.rank, a.K, a.rows.E, S::kWBox, kDepth)
-                                            : encode_map(&w_map, a.w, a.K, a.rank, a.rows.E, kDepth, RP);
+                                            : encode_map(&w_map, a.w, a.K, a.rank, a.rows.E, 64, RP);
         if (st != cudaSuccess)
             return st;
         const int steps = (a.K + kDepth - 1) / kDepth;
         int parts = 1;
-        while (parts < 8 && tiles * parts <= 148 && steps >= 8 * parts)
+        while (parts < 8 && tiles * parts <= 148 && steps >= 4 * parts)
             parts *= 2;
         return launch_after(a.transposed ? lora_shrink_kernel<RP, true> : lora_shrink_kernel<RP, false>,
                             static_cast<unsigned>(tiles) * parts, kShrinkThreads, S::kBytes, parts, stream, w_map, a);
