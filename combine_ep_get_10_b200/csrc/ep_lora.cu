@@ -601,26 +601,23 @@ __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
 }
 
 // ------------------------------------------------------------------- outer
-#ifndef EP_OUTER_COLS
-#define EP_OUTER_COLS 128
-#endif
-#ifndef EP_OUTER_STAGE_KB
-#define EP_OUTER_STAGE_KB 100
-#endif
 constexpr int kOuterThreads = 320; // four warps that load x or dy, four that split u and store, one that multiplies, one that loads u
 constexpr int kOuterRows = 64;     // rows a stage
+constexpr int kOuterCols = 128;    // columns of x or dy a tile: the product's M
 
 template <int RP>
 struct OuterShape {
-    static constexpr int kCols = EP_OUTER_COLS;            // columns of x or dy: kCols / 128 products
     static constexpr int kHalfBytes = kOuterRows * 128;    // 64 columns of x or dy, or of u's terms
-    static constexpr int kVBytes = kOuterRows * kCols * 2;
+    static constexpr int kVBytes = kOuterRows * kOuterCols * 2;
     static constexpr int kUBytes = kOuterRows * RP * 4;    // u as it is in HBM, then its two terms
     static constexpr int kTermBytes = kUBytes / 2;
     static constexpr int kStageBytes = kVBytes + kUBytes;
-    static constexpr int kStages = EP_OUTER_STAGE_KB * 1024 / kStageBytes < 2 ? 2 : EP_OUTER_STAGE_KB * 1024 / kStageBytes;
+    // Three CTAs an SM (two at the largest rank), their stages in 72 KB each:
+    // at rank 32 77 us, against 81 us with two CTAs and 96 KB.
+    static constexpr int kCtas = RP <= 64 ? 3 : 2;
+    static constexpr int kStages = RP <= 32 ? 3 : 2;
     static constexpr int kBytes = kStages * kStageBytes + 1024; // tiles start on 1024 bytes
-    static constexpr int kTmem = kCols / 128 * 2 * RP; // both terms' sums
+    static constexpr int kTmem = 2 * RP;                        // both terms' sums
     static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
     static constexpr int kUChunks = RP < 64 ? RP / 8 : 8; // 16-byte chunks a row of u's terms
 };
@@ -631,39 +628,99 @@ __device__ __forceinline__ uint32_t in_halves(int row, int c)
     return static_cast<uint32_t>(c >> 3) * (kOuterRows * 128u) + swizzled<8>(row, c & 7);
 }
 
-// The adapter that is i-th by rows, most first (E <= 32; else the i-th), so
-// that the CTAs that run longest start first.  One warp.
-__device__ __forceinline__ int by_rows(const LoraRows& g, int i, int lane)
+// The output tiles of a call: adapter after adapter, in each the column tiles of
+// db and then of da.  Up to 32 adapters are taken in the order of their rows,
+// most first; CTAs take tiles in turn, forth and back, so that each gets long
+// and short ones.
+struct OuterTile {
+    RowRange rows;
+    int e, n0, stages;
+    bool in; // da, from x and dh; else db, from dy and h
+};
+
+struct OuterTiles {
+    int in_tiles, out_tiles, total;
+    int adapter;   // lane i: the i-th adapter by rows
+    RowRange rows; // and its rows
+
+    // One warp.
+    __device__ __forceinline__ OuterTiles(const LoraRows& g, int in_tiles_, int out_tiles_, int lane)
+        : in_tiles(in_tiles_), out_tiles(out_tiles_), total(g.E * (in_tiles_ + out_tiles_)), adapter(0), rows{0, 0}
+    {
+        if (g.E > 32)
+            return;
+        RowRange mine{0, -1};
+        if (lane < g.E)
+            mine = group_rows(g, lane);
+        const int n = mine.end - mine.begin;
+        int before = 0;
+        for (int j = 0; j < g.E; ++j) {
+            const int o = __shfl_sync(kFullMask, n, j);
+            before += o > n || (o == n && j < lane) ? 1 : 0;
+        }
+        for (int j = 0; j < g.E; ++j) {
+            const int place = __shfl_sync(kFullMask, before, j);
+            adapter = place == lane ? j : adapter;
+        }
+        rows.begin = __shfl_sync(kFullMask, mine.begin, adapter);
+        rows.end = __shfl_sync(kFullMask, mine.end, adapter);
+    }
+    // Tile k of this CTA; false for none (a later one may be).  One warp.
+    __device__ __forceinline__ bool get(const LoraRows& g, int k, OuterTile& t) const
+    {
+        const int i = k * static_cast<int>(gridDim.x) +
+                      static_cast<int>((k & 1) != 0 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        if (i >= total)
+            return false;
+        const int per = in_tiles + out_tiles, place = i / per, tile = i - place * per;
+        t.in = tile >= out_tiles;
+        t.n0 = (t.in ? tile - out_tiles : tile) * kOuterCols;
+        if (g.E > 32) {
+            t.e = place;
+            t.rows = group_rows(g, place);
+        } else {
+            t.e = __shfl_sync(kFullMask, adapter, place);
+            t.rows.begin = __shfl_sync(kFullMask, rows.begin, place);
+            t.rows.end = __shfl_sync(kFullMask, rows.end, place);
+        }
+        t.stages = (t.rows.end - t.rows.begin + kOuterRows - 1) / kOuterRows;
+        return true;
+    }
+    __device__ __forceinline__ int rounds() const { return (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x); }
+};
+
+// The four warps that split u.
+__device__ __forceinline__ void split_warps_sync()
 {
-    if (g.E > 32)
-        return i;
-    int n = -1;
-    if (lane < g.E) {
-        const RowRange r = group_rows(g, lane);
-        n = r.end - r.begin;
-    }
-    int before = 0;
-    for (int j = 0; j < g.E; ++j) {
-        const int o = __shfl_sync(kFullMask, n, j);
-        before += o > n || (o == n && j < lane) ? 1 : 0;
-    }
-    return __ffs(__ballot_sync(kFullMask, lane < g.E && before == i)) - 1;
+    asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
 }
 
-// dW of one adapter and kCols columns of x or dy: the columns are the
-// products' rows (M = 128 each), the rank their columns (N), and the sum runs
-// over the adapter's rows, kOuterRows a stage.  Both operands are MN-major: the
-// row data as it lies in HBM, and u, copied as fp32 and turned in place into
+__device__ __forceinline__ bool split_warps_any(bool mine)
+{
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any)
+                 : "r"(mine ? 1u : 0u)
+                 : "memory");
+    return any != 0u;
+}
+
+// dW of one adapter and kOuterCols columns of x or dy, tile after tile: the
+// columns are the product's rows (M), the rank its columns (N), and the sum
+// runs over the adapter's rows, kOuterRows a stage.  Both operands are MN-major:
+// the row data as it lies in HBM, and u, copied as fp32 and turned in place into
 // two bf16 tiles (hi, lo) that one product takes side by side.  Sums stay in
-// tensor memory until the last row; there the two terms' are added.
+// tensor memory until the last row; there the two terms' are added.  The warps
+// that load run on into the next tile's stages while a tile is stored.
 template <int RP>
-__global__ void __launch_bounds__(kOuterThreads)
+__global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
     lora_outer_kernel(LoraOuterLaunch a, int in_tiles, int out_tiles)
 {
     using S = OuterShape<RP>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t s_v[S::kStages], s_u[S::kStages], s_split[S::kStages], s_free[S::kStages], s_done;
-    __shared__ uint32_t s_tmem, s_on[2][2];
+    __shared__ uint32_t s_tmem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = smem_addr(smem);
@@ -677,215 +734,205 @@ __global__ void __launch_bounds__(kOuterThreads)
         mbar_init(&s_done, 1);
         fence_mbar_init();
     }
-    const int per = in_tiles + out_tiles;
-    const int i_adapter = blockIdx.x / per, i_tile = blockIdx.x - i_adapter * per;
-    const bool in = i_tile >= out_tiles; // da, from x and dh; else db, from dy and h
-    const int N = in ? a.hidden_in : a.hidden_out;
-    const int n0 = (in ? i_tile - out_tiles : i_tile) * S::kCols;
-    const float* u = in ? a.dh : a.h;
-    const uint16_t* v = static_cast<const uint16_t*>(in ? a.x : a.dy);
     pdl_wait();
     if (a.trigger_dependents != 0)
         pdl_launch_dependents(); // what comes next needs dh, which is there
-    const int e = by_rows(a.rows, i_adapter, lane);
-    const RowRange rows = group_rows(a.rows, e);
-    const int live = rows.end - rows.begin;
-    const int n = (live + kOuterRows - 1) / kOuterRows;
-    uint32_t tmem = 0;
-    if (n > 0) {
-        if (warp == 8)
-            tmem_alloc(&s_tmem, S::kTmem);
-        tc_fence_before_sync();
-        __syncthreads();
-        tc_fence_after_sync();
-        tmem = s_tmem;
-    }
+    if (warp == 8)
+        tmem_alloc(&s_tmem, S::kTmem);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    const OuterTiles tiles(a.rows, in_tiles, out_tiles, lane);
+    const int rounds = tiles.rounds();
+    OuterTile t;
+    bool alive = true; // no wait has run out
+    int at_stage = 0;  // stages so far, over all tiles
+    const auto stage_free = [&] { // the products that read the stage's place before are done
+        if (at_stage >= S::kStages && alive)
+            alive = mbar_wait_bounded(&s_free[at_stage % S::kStages], (at_stage / S::kStages - 1) & 1, a.rows.err);
+    };
 
     if (warp < 4) {
-        // 16-byte chunk tid % VC of rows r0 + kStep j; lane l looks up the row of
-        // the warp's copy l / kLanes for its lanes of number l % kLanes
-        constexpr int VC = S::kCols / 8, kStep = 128 / VC, kCopies = kOuterRows / kStep, kLanes = kStep / 4;
-        static_assert(kCopies * kLanes <= 32 && kStep % 8 == 0, "a lane has one row to look up, a thread's rows one swizzle");
-        const int c = tid % VC, r0 = tid / VC;
-        const uint32_t to = (c >> 3) * S::kHalfBytes + swizzled<8>(r0 & 7, c & 7) + (r0 & ~7) * 128u; // + 128 kStep j
-        const bool in_col = n0 + c * 8 < N;
-        const uint16_t* from = in_col ? v + n0 + c * 8 : v;
-        const int mine = warp * kLanes + lane % kLanes + kStep * (lane / kLanes);
-        const auto find = [&](int i) {
-            return row_entry(a.rows, rows.begin + i * kOuterRows + mine, lane < kCopies * kLanes ? rows.end : 0);
-        };
-        bool alive = true; // no wait has run out
-        const auto load = [&](int i, int& entry) {
-            const int stage = i % S::kStages;
-            const int first = rows.begin + i * kOuterRows;
-            const int index = row_index(a.rows, entry, first + mine, lane < kCopies * kLanes ? rows.end : 0);
-            entry = find(i + 2);
-            if (i >= S::kStages && alive)
-                alive = mbar_wait_bounded(&s_free[stage], (i / S::kStages - 1) & 1, a.rows.err);
-            int at[kCopies];
+        // 16-byte chunk tid % 16 of rows tid / 16 + 8 j; lanes 0 .. 15 look up the
+        // rows of the warp's two half rows: j = lane / 2 of half warp lane % 2
+        const int c = tid % 16, r0 = tid / 16;
+        const uint32_t to = in_halves(r0, c); // + 1024 j
+        const int mine = warp * 2 + (lane & 1) + 8 * (lane / 2);
+        for (int k = 0; k < rounds; ++k) {
+            if (!tiles.get(a.rows, k, t))
+                continue;
+            const int N = t.in ? a.hidden_in : a.hidden_out;
+            const uint16_t* v = static_cast<const uint16_t*>(t.in ? a.x : a.dy);
+            const bool in_col = t.n0 + c * 8 < N;
+            const uint16_t* from = in_col ? v + t.n0 + c * 8 : v;
+            const int end = lane < 16 ? t.rows.end : 0;
+            const auto find = [&](int i) { return row_entry(a.rows, t.rows.begin + i * kOuterRows + mine, end); };
+            const auto load = [&](int i, int& entry) {
+                const int index = row_index(a.rows, entry, t.rows.begin + i * kOuterRows + mine, end);
+                entry = find(i + 2);
+                stage_free();
+                int at[8];
 #pragma unroll
-            for (int j = 0; j < kCopies; ++j)
-                at[j] = __shfl_sync(kFullMask, index, j * kLanes + r0 % kLanes);
-            const uint32_t vs = base + stage * S::kStageBytes + to;
+                for (int j = 0; j < 8; ++j)
+                    at[j] = __shfl_sync(kFullMask, index, j * 2 + (r0 & 1));
+                const uint32_t vs = base + at_stage % S::kStages * S::kStageBytes + to;
 #pragma unroll
-            for (int j = 0; j < kCopies; ++j) // rows that are none, and columns past the last, are zeros
-                cp_async16(vs + 128u * kStep * j, from + static_cast<int64_t>(max(at[j], 0)) * N,
-                           at[j] >= 0 && in_col ? 16 : 0);
-            cp_async_arrive(&s_v[stage]);
-        };
-        int even = find(0), odd = find(1); // entries of the stage at hand and of the next one
-        for (int i = 0; i < n; i += 2) {
-            load(i, even);
-            if (i + 1 < n)
-                load(i + 1, odd);
+                for (int j = 0; j < 8; ++j) // rows that are none, and columns past the last, are zeros
+                    cp_async16(vs + 1024u * j, from + static_cast<int64_t>(max(at[j], 0)) * N,
+                               at[j] >= 0 && in_col ? 16 : 0);
+                cp_async_arrive(&s_v[at_stage % S::kStages]);
+                ++at_stage;
+            };
+            int even = find(0), odd = find(1); // entries of the stage at hand and of the next one
+            for (int i = 0; i < t.stages; i += 2) {
+                load(i, even);
+                if (i + 1 < t.stages)
+                    load(i + 1, odd);
+            }
         }
         cp_async_wait_all();
     } else if (warp == 9) {
-        for (int i = 0; lane == 0 && i < n; ++i) {
-            const int stage = i % S::kStages;
-            if (i >= S::kStages && !mbar_wait_bounded(&s_free[stage], (i / S::kStages - 1) & 1, a.rows.err))
-                break;
-            const int first = rows.begin + i * kOuterRows;
-            const uint32_t bytes = static_cast<uint32_t>(min(kOuterRows, rows.end - first)) * a.rank * 4;
-            mbar_arrive_expect_tx(&s_u[stage], bytes);
-            bulk_load_g2s(smem + stage * S::kStageBytes + S::kVBytes, u + static_cast<int64_t>(first) * a.rank, bytes,
-                          &s_u[stage]);
+        for (int k = 0; k < rounds; ++k) {
+            if (!tiles.get(a.rows, k, t) || lane != 0)
+                continue;
+            for (int i = 0; i < t.stages; ++i, ++at_stage) {
+                stage_free();
+                const int first = t.rows.begin + i * kOuterRows, stage = at_stage % S::kStages;
+                const uint32_t bytes = static_cast<uint32_t>(min(kOuterRows, t.rows.end - first)) * a.rank * 4;
+                mbar_arrive_expect_tx(&s_u[stage], bytes);
+                bulk_load_g2s(smem + stage * S::kStageBytes + S::kVBytes,
+                              (t.in ? a.dh : a.h) + static_cast<int64_t>(first) * a.rank, bytes, &s_u[stage]);
+            }
         }
     } else if (warp == 8) {
-        if (lane == 0) {
-            constexpr uint32_t desc = product_desc(128, 2 * RP, true, true);
-            constexpr uint32_t next = RP < 64 ? S::kTermBytes : S::kHalfBytes; // the following columns of u's terms
-            constexpr uint32_t group = S::kUChunks * 128u; // 8 rows of u's terms
-            for (int i = 0; i < n; ++i) {
-                const int stage = i % S::kStages;
-                const uint32_t parity = (i / S::kStages) & 1;
-                if (!mbar_wait_bounded(&s_v[stage], parity, a.rows.err) ||
-                    !mbar_wait_bounded(&s_split[stage], parity, a.rows.err))
+        constexpr uint32_t desc = product_desc(128, 2 * RP, true, true);
+        constexpr uint32_t next = RP < 64 ? S::kTermBytes : S::kHalfBytes; // the following columns of u's terms
+        constexpr uint32_t group = S::kUChunks * 128u;                     // 8 rows of u's terms
+        for (int k = 0; k < rounds; ++k) {
+            if (!tiles.get(a.rows, k, t) || lane != 0)
+                continue;
+            for (int i = 0; i < t.stages && alive; ++i, ++at_stage) {
+                const int stage = at_stage % S::kStages;
+                const uint32_t parity = (at_stage / S::kStages) & 1;
+                alive = mbar_wait_bounded(&s_v[stage], parity, a.rows.err) &&
+                        mbar_wait_bounded(&s_split[stage], parity, a.rows.err);
+                if (!alive)
                     break;
                 fence_proxy_async_shared(); // the copies were the other threads'
                 tc_fence_after_sync();
-                const int steps = (min(kOuterRows, live - i * kOuterRows) + 15) / 16;
+                const int steps = (min(kOuterRows, t.rows.end - t.rows.begin - i * kOuterRows) + 15) / 16;
                 const uint32_t vs = base + stage * S::kStageBytes;
-                for (int kk = 0; kk < steps; ++kk) {
-                    const uint32_t us = vs + S::kVBytes + kk * 2 * group;
-                    const uint64_t ud = operand_desc(us, S::kSwizzle, next, group);
-#pragma unroll
-                    for (int m = 0; m < S::kCols / 128; ++m)
-                        tc_product(tmem + m * 2 * RP,
-                                   operand_desc(vs + m * 2 * S::kHalfBytes + kk * 2048u, Swizzle::k128, S::kHalfBytes, 1024u),
-                                   ud, desc, i > 0 || kk > 0);
-                }
-                tc_commit(i == n - 1 ? &s_done : &s_free[stage]);
+                for (int kk = 0; kk < steps; ++kk)
+                    tc_product(tmem, operand_desc(vs + kk * 2048u, Swizzle::k128, S::kHalfBytes, 1024u),
+                               operand_desc(vs + S::kVBytes + kk * 2 * group, S::kSwizzle, next, group), desc,
+                               i > 0 || kk > 0);
+                tc_commit(&s_free[stage]);
+                if (i == t.stages - 1)
+                    tc_commit(&s_done);
             }
         }
     } else {
         constexpr int kVecs = RP / 16; // pieces of 8 ranks a thread and stage
         const int st = tid - 128;
-        // one thread a row: is it one of the group's, with data?
-        const auto find = [&](int i) {
-            return row_entry(a.rows, rows.begin + i * kOuterRows + st, st < kOuterRows ? rows.end : 0);
-        };
-        int even = find(0), odd = find(1);
-        bool alive = true; // no wait has run out
-        const auto split = [&](int i, int& entry) {
-            const int stage = i % S::kStages;
-            const uint32_t who = __ballot_sync(
-                kFullMask,
-                st < kOuterRows && row_index(a.rows, entry, rows.begin + i * kOuterRows + st, rows.end) >= 0);
-            if (warp < 6 && lane == 0)
-                s_on[i & 1][warp - 4] = who;
-            entry = find(i + 2);
-            if (alive)
-                alive = mbar_wait_bounded(&s_u[stage], (i / S::kStages) & 1, a.rows.err);
-            uint8_t* us = smem + stage * S::kStageBytes + S::kVBytes;
-            float4 f[kVecs][2];
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const int t = st + j * 128, row = t / (RP / 8), c = t % (RP / 8);
-                const float4* from = reinterpret_cast<const float4*>(us + (row * a.rank + c * 8) * 4);
-                f[j][0] = f[j][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (c * 8 < a.rank) {
-                    f[j][0] = from[0];
-                    f[j][1] = from[1];
+        int sums = 0; // tiles with rows so far
+        for (int k = 0; k < rounds; ++k) {
+            if (!tiles.get(a.rows, k, t))
+                continue;
+            bool bad = false; // a row of the group has no data
+            if (a.rows.row_token != nullptr && t.stages > 0) {
+#pragma unroll 4
+                for (int row = t.rows.begin + st; row < t.rows.end; row += 128) {
+                    const int token = __ldg(a.rows.row_token + row);
+                    bad = bad || token < 0 || token >= a.rows.T;
                 }
+                bad = split_warps_any(bad);
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory"); // u is read (and s_on written) before its terms take its place
-            const uint2 rows_on = make_uint2(s_on[i & 1][0], s_on[i & 1][1]);
+            for (int i = 0; i < t.stages; ++i, ++at_stage) {
+                const int stage = at_stage % S::kStages;
+                if (alive)
+                    alive = mbar_wait_bounded(&s_u[stage], (at_stage / S::kStages) & 1, a.rows.err);
+                uint8_t* us = smem + stage * S::kStageBytes + S::kVBytes;
+                float4 f[kVecs][2];
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const int t = st + j * 128, row = t / (RP / 8), c = t % (RP / 8);
-                uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
-                if (((row < 32 ? rows_on.x : rows_on.y) >> (row & 31) & 1u) != 0u) {
-                    split_bf16x2(f[j][0].x, f[j][0].y, h.x, l.x);
-                    split_bf16x2(f[j][0].z, f[j][0].w, h.y, l.y);
-                    split_bf16x2(f[j][1].x, f[j][1].y, h.z, l.z);
-                    split_bf16x2(f[j][1].z, f[j][1].w, h.w, l.w);
+                for (int j = 0; j < kVecs; ++j) {
+                    const int p = st + j * 128, row = p / (RP / 8), c = p % (RP / 8);
+                    const float4* from = reinterpret_cast<const float4*>(us + (row * a.rank + c * 8) * 4);
+                    f[j][0] = f[j][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (c * 8 < a.rank) {
+                        f[j][0] = from[0];
+                        f[j][1] = from[1];
+                    }
                 }
-                const uint32_t place = RP < 64 ? swizzled<S::kUChunks>(row, c) : in_halves(row, c);
-                *reinterpret_cast<uint4*>(us + place) = h;
-                *reinterpret_cast<uint4*>(us + S::kTermBytes + place) = l;
-            }
-            fence_proxy_async_shared();
-            mbar_arrive(&s_split[stage]);
-        };
-        for (int i = 0; i < n; i += 2) {
-            split(i, even);
-            if (i + 1 < n)
-                split(i + 1, odd);
-        }
-        if (n > 0)
-            mbar_wait_bounded(&s_done, 0, a.rows.err);
-        tc_fence_after_sync();
-        // thread: column n0 + 128 m + st, every rank
-        uint16_t* out = static_cast<uint16_t*>(in ? a.da : a.db) + static_cast<int64_t>(e) * a.rank * N;
+                split_warps_sync(); // u is read before its terms take its place
+                const int first = t.rows.begin + i * kOuterRows;
 #pragma unroll
-        for (int m = 0; m < S::kCols / 128; ++m) {
-            const int col = n0 + m * 128 + st;
+                for (int j = 0; j < kVecs; ++j) {
+                    const int p = st + j * 128, row = p / (RP / 8), c = p % (RP / 8);
+                    uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
+                    if (first + row < t.rows.end && (!bad || row_at(a.rows, first + row, t.rows.end) >= 0)) {
+                        split_bf16x2(f[j][0].x, f[j][0].y, h.x, l.x);
+                        split_bf16x2(f[j][0].z, f[j][0].w, h.y, l.y);
+                        split_bf16x2(f[j][1].x, f[j][1].y, h.z, l.z);
+                        split_bf16x2(f[j][1].z, f[j][1].w, h.w, l.w);
+                    }
+                    const uint32_t place = RP < 64 ? swizzled<S::kUChunks>(row, c) : in_halves(row, c);
+                    *reinterpret_cast<uint4*>(us + place) = h;
+                    *reinterpret_cast<uint4*>(us + S::kTermBytes + place) = l;
+                }
+                fence_proxy_async_shared();
+                mbar_arrive(&s_split[stage]);
+            }
+            if (t.stages > 0) {
+                if (alive)
+                    alive = mbar_wait_bounded(&s_done, sums & 1, a.rows.err);
+                ++sums;
+                tc_fence_after_sync();
+            }
+            // thread: column n0 + st, every rank
+            const int N = t.in ? a.hidden_in : a.hidden_out, col = t.n0 + st;
+            uint16_t* out = static_cast<uint16_t*>(t.in ? a.da : a.db) + static_cast<int64_t>(t.e) * a.rank * N;
 #pragma unroll
             for (int j0 = 0; j0 < RP; j0 += 16) {
                 if (j0 >= a.rank)
                     break;
-                float d[16];
-                if (n > 0) {
-                    const uint32_t from = tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + m * 2 * RP + j0;
-                    float lo[16];
-                    tmem_load16(d, from);
+                uint32_t d[8]; // two ranks each
+                if (t.stages > 0) {
+                    const uint32_t from = tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + j0;
+                    float hi[16], lo[16];
+                    tmem_load16(hi, from);
                     tmem_load16(lo, from + RP);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        d[i] += lo[i];
+                    for (int i = 0; i < 8; ++i)
+                        d[i] = pack_bf16x2(hi[2 * i] + lo[2 * i], hi[2 * i + 1] + lo[2 * i + 1]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        d[i] = 0.0f;
+                    for (int i = 0; i < 8; ++i)
+                        d[i] = 0u;
                 }
-                if (col < N) {
+                if (col >= N)
+                    continue;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (j0 + 8 * h >= a.rank)
-                            break;
-                        if (in) {
+                for (int h = 0; h < 2; ++h) {
+                    if (j0 + 8 * h >= a.rank)
+                        break;
+                    if (t.in) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                out[static_cast<int64_t>(j0 + 8 * h + i) * N + col] =
-                                    static_cast<uint16_t>(pack_bf16x2(d[8 * h + i], 0.0f));
-                        } else {
-                            st_v4(out + static_cast<int64_t>(col) * a.rank + j0 + 8 * h,
-                                  make_uint4(pack_bf16x2(d[8 * h], d[8 * h + 1]), pack_bf16x2(d[8 * h + 2], d[8 * h + 3]),
-                                             pack_bf16x2(d[8 * h + 4], d[8 * h + 5]),
-                                             pack_bf16x2(d[8 * h + 6], d[8 * h + 7])));
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            out[static_cast<int64_t>(j0 + 8 * h + i) * N + col] =
+                                static_cast<uint16_t>(d[4 * h + i / 2] >> (16 * (i & 1)));
+                    } else {
+                        st_v4(out + static_cast<int64_t>(col) * a.rank + j0 + 8 * h,
+                              make_uint4(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3]));
                     }
                 }
             }
+            tc_fence_before_sync(); // the next tile's first product follows the splits of its first stage
         }
-        tc_fence_before_sync();
     }
-    if (n > 0) {
-        __syncthreads();
-        if (warp == 8)
-            tmem_free(tmem, S::kTmem);
-    }
+    __syncthreads();
+    if (warp == 8)
+        tmem_free(tmem, S::kTmem);
 }
 
 // -------------------------------------------------------------- row tokens
@@ -1019,10 +1066,11 @@ cudaError_t launch_lora_outer(const LoraOuterLaunch& a, cudaStream_t stream)
     return with_rank(a.rank, [&](auto rp) {
         constexpr int RP = decltype(rp)::value;
         using S = OuterShape<RP>;
-        const int in_tiles = (a.hidden_in + S::kCols - 1) / S::kCols, out_tiles = (a.hidden_out + S::kCols - 1) / S::kCols;
-        const int64_t grid = static_cast<int64_t>(a.rows.E) * (in_tiles + out_tiles);
-        return launch_after(lora_outer_kernel<RP>, static_cast<unsigned>(grid), kOuterThreads, S::kBytes, 1, stream, a,
-                            in_tiles, out_tiles);
+        const int in_tiles = (a.hidden_in + kOuterCols - 1) / kOuterCols;
+        const int out_tiles = (a.hidden_out + kOuterCols - 1) / kOuterCols;
+        const int64_t total = static_cast<int64_t>(a.rows.E) * (in_tiles + out_tiles);
+        const unsigned grid = static_cast<unsigned>(std::min<int64_t>(total, 148 * S::kCtas));
+        return launch_after(lora_outer_kernel<RP>, grid, kOuterThreads, S::kBytes, 1, stream, a, in_tiles, out_tiles);
     });
 }
 
