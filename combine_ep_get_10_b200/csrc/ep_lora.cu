@@ -156,11 +156,14 @@ __device__ __forceinline__ int row_at(const LoraRows& g, int row, int end)
 // ------------------------------------------------------------------ shrink
 constexpr int kShrinkThreads = 192; // four warps that load x and store, one that multiplies, one that loads w
 constexpr int kShrinkTile = 64; // rows
+#ifndef EP_SHRINK_STAGES
+#define EP_SHRINK_STAGES 3
+#endif
 constexpr int kDepth = 128;     // hidden channels a stage, in tiles of 64
 
 template <int RP>
 struct ShrinkShape {
-    static constexpr int kStages = RP <= 32 ? 4 : (RP == 64 ? 3 : 2); // 96 KB: two CTAs an SM
+    static constexpr int kStages = RP <= 32 ? EP_SHRINK_STAGES : (RP == 64 ? 3 : 2);
     static constexpr int kHalfBytes = kShrinkTile * 128; // 64 channels of x
     static constexpr int kXBytes = kShrinkTile * kDepth * 2;
     static constexpr int kWBytes = RP * kDepth * 2;
@@ -242,18 +245,26 @@ __global__ void __launch_bounds__(kShrinkThreads)
             none |= (at < 0 && row < rows.end ? 1u : 0u) << i;
             x_row[i] = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(max(at, 0)) * a.K + c * 8;
         }
-        const uint32_t to = (c >> 3) * S::kHalfBytes + swizzled<8>(tid / 16, c & 7); // + 1024 j
+        const uint32_t to = base + (c >> 3) * S::kHalfBytes + swizzled<8>(tid / 16, c & 7); // + 1024 j
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            x_row[j] += part * kDepth;
+            if ((none >> j & 1u) != 0u)
+                for (int i = 0; i < S::kStages; ++i)
+                    sts_v4(to + i * S::kStageBytes + 1024u * j, make_uint4(0u, 0u, 0u, 0u));
+        }
         bool alive = true; // no wait has run out
         for (int i = 0; i < n; ++i) {
-            const int stage = i % S::kStages, k = (part + i * parts) * kDepth;
+            const int stage = i % S::kStages;
             if (i >= S::kStages && alive)
                 alive = mbar_wait_bounded(&s_free[stage], (i / S::kStages - 1) & 1, a.rows.err);
-            const uint32_t xs = base + stage * S::kStageBytes;
-            const bool in = k + c * 8 < a.K;
+            const uint32_t bytes = (part + i * parts) * kDepth + c * 8 < a.K ? 16 : 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (((on | none) >> j & 1u) != 0u)
-                    cp_async16(xs + to + 1024u * j, in ? x_row[j] + k : a.x, in && (on >> j & 1u) != 0u ? 16 : 0);
+            for (int j = 0; j < 8; ++j) {
+                if ((on >> j & 1u) != 0u)
+                    cp_async16(to + stage * S::kStageBytes + 1024u * j, x_row[j], bytes);
+                x_row[j] += parts * kDepth;
+            }
             cp_async_arrive(&s_full[stage]);
         }
         cp_async_wait_all();
@@ -341,20 +352,104 @@ __global__ void __launch_bounds__(kShrinkThreads)
 }
 
 // ------------------------------------------------------------------ expand
-constexpr int kExpandThreads = 256; // (a ninth warp would leave 96 registers a thread, which spill)
+constexpr int kExpandThreads = 288; // eight warps that add and store, one that loads w and multiplies
 constexpr int kExpandTile = 128;    // rows: the product's M
-constexpr int kExpandCols = 128;    // columns a step: the product's N
-#ifndef EP_EXPAND_CTAS
-#define EP_EXPAND_CTAS 2
+constexpr int kExpandCols = 64;     // columns a step: the product's N
+constexpr int kExpandGrid = 2 * 148;
+#ifndef EP_STEP_ROWS
+#define EP_STEP_ROWS 128
 #endif
+#ifndef EP_SHRINK_CTAS
+#define EP_SHRINK_CTAS 296
+#endif
+
+// A CTA's share of a call: one tile of rows, and every parts-th column step of
+// it from step `part` on.
+struct ExpandShare {
+    RowRange rows;
+    int e, part, parts;
+};
+
+// Share i; false when there are fewer.  A step is taken to cost as its live rows
+// and kStepRows more; each tile gets shares for its part of the whole, rounded
+// up, so that kExpandGrid CTAs are enough (with one share a tile where there are
+// more tiles than that).  One warp; all lanes get the answer.
+__device__ __forceinline__ bool find_share(const LoraRows& g, int i, int steps, int lane, ExpandShare& s)
+{
+    constexpr int kStepRows = EP_STEP_ROWS;
+    const int per = (g.E + 31) / 32; // adapters a lane, consecutive
+    const int e0 = min(lane * per, g.E), e1 = min(e0 + per, g.E);
+    int64_t cost = 0;
+    int tiles = 0;
+#pragma unroll 8
+    for (int j = e0; j < e1; ++j) {
+        const RowRange r = group_rows(g, j);
+        const int t = (r.end - r.begin + kExpandTile - 1) / kExpandTile;
+        tiles += t;
+        cost += r.end - r.begin + t * kStepRows;
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+        tiles += __shfl_xor_sync(kFullMask, tiles, d);
+        cost += __shfl_xor_sync(kFullMask, cost, d);
+    }
+    const float spare = static_cast<float>(max(kExpandGrid - tiles, 0)) / static_cast<float>(max(cost, int64_t{1}));
+    // (the product's rounding moves a share's border at most: never more than `spare` and one a tile)
+    const auto shares = [&](int rows) {
+        return min(steps, static_cast<int>(static_cast<float>(rows + kStepRows) * spare) + 1);
+    };
+    const int full = shares(kExpandTile);
+    const auto of = [&](const RowRange& r) { // of an adapter
+        const int n = r.end - r.begin, t = (n + kExpandTile - 1) / kExpandTile;
+        return t == 0 ? 0 : (t - 1) * full + shares(n - (t - 1) * kExpandTile);
+    };
+    int n = 0;
+#pragma unroll 8
+    for (int j = e0; j < e1; ++j)
+        n += of(group_rows(g, j));
+    int inc = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kFullMask, inc, d);
+        if (lane >= d)
+            inc += o;
+    }
+    const uint32_t past = __ballot_sync(kFullMask, inc > i);
+    if (past == 0u)
+        return false;
+    const int from = __ffs(past) - 1;
+    ExpandShare mine{};
+    if (lane == from) {
+        int left = i - (inc - n);
+        for (int j = e0; j < e1; ++j) {
+            const RowRange r = group_rows(g, j);
+            const int here = of(r);
+            if (left < here) {
+                const int t = (r.end - r.begin + kExpandTile - 1) / kExpandTile, tile = min(left / full, t - 1);
+                mine.e = j;
+                mine.rows.begin = r.begin + tile * kExpandTile;
+                mine.rows.end = min(r.end, mine.rows.begin + kExpandTile);
+                mine.part = left - tile * full;
+                mine.parts = shares(mine.rows.end - mine.rows.begin);
+                break;
+            }
+            left -= here;
+        }
+    }
+    s.e = __shfl_sync(kFullMask, mine.e, from);
+    s.rows.begin = __shfl_sync(kFullMask, mine.rows.begin, from);
+    s.rows.end = __shfl_sync(kFullMask, mine.rows.end, from);
+    s.part = __shfl_sync(kFullMask, mine.part, from);
+    s.parts = __shfl_sync(kFullMask, mine.parts, from);
+    return true;
+}
 
 template <int RP>
 struct ExpandShape {
     static constexpr int kTermBytes = kExpandTile * RP * 2; // one bf16 tile of u
     static constexpr int kWBytes = kExpandCols * RP * 2;
-    static constexpr int kWStages = RP == 16 ? 6 : 2;
-    static constexpr int kPitch = 144;                      // bytes a row of a warp's tile of base: 32 x 64 columns
-    static constexpr int kTileBytes = 8 * 32 * kPitch;
+    static constexpr int kWStages = RP == 16 ? 6 : (RP == 32 ? 4 : 3); // three at least: one ahead of the step that loads
+    static constexpr int kTileBytes = 8 * 32 * 64;          // base: 32 rows of 64 bytes a warp
     static constexpr int kTilesAt = 2 * kTermBytes + kWStages * kWBytes;
     static constexpr int kBytes = kTilesAt + 2 * kTileBytes + 1024; // operands start on 1024 bytes
     static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
@@ -366,29 +461,27 @@ __device__ __forceinline__ uint32_t add_to_bf16x2(uint32_t base, float a, float 
     return pack_bf16x2(bf16_lo(base) + a, bf16_hi(base) + b);
 }
 
-// A CTA has one tile of rows and every parts-th column tile.  u stays in shared
-// memory as two bf16 tiles (hi, lo).  While one thread, another warp's each
-// time, has the factor's next column tile multiplied into one of two places in
-// tensor memory, eight warps take the other one (32 rows and 64 columns each):
+// A CTA has one tile of rows and every parts-th column step.  u stays in shared
+// memory as two bf16 tiles (hi, lo).  While one thread has the factor's next
+// columns multiplied into one of two places in tensor memory, eight warps take the other one (32 rows and 32 columns each):
 // a thread adds a row's sums to base in shared memory, then the warp stores its
 // rows from there, four lanes 32 columns, and asks for base's tile after next.
 template <int RP, bool TRANS>
 __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
-    lora_expand_kernel(const __grid_constant__ CUtensorMap w_map, LoraExpandLaunch a, int tiles, int parts)
+    lora_expand_kernel(const __grid_constant__ CUtensorMap w_map, LoraExpandLaunch a, int shares)
 {
     using S = ExpandShape<RP>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t s_w[S::kWStages], s_free[S::kWStages], s_sums[2], s_taken[2];
+    __shared__ uint64_t s_w[S::kWStages], s_sums[2], s_taken[2];
     __shared__ uint32_t s_tmem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (a.after_u == 0)
         pdl_wait();
-    const int tile = blockIdx.x / parts;
-    if (blockIdx.x >= static_cast<unsigned>(tiles) * parts) { // tokens without an adapter: out = base
-        const int t0 = (blockIdx.x - tiles * parts) * kRowTile;
+    if (static_cast<int>(blockIdx.x) >= shares) { // tokens without an adapter: out = base
+        const int t0 = (blockIdx.x - shares) * kRowTile;
         const int mine = t0 + (lane & 7) * 8 + warp;
         uint32_t todo =
-            __ballot_sync(kFullMask, lane < 8 && mine < a.rows.T && __ldg(a.slot + mine) < 0);
+            __ballot_sync(kFullMask, warp < 8 && lane < 8 && mine < a.rows.T && __ldg(a.slot + mine) < 0);
         for (; todo != 0u; todo &= todo - 1u) {
             const int64_t at = static_cast<int64_t>(t0 + (__ffs(todo) - 1) * 8 + warp) * a.N;
 #pragma unroll 4
@@ -403,26 +496,24 @@ __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
     }
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t us = smem_addr(smem), ws0 = us + 2 * S::kTermBytes;
-    if (tid == 0) {
+    if (tid == 256) {
         prefetch_map(&w_map);
-        for (int i = 0; i < S::kWStages; ++i) {
+        for (int i = 0; i < S::kWStages; ++i)
             mbar_init(&s_w[i], 1);
-            mbar_init(&s_free[i], 1);
-        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_sums[i], 1);
             mbar_init(&s_taken[i], 8);
         }
         fence_mbar_init();
     }
-    int e;
-    RowRange rows;
-    if (!find_tile<kExpandTile>(a.rows, tile, lane, e, rows)) {
+    const int steps = (a.N + kExpandCols - 1) / kExpandCols;
+    ExpandShare share;
+    if (!find_share(a.rows, blockIdx.x, steps, lane, share)) {
         pdl_wait();
         return;
     }
-    const int steps = (a.N + kExpandCols - 1) / kExpandCols;
-    const int part = blockIdx.x - tile * parts;
+    const RowRange rows = share.rows;
+    const int e = share.e, part = share.part, parts = share.parts;
     const int n = (steps - part + parts - 1) / parts; // steps part, part + parts, ..
 
     const auto load_w = [&](int i) {
@@ -435,33 +526,29 @@ __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
             for (int j = 0; j < RP; j += S::kBox)
                 tma_load3(ws + j * kExpandCols * 2, &w_map, j, n0, e, bar);
         } else {
-#pragma unroll
-            for (int h = 0; h < kExpandCols / 64; ++h)
-                tma_load3(ws + h * RP * 128, &w_map, n0 + h * 64, 0, e, bar);
+            tma_load3(ws, &w_map, n0, 0, e, bar);
         }
     };
-    if (tid == 0)
+    if (tid == 256)
         for (int i = 0; i < min(n, S::kWStages); ++i)
             load_w(i);
 
-    // warps 0 .. 7: rows 32 (warp % 4).., columns 64 (warp / 4)..; lane: rows
-    // lane / 4 + 8 r of them, 8 columns from 8 (lane % 4) on of each 32
-    const int q = warp & 3, ch = (warp >> 2) * 64;
-    const bool busy = rows.begin + 32 * q < rows.end;
+    // warp: rows 32 (warp % 4).., columns 32 (warp / 4)..; lane: rows lane / 4 + 8 r
+    // of them, 8 columns from 8 (lane % 4) on
+    const int q = warp & 3, ch = (warp >> 2) * 32;
+    const bool busy = warp < 8 && rows.begin + 32 * q < rows.end;
     int at[4];
-    const uint32_t mine = us + S::kTilesAt + warp * 32 * S::kPitch;
-    const uint32_t quad = mine + (lane / 4) * S::kPitch + (lane & 3) * 16; // + 8 kPitch r + 64 p
+    const uint32_t mine = us + S::kTilesAt + warp * 2048;
+    const uint32_t quad = mine + swizzled<4>(lane / 4, lane & 3); // + 512 r
     const auto load_base = [&](int i) {
         const int col = (part + i * parts) * kExpandCols + ch + (lane & 3) * 8;
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const bool on = a.base != nullptr && at[r] >= 0 && col + p * 32 < a.N;
-                const uint16_t* from = static_cast<const uint16_t*>(a.base) + static_cast<int64_t>(at[r]) * a.N + col + p * 32;
-                if (at[r] >= 0)
-                    cp_async16(quad + (i & 1) * S::kTileBytes + r * 8 * S::kPitch + p * 64, on ? from : a.w, on ? 16 : 0);
-            }
+        for (int r = 0; r < 4; ++r) {
+            const bool on = a.base != nullptr && at[r] >= 0 && col < a.N;
+            const uint16_t* from = static_cast<const uint16_t*>(a.base) + static_cast<int64_t>(at[r]) * a.N + col;
+            if (at[r] >= 0)
+                cp_async16(quad + (i & 1) * S::kTileBytes + r * 512, on ? from : a.w, on ? 16 : 0);
+        }
     };
     if (busy) {
 #pragma unroll
@@ -479,7 +566,7 @@ __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
 
     // u in two terms; rows past the group's end give sums that nobody reads
     const int live = rows.end - rows.begin;
-    {
+    if (warp < 8) {
         const float* u = a.u + static_cast<int64_t>(rows.begin) * a.rank;
 #pragma unroll 4
         for (int t = tid; t < live * (RP / 8); t += 256) {
@@ -498,91 +585,79 @@ __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
             *reinterpret_cast<uint4*>(smem + S::kTermBytes + place) = l;
         }
         fence_proxy_async_shared();
-    }
-    if (warp == 0)
+    } else {
         tmem_alloc(&s_tmem, 2 * kExpandCols);
+    }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = s_tmem;
 
-    const auto multiply = [&](int i) {
+    bool alive = true; // no wait has run out
+    if (tid == 256) {
         constexpr uint32_t desc = product_desc(128, kExpandCols, false, TRANS);
         constexpr uint32_t group = S::kBox * 16; // 8 rows of u's tiles
-        const int stage = i % S::kWStages;
-        bool ok = mbar_wait_bounded(&s_w[stage], (i / S::kWStages) & 1, a.rows.err);
-        if (i >= 2 && ok)
-            ok = mbar_wait_bounded(&s_taken[i & 1], (i / 2 - 1) & 1, a.rows.err);
-        if (!ok)
-            return false;
-        tc_fence_after_sync();
-        const uint32_t ws = ws0 + stage * S::kWBytes;
+        for (int i = 0; i < n && alive; ++i) {
+            const int stage = i % S::kWStages;
+            alive = mbar_wait_bounded(&s_w[stage], (i / S::kWStages) & 1, a.rows.err);
+            if (i >= 2 && alive)
+                alive = mbar_wait_bounded(&s_taken[i & 1], (i / 2 - 1) & 1, a.rows.err);
+            if (!alive)
+                break;
+            tc_fence_after_sync();
+            const uint32_t ws = ws0 + stage * S::kWBytes;
 #pragma unroll
-        for (int kk = 0; kk < RP / 16; ++kk) {
-            const uint32_t k_at = kk / 4 * kExpandTile * 128 + kk % 4 * 32;
-            const uint64_t hi = operand_desc(us + k_at, S::kSwizzle, 0, group);
-            const uint64_t lo = operand_desc(us + S::kTermBytes + k_at, S::kSwizzle, 0, group);
-            const uint64_t w = TRANS ? operand_desc(ws + kk * 2048, Swizzle::k128, RP * 128, 1024)
-                                     : operand_desc(ws + kk / 4 * kExpandCols * 128 + kk % 4 * 32, S::kSwizzle, 0, group);
-            tc_product(tmem + (i & 1) * kExpandCols, hi, w, desc, kk > 0);
-            tc_product(tmem + (i & 1) * kExpandCols, lo, w, desc, true);
+            for (int kk = 0; kk < RP / 16; ++kk) {
+                const uint32_t k_at = kk / 4 * kExpandTile * 128 + kk % 4 * 32;
+                const uint64_t hi = operand_desc(us + k_at, S::kSwizzle, 0, group);
+                const uint64_t lo = operand_desc(us + S::kTermBytes + k_at, S::kSwizzle, 0, group);
+                const uint64_t w = TRANS ? operand_desc(ws + kk * 2048, Swizzle::k128, 0, 1024)
+                                         : operand_desc(ws + kk / 4 * kExpandCols * 128 + kk % 4 * 32, S::kSwizzle, 0, group);
+                tc_product(tmem + (i & 1) * kExpandCols, hi, w, desc, kk > 0);
+                tc_product(tmem + (i & 1) * kExpandCols, lo, w, desc, true);
+            }
+            tc_commit(&s_sums[i & 1]); // frees w's stage too
+            if (i >= 1 && i - 1 + S::kWStages < n) { // the step before is done, or nearly
+                alive = mbar_wait_bounded(&s_sums[(i - 1) & 1], ((i - 1) / 2) & 1, a.rows.err);
+                if (alive)
+                    load_w(i - 1 + S::kWStages);
+            }
         }
-        tc_commit(&s_free[stage]);
-        tc_commit(&s_sums[i & 1]);
-        return true;
-    };
-    {
-        bool alive = true; // no wait has run out
-        if (tid == 0)
-            alive = multiply(0);
-        __syncwarp();
+    } else if (warp < 8) {
         uint16_t* out = static_cast<uint16_t*>(a.out);
         for (int i = 0; i < n; ++i) {
-            if (lane == 0 && warp == (i & 7) && alive) { // each warp in its turn
-                if (i >= 1 && i - 1 + S::kWStages < n) { // (before the product: with two stages it is the one it needs)
-                    alive = mbar_wait_bounded(&s_free[(i - 1) % S::kWStages], ((i - 1) / S::kWStages) & 1, a.rows.err);
-                    if (alive)
-                        load_w(i - 1 + S::kWStages);
-                }
-                if (i + 1 < n && alive)
-                    alive = multiply(i + 1);
-            }
-            __syncwarp();
             if (alive)
                 alive = mbar_wait_bounded(&s_sums[i & 1], (i / 2) & 1, a.rows.err);
             tc_fence_after_sync();
             if (busy) {
                 const uint32_t from = tmem + (static_cast<uint32_t>(q * 32) << 16) + (i & 1) * kExpandCols + ch;
-                const uint32_t tile = (i & 1) * S::kTileBytes, row = mine + tile + lane * S::kPitch;
+                const uint32_t tile = (i & 1) * S::kTileBytes;
                 cp_async_wait<1>();
                 __syncwarp();
 #pragma unroll
-                for (int h = 0; h < 64; h += 16) {
+                for (int h = 0; h < 2; ++h) {
                     float d[16];
-                    tmem_load16(d, from + h);
-                    uint4 v0 = lds_v4(row + h * 2), v1 = lds_v4(row + h * 2 + 16);
+                    tmem_load16(d, from + 16 * h);
+                    const uint32_t p0 = mine + tile + swizzled<4>(lane, 2 * h), p1 = mine + tile + swizzled<4>(lane, 2 * h + 1);
+                    uint4 v0 = lds_v4(p0), v1 = lds_v4(p1);
                     v0 = make_uint4(add_to_bf16x2(v0.x, d[0], d[1]), add_to_bf16x2(v0.y, d[2], d[3]),
                                     add_to_bf16x2(v0.z, d[4], d[5]), add_to_bf16x2(v0.w, d[6], d[7]));
                     v1 = make_uint4(add_to_bf16x2(v1.x, d[8], d[9]), add_to_bf16x2(v1.y, d[10], d[11]),
                                     add_to_bf16x2(v1.z, d[12], d[13]), add_to_bf16x2(v1.w, d[14], d[15]));
-                    sts_v4(row + h * 2, v0);
-                    sts_v4(row + h * 2 + 16, v1);
+                    sts_v4(p0, v0);
+                    sts_v4(p1, v1);
                 }
                 tc_fence_before_sync();
                 __syncwarp();
                 const int col = (part + i * parts) * kExpandCols + ch + (lane & 3) * 8;
-                uint4 v[2][4];
+                uint4 v[4];
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
+                for (int r = 0; r < 4; ++r)
+                    v[r] = lds_v4(quad + tile + r * 512);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[p][r] = lds_v4(quad + tile + r * 8 * S::kPitch + p * 64);
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (at[r] >= 0 && col + p * 32 < a.N)
-                            st_v4(out + static_cast<int64_t>(at[r]) * a.N + col + p * 32, v[p][r]);
+                for (int r = 0; r < 4; ++r)
+                    if (at[r] >= 0 && col < a.N)
+                        st_v4(out + static_cast<int64_t>(at[r]) * a.N + col, v[r]);
                 __syncwarp();
                 if (i + 2 < n)
                     load_base(i + 2);
@@ -594,7 +669,7 @@ __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
         }
     }
     __syncthreads();
-    if (warp == 0)
+    if (warp == 8)
         tmem_free(tmem, 2 * kExpandCols);
     if (a.after_u == 2)
         pdl_wait(); // this grid ends after the one before it
@@ -1032,7 +1107,7 @@ cudaError_t launch_lora_shrink(const LoraShrinkLaunch& a, cudaStream_t stream)
             return st;
         const int steps = (a.K + kDepth - 1) / kDepth;
         int parts = 1;
-        while (parts < 8 && tiles * parts <= 148 && steps >= 4 * parts)
+        while (parts < 8 && tiles * parts * 2 <= EP_SHRINK_CTAS && steps >= 4 * parts)
             parts *= 2;
         return launch_after(a.transposed ? lora_shrink_kernel<RP, true> : lora_shrink_kernel<RP, false>,
                             static_cast<unsigned>(tiles) * parts, kShrinkThreads, S::kBytes, parts, stream, w_map, a);
@@ -1043,9 +1118,9 @@ cudaError_t launch_lora_expand(const LoraExpandLaunch& a, cudaStream_t stream)
 {
     const int tiles = most_tiles(a.rows, kExpandTile);
     const int steps = (a.N + kExpandCols - 1) / kExpandCols;
-    const int parts = std::min(steps, std::max(1, EP_EXPAND_CTAS * 148 / std::max(tiles, 1)));
-    const int64_t grid = static_cast<int64_t>(tiles) * parts +
-                         (a.slot != nullptr ? (a.rows.T + kRowTile - 1) / kRowTile : 0);
+    const int shares = static_cast<int>(
+        std::min<int64_t>(static_cast<int64_t>(tiles) * steps, std::max(kExpandGrid, tiles)));
+    const int64_t grid = shares + (a.slot != nullptr ? (a.rows.T + kRowTile - 1) / kRowTile : 0);
     if (grid == 0)
         return cudaSuccess;
     return with_rank(a.rank, [&](auto rp) {
@@ -1057,7 +1132,7 @@ cudaError_t launch_lora_expand(const LoraExpandLaunch& a, cudaStream_t stream)
         if (e != cudaSuccess)
             return e;
         return launch_after(a.transposed ? lora_expand_kernel<RP, true> : lora_expand_kernel<RP, false>,
-                            static_cast<unsigned>(grid), kExpandThreads, S::kBytes, 1, stream, w_map, a, tiles, parts);
+                            static_cast<unsigned>(grid), kExpandThreads, S::kBytes, 1, stream, w_map, a, shares);
     });
 }
 
