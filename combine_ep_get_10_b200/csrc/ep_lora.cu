@@ -157,7 +157,7 @@ __device__ __forceinline__ int row_at(const LoraRows& g, int row, int end)
 constexpr int kShrinkThreads = 192; // four warps that load x and store, one that multiplies, one that loads w
 constexpr int kShrinkTile = 64; // rows
 #ifndef EP_SHRINK_STAGES
-#define EP_SHRINK_STAGES 3
+#define EP_SHRINK_STAGES 4
 #endif
 constexpr int kDepth = 128;     // hidden channels a stage, in tiles of 64
 
@@ -1106,9 +1106,7 @@ cudaError_t launch_lora_shrink(const LoraShrinkLaunch& a, cudaStream_t stream)
         if (st != cudaSuccess)
             return st;
         const int steps = (a.K + kDepth - 1) / kDepth;
-        int parts = 1;
-        while (parts < 8 && tiles * parts * 2 <= EP_SHRINK_CTAS && steps >= 4 * parts)
-            parts *= 2;
+        const int parts = std::max(1, std::min({8, EP_SHRINK_CTAS / tiles, steps / 4}));
         return launch_after(a.transposed ? lora_shrink_kernel<RP, true> : lora_shrink_kernel<RP, false>,
                             static_cast<unsigned>(tiles) * parts, kShrinkThreads, S::kBytes, parts, stream, w_map, a);
     });
