@@ -5,10 +5,14 @@
 #include <algorithm>
 #include <cfloat>
 
+#include <cooperative_groups.h>
+
 #include "ep_device.cuh"
 #include "ep_router_launch.h"
 
 namespace ep {
+
+namespace cg = cooperative_groups;
 
 namespace {
 
@@ -17,19 +21,17 @@ constexpr float kNegInf = -INFINITY;
 
 // ------------------------------------------------------------------ rows
 // Which experts a lane's NPL registers hold.
-//   without groups: vectors of kVec consecutive experts, vector after vector
-//     dealt to the lanes (one 16-byte load each), or single ones where E or
+//   without groups: vectors of kFull consecutive experts, vector after vector
+//     dealt to the lanes (VEC, one 16-byte load each), or single ones where E or
 //     the rows' alignment rules that out;
 //   with groups: 32 / G lanes hold a group, `c` consecutive experts each, so
-//     that a group is a run of whole lanes.
-template <int NPL, bool BF16, bool GROUPED>
+//     that a group is a run of whole lanes (VEC: c whole vectors).
+template <int NPL, bool BF16, bool GROUPED, bool VEC>
 struct RowMap {
     static constexpr int kFull = BF16 ? 8 : 4;
-    static constexpr int kVec = NPL < kFull ? NPL : kFull;
     int e0, n, E;
-    bool vec; // 16-byte loads
 
-    __device__ __forceinline__ RowMap(const ep_router_desc_t& r, int lane, bool vec_) : E(r.num_experts), vec(vec_)
+    __device__ __forceinline__ RowMap(const ep_router_desc_t& r, int lane) : E(r.num_experts)
     {
         if (GROUPED) {
             const int bits = 5 - (31 - __clz(r.num_groups)); // 2^bits lanes a group
@@ -38,16 +40,14 @@ struct RowMap {
             e0 = (lane >> bits) * per + min(q * c, per);
             n = max(0, min(c, per - q * c));
         } else {
-            e0 = vec ? lane * kVec : lane;
+            e0 = VEC ? lane * kFull : lane;
             n = E - e0;
         }
     }
     // Register j holds expert e0 + offset(j), if holds(j).
-    __device__ __forceinline__ int offset(int j) const
+    static __device__ __forceinline__ constexpr int offset(int j)
     {
-        if (GROUPED)
-            return j;
-        return vec ? (j / kVec) * (32 * kVec) + j % kVec : 32 * j;
+        return GROUPED ? j : (VEC ? (j / kFull) * (32 * kFull) + j % kFull : 32 * j);
     }
     __device__ __forceinline__ bool holds(int j) const { return offset(j) < n; }
 };
@@ -63,7 +63,7 @@ int groups_run(const ep_router_desc_t& r) // c of RowMap
 // inf - inf).
 __device__ __forceinline__ float clean_logit(float l)
 {
-    return l > kNegInf ? fminf(l, FLT_MAX) : kNegInf;
+    return fminf(fmaxf(l, kNegInf), FLT_MAX); // fmaxf(NaN, x) is x
 }
 
 template <bool BF16>
@@ -74,48 +74,61 @@ __device__ __forceinline__ float load_logit(const void* logits, int64_t i)
     return __ldg(static_cast<const float*>(logits) + i);
 }
 
-// The lane's logits, closed ones and registers that hold nothing as -inf.
-template <int NPL, bool BF16, bool GROUPED>
-__device__ __forceinline__ void load_row(float (&v)[NPL], const void* logits, int64_t row,
-                                         const RowMap<NPL, BF16, GROUPED>& map)
-{
-    using Map = RowMap<NPL, BF16, GROUPED>;
-    const int64_t at = row * map.E + map.e0;
-    if (Map::kVec == Map::kFull && map.vec) {
+// A lane's part of a row as it lies in memory, so that the next row can be on
+// its way while one is worked on.
+template <int NPL, bool BF16, bool GROUPED, bool VEC>
+struct RawRow {
+    using Map = RowMap<NPL, BF16, GROUPED, VEC>;
+    static constexpr int kWords = VEC ? NPL * (BF16 ? 2 : 4) / 16 : NPL;
+    uint4 vec[VEC ? kWords : 1];
+    float one[VEC ? 1 : NPL];
+
+    __device__ __forceinline__ void load(const void* logits, int64_t row, const Map& map, bool on)
+    {
+        const int64_t at = row * map.E + map.e0;
+        if (VEC) {
+            const uint32_t closed = BF16 ? 0xff80ff80u : 0xff800000u;
 #pragma unroll
-        for (int j = 0; j < NPL; j += Map::kVec) {
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            const bool on = map.holds(j);
-            if (on)
-                w = BF16 ? ld_nc_v4(static_cast<const uint16_t*>(logits) + at + map.offset(j))
-                         : ld_nc_v4(static_cast<const float*>(logits) + at + map.offset(j));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (BF16) {
-                    v[(j + 2 * i) % NPL] = on ? bf16_lo(u[i]) : kNegInf;
-                    v[(j + 2 * i + 1) % NPL] = on ? bf16_hi(u[i]) : kNegInf;
-                } else {
-                    v[(j + i) % NPL] = on ? __uint_as_float(u[i]) : kNegInf;
-                }
+            for (int j = 0; j < NPL; j += Map::kFull) {
+                uint4& w = vec[j / Map::kFull];
+                w = make_uint4(closed, closed, closed, closed);
+                const void* from = BF16 ? static_cast<const void*>(static_cast<const uint16_t*>(logits) + at + Map::offset(j))
+                                        : static_cast<const void*>(static_cast<const float*>(logits) + at + Map::offset(j));
+                asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                             "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                             : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)
+                             : "l"(from), "r"(on && map.holds(j) ? 1u : 0u));
             }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NPL; ++j)
+                one[j] = on && map.holds(j) ? load_logit<BF16>(logits, at + Map::offset(j)) : kNegInf;
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < NPL; ++j)
-            v[j] = map.holds(j) ? load_logit<BF16>(logits, at + map.offset(j)) : kNegInf;
     }
+    // The logits, closed ones and registers that hold nothing as -inf.
+    __device__ __forceinline__ void take(float (&v)[NPL]) const
+    {
 #pragma unroll
-    for (int j = 0; j < NPL; ++j)
-        v[j] = clean_logit(v[j]);
-}
+        for (int j = 0; j < NPL; ++j) {
+            float l;
+            if (VEC) {
+                const uint4& w = vec[j / Map::kFull];
+                const int i = j % Map::kFull, k = BF16 ? i / 2 : i;
+                const uint32_t u = k == 0 ? w.x : (k == 1 ? w.y : (k == 2 ? w.z : w.w));
+                l = BF16 ? (i % 2 == 0 ? bf16_lo(u) : bf16_hi(u)) : __uint_as_float(u);
+            } else {
+                l = one[j];
+            }
+            v[j] = clean_logit(l);
+        }
+    }
+};
 
 __device__ __forceinline__ float warp_max(float v)
 {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(kFullMask, v, d));
-    return v;
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
 }
 
 __device__ __forceinline__ float warp_min(float v)
@@ -158,19 +171,6 @@ __device__ __forceinline__ float fast_sigmoid(float l)
 constexpr float kSigmoidTail = -60.0f;
 
 // -------------------------------------------------------------- selection
-// Finite floats and +inf as unsigned integers of the same order; 0 is below
-// every one of them and stands for "cannot be chosen".  -0 counts as +0.
-__device__ __forceinline__ uint32_t order_key(float c)
-{
-    const uint32_t b = __float_as_uint(c + 0.0f);
-    return b ^ ((b >> 31) != 0u ? 0xffffffffu : 0x80000000u);
-}
-
-__device__ __forceinline__ float key_value(uint32_t k)
-{
-    return __uint_as_float(k ^ ((k >> 31) != 0u ? 0x80000000u : 0xffffffffu));
-}
-
 // The choice of one row in fp64, for the rows whose fp32 values lie too close
 // together to tell their order.  c (shared memory of this warp): E values.
 // Lane k returns the k-th chosen id, or -1.
@@ -302,19 +302,22 @@ __device__ __forceinline__ int place_in_order(T value, int e, int count)
 // values alone where only their order is open, else (a value below t, or a
 // group, could come in) the whole row.  Values that are equal because logit
 // and bias are equal need no second look.
-template <int NPL, bool BF16, bool GROUPED>
-__global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopkLaunch a, bool vec)
+template <int NPL, bool BF16, bool GROUPED, bool VEC>
+__global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopkLaunch a)
 {
     extern __shared__ double s_wide[];
-    __shared__ uint2 s_list[kTopkWarps][2][32]; // (key, expert): as gathered, in order
+    __shared__ float2 s_list[kTopkWarps][2][32]; // (value, expert): as gathered, in order
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_wait();
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTopkWarps + warp;
+    const int E = a.r.num_experts, K = a.r.num_topk;
+    const RowMap<NPL, BF16, GROUPED, VEC> map(a.r, lane);
+    pdl_wait();
     if (t >= a.r.num_tokens)
         return;
-    const int E = a.r.num_experts, K = a.r.num_topk;
     int64_t* idx_out = a.topk_idx + t * K;
     float* w_out = a.topk_weights + t * K;
+    RawRow<NPL, BF16, GROUPED, VEC> raw;
+    raw.load(a.logits, t, map, true);
     if (a.token_mask != nullptr && __ldg(a.token_mask + t) == 0) {
         if (lane < K) {
             idx_out[lane] = -1;
@@ -324,38 +327,30 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
     }
     const bool softmax = a.r.score == EP_SCORE_SOFTMAX;
     const bool by_logit = !GROUPED && a.bias == nullptr;
-    const RowMap<NPL, BF16, GROUPED> map(a.r, lane, vec);
-    float v[NPL];
-    load_row(v, a.logits, t, map);
+    float c[NPL]; // the values chosen by; -inf: not to be chosen
+    raw.take(c);
 
     float m = 0.0f, z = 1.0f;
     if (softmax && (!by_logit || a.r.normalize == 0)) {
-        m = row_max(v);
+        m = fmaxf(row_max(c), -FLT_MAX);
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < NPL; ++j)
-            sum += v[j] > kNegInf ? __expf(v[j] - m) : 0.0f;
+            sum += __expf(c[j] - m); // 0 for -inf
         z = warp_sum(sum);
     }
     const float es = softmax ? 4e-6f / z : 5e-7f;
-    const auto err = [es](float c) { return es + 1.3e-7f * fabsf(c); };
+    const auto err = [es](float x) { return es + 1.3e-7f * fabsf(x); };
     bool sure = true; // no group's place is open
-    uint32_t key[NPL];
-    if (by_logit) {
-#pragma unroll
-        for (int j = 0; j < NPL; ++j)
-            key[j] = v[j] > kNegInf ? order_key(v[j]) : 0u;
-    } else {
-        float c[NPL];
+    if (!by_logit) {
         const float inv_z = 1.0f / z;
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-            float s = softmax ? __expf(v[j] - m) * inv_z : fast_sigmoid(v[j]);
+            float s = softmax ? __expf(c[j] - m) * inv_z : fast_sigmoid(c[j]);
             if (a.bias != nullptr && map.holds(j))
                 s += __ldg(a.bias + map.e0 + map.offset(j));
-            c[j] = v[j] > kNegInf && s > kNegInf ? s : kNegInf;
+            c[j] = c[j] > kNegInf ? fmaxf(s, kNegInf) : kNegInf; // (a bias of NaN closes too)
         }
-        bool stay = true;
         if (GROUPED && a.r.topk_groups < a.r.num_groups) {
             const int G = a.r.num_groups, bits = 5 - (31 - __clz(G)), mine = lane >> bits;
             float t1 = kNegInf, t2 = kNegInf;
@@ -377,120 +372,121 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
                 const float o = __shfl_sync(kFullMask, value, g << bits);
                 before += (o > value || (o == value && g < mine)) ? 1 : 0;
             }
-            stay = before < a.r.topk_groups;
+            const bool stay = before < a.r.topk_groups;
             const float low = warp_min(stay ? value - ge : INFINITY);
             const float high = warp_max(stay || value == kNegInf ? kNegInf : value + ge);
             sure = high == kNegInf || low > high;
-        }
 #pragma unroll
-        for (int j = 0; j < NPL; ++j)
-            key[j] = stay && c[j] > kNegInf ? order_key(c[j]) : 0u;
+            for (int j = 0; j < NPL; ++j)
+                c[j] = stay ? c[j] : kNegInf;
+        }
     }
 
     // lane k: the k-th chosen, and those after it as far as they are known
     int my_idx = -1;
-    uint32_t my_key = 0u;
-    uint32_t best = key[0];
+    float my_c = kNegInf;
+    float best = c[0];
 #pragma unroll
     for (int j = 1; j < NPL; ++j)
-        best = max(best, key[j]);
+        best = fmaxf(best, c[j]);
     // (two values more where the order has to be checked: what comes after the
     // K-th is then known, and what is not gathered is well below it)
-    uint32_t least = 0u;
+    float least = kNegInf;
     const int values = by_logit ? K : K + 2;
     for (int k = 0; k < values; ++k) {
-        least = __reduce_max_sync(kFullMask, best);
-        if (least == 0u)
+        least = warp_max(best);
+        if (least == kNegInf)
             break;
         if (best == least)
-            best = 0u;
+            best = kNegInf;
     }
-    const bool all = least == 0u; // everything that can be chosen is gathered
-    least = max(least, 1u);
+    const bool all = least == kNegInf; // everything that can be chosen is gathered
+    least = fmaxf(least, -FLT_MAX);
     int count = 0;
 #pragma unroll
     for (int j = 0; j < NPL; ++j) {
-        const bool in = key[j] >= least;
+        const bool in = c[j] >= least;
         const uint32_t who = __ballot_sync(kFullMask, in);
         const int at = count + __popc(who & ((1u << lane) - 1u));
         if (in && at < 32)
-            s_list[warp][0][at] = make_uint2(key[j], static_cast<uint32_t>(map.e0 + map.offset(j)));
+            s_list[warp][0][at] = make_float2(c[j], __int_as_float(map.e0 + map.offset(j)));
         count += __popc(who);
     }
     __syncwarp();
-    uint32_t after = 0u; // one by one: the (K + 1)-th value
+    float after = kNegInf; // one by one: the (K + 1)-th value
     if (count <= 32) {
-        uint2 mine = make_uint2(0u, 0u);
+        float2 mine = make_float2(kNegInf, 0.0f);
         if (lane < count)
             mine = s_list[warp][0][lane];
+        const int id = __float_as_int(mine.y);
         int place = 0;
+#pragma unroll 4
         for (int i = 0; i < count; ++i) {
-            const uint2 o = s_list[warp][0][i];
-            place += (o.x > mine.x || (o.x == mine.x && o.y < mine.y)) ? 1 : 0;
+            const float2 o = s_list[warp][0][i];
+            place += (o.x > mine.x || (o.x == mine.x && __float_as_int(o.y) < id)) ? 1 : 0;
         }
         if (lane < count)
             s_list[warp][1][place] = mine;
         __syncwarp();
         if (lane < count) {
             mine = s_list[warp][1][lane];
-            my_key = mine.x;
-            my_idx = static_cast<int>(mine.y);
+            my_c = mine.x;
+            my_idx = __float_as_int(mine.y);
         }
     } else {
         for (int k = 0; k <= K; ++k) {
-            uint32_t top = 0u;
+            float top = kNegInf;
             int e = E;
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
-                if (key[j] > top) {
-                    top = key[j];
+                if (c[j] > top) {
+                    top = c[j];
                     e = map.e0 + map.offset(j);
                 }
-            after = __reduce_max_sync(kFullMask, top);
-            if (after == 0u)
+            after = warp_max(top);
+            if (after == kNegInf)
                 break;
             const int first = static_cast<int>(__reduce_min_sync(kFullMask, static_cast<uint32_t>(top == after ? e : E)));
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
                 if (map.e0 + map.offset(j) == first)
-                    key[j] = 0u;
+                    c[j] = kNegInf;
             if (lane == k && k < K) {
                 my_idx = first;
-                my_key = after;
+                my_c = after;
             }
         }
     }
+    float l = my_c; // the logit itself without bias and groups
     if (!by_logit) {
-        const float l = my_idx >= 0 ? clean_logit(load_logit<BF16>(a.logits, t * E + my_idx)) : 0.0f;
+        l = my_idx >= 0 ? clean_logit(load_logit<BF16>(a.logits, t * E + my_idx)) : 0.0f;
         const float b = my_idx >= 0 && a.bias != nullptr ? __ldg(a.bias + my_idx) : 0.0f;
-        uint32_t next = __shfl_down_sync(kFullMask, my_key, 1);
+        float n = __shfl_down_sync(kFullMask, my_c, 1);
         const float nl = __shfl_down_sync(kFullMask, l, 1), nb = __shfl_down_sync(kFullMask, b, 1);
-        const uint32_t last = __shfl_sync(kFullMask, my_key, K - 1); // 0: fewer than K
-        const float c = key_value(my_key);
+        const float last = __shfl_sync(kFullMask, my_c, K - 1); // -inf: fewer than K
         // the order of the chosen, and of what is equal to the last of them
-        bool like = l == nl && b == nb, open = lane < K || my_key == last;
+        bool like = l == nl && b == nb;
+        const bool open = lane < K || my_c == last;
         if (lane == 31)
-            next = 0u;
+            n = kNegInf;
         if (count > 32 && lane == K - 1) {
-            next = after; // more of these values may follow: equal ones settle nothing
+            n = after; // more of these values may follow: equal ones settle nothing
             like = false;
         }
-        const float n = key_value(next);
-        const bool order = __all_sync(kFullMask, !open || my_key == 0u || next == 0u || like || c - err(c) > n + err(n));
+        const bool order = __all_sync(kFullMask, !open || my_c == kNegInf || n == kNegInf || like ||
+                                                     my_c - err(my_c) > n + err(n));
         // what was not gathered is below `least`
-        const float k_th = key_value(last), rest = key_value(least);
-        const bool closed = all || count > 32 || k_th - err(k_th) > rest + err(rest);
+        const bool closed = all || count > 32 || last - err(last) > least + err(least);
         if (!sure || !closed || (!order && count > 32)) {
             my_idx = choose_wide<BF16>(a, t, s_wide + static_cast<size_t>(warp) * E, lane);
+            l = my_idx >= 0 ? clean_logit(load_logit<BF16>(a.logits, t * E + my_idx)) : 0.0f;
         } else if (!order) {
             double sum = 1.0;
             if (softmax) {
                 sum = 0.0;
 #pragma unroll 1
-                for (int e = lane; e < E; e += 32) {
-                    const float o = clean_logit(load_logit<BF16>(a.logits, t * E + e));
-                    sum += o > kNegInf ? exp(static_cast<double>(o) - m) : 0.0;
-                }
+                for (int e = lane; e < E; e += 32)
+                    sum += exp(static_cast<double>(clean_logit(load_logit<BF16>(a.logits, t * E + e))) - m);
                 for (int d = 16; d >= 1; d >>= 1)
                     sum += __shfl_xor_sync(kFullMask, sum, d);
             }
@@ -498,20 +494,21 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
             const double c64 = (softmax ? exp(l64 - m) / sum : 1.0 / (1.0 + exp(-l64))) + b;
             const int place = place_in_order(c64, my_idx, count);
             if (lane < count)
-                s_list[warp][0][place].y = static_cast<uint32_t>(my_idx);
+                s_list[warp][0][place] = make_float2(l, __int_as_float(my_idx));
             __syncwarp();
-            if (lane < count)
-                my_idx = static_cast<int>(s_list[warp][0][lane].y);
+            if (lane < count) {
+                l = s_list[warp][0][lane].x;
+                my_idx = __float_as_int(s_list[warp][0][lane].y);
+            }
         }
     }
     if (lane >= K)
         my_idx = -1;
 
     const bool got = my_idx >= 0;
-    const float l = got ? clean_logit(load_logit<BF16>(a.logits, t * E + my_idx)) : kNegInf;
     float w = 0.0f;
     if (a.r.normalize != 0) {
-        const float lm = warp_max(l);
+        const float lm = warp_max(got ? l : kNegInf);
         if (got)
             w = softmax || lm < kSigmoidTail ? expf(l - lm) : sigmoid(l);
         const float total = warp_sum(w);
@@ -529,16 +526,21 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
 // Tokens are dealt out in chunks of at most `chunk` tokens of one sequence,
 // sequence after sequence.  A CTA sums a chunk; where that is the whole
 // sequence it writes the results, else it leaves its sums in the workspace and
-// a CTA of the second kernel adds the sequence's up in chunk order (fixed
+// a cluster of the second kernel adds the sequence's up in a fixed order (fixed
 // order, no floating-point atomics, nothing that one call leaves for the next).
 constexpr int kBalanceWarps = 16;
 constexpr int kBalanceThreads = kBalanceWarps * 32;
-constexpr int kBalanceCtas = 148; // chunks of a long batch: one a CTA and SM
+#ifndef EP_BAL_CTAS
+#define EP_BAL_CTAS 148
+#endif
+constexpr int kBalanceCtas = EP_BAL_CTAS; // chunks of a long batch: one a CTA and SM
+constexpr int kFewTokens = 256;
 
-// Tokens a chunk, a multiple of the warps.
-__host__ __device__ __forceinline__ int chunk_tokens(int64_t T)
+// Tokens a chunk, a multiple of the warps.  Few tokens make one chunk each
+// sequence: the second launch would cost more than the longer sums.
+int chunk_tokens(int64_t T)
 {
-    const int64_t each = (T + kBalanceCtas - 1) / kBalanceCtas;
+    const int64_t each = T <= kFewTokens ? T : (T + kBalanceCtas - 1) / kBalanceCtas;
     return static_cast<int>((each + kBalanceWarps - 1) / kBalanceWarps * kBalanceWarps);
 }
 
@@ -672,8 +674,8 @@ __device__ __forceinline__ void write_balance(const BalanceLaunch& a, int s, int
     }
 }
 
-template <int NPL, bool BF16>
-__global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch a, int chunk, bool vec, bool finish)
+template <int NPL, bool BF16, bool VEC>
+__global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch a, int chunk, bool finish)
 {
     // [2 * kBalanceWarps, E] floats at most: each warp's sums, then the experts'
     extern __shared__ float s_q[];
@@ -711,21 +713,32 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch 
     __syncthreads();
 
     const bool softmax = a.r.score == EP_SCORE_SOFTMAX;
-    const RowMap<NPL, BF16, false> map(a.r, lane, vec);
+    const RowMap<NPL, BF16, false, VEC> map(a.r, lane);
     float acc[NPL];
 #pragma unroll
     for (int j = 0; j < NPL; ++j)
         acc[j] = 0.0f;
     float zz = 0.0f;
     int live = 0;
+    // one token a warp: its row, mask and ids are loaded while the one before is summed
+    RawRow<NPL, BF16, false, VEC> raw;
+    int64_t e_next = -1;
+    bool on_next = false;
+    const auto load = [&](int t) {
+        const bool in = t < c.tokens.end;
+        on_next = in && (a.token_mask == nullptr || __ldg(a.token_mask + t) != 0);
+        e_next = in && lane < K ? __ldg(a.topk_idx + static_cast<int64_t>(t) * K + lane) : -1;
+        raw.load(a.logits, t, map, in);
+    };
+    load(c.tokens.begin + warp);
     for (int t = c.tokens.begin + warp; t < c.tokens.end; t += kBalanceWarps) {
-        if (a.token_mask != nullptr && __ldg(a.token_mask + t) == 0)
-            continue;
         float v[NPL];
-        load_row(v, a.logits, t, map);
-        int64_t e = -1;
-        if (lane < K)
-            e = __ldg(a.topk_idx + static_cast<int64_t>(t) * K + lane);
+        raw.take(v);
+        const int64_t e = e_next;
+        const bool on = on_next;
+        load(t + kBalanceWarps);
+        if (!on)
+            continue;
         const float m = row_max(v);
         if (!(m > kNegInf))
             continue; // every expert closed
@@ -736,7 +749,7 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch 
         float p[NPL];
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-            p[j] = v[j] > kNegInf ? __expf(v[j] - m) : 0.0f;
+            p[j] = __expf(v[j] - m); // 0 for -inf
             sum += p[j];
         }
         sum = warp_sum(sum);
@@ -788,38 +801,43 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch 
         part.tails[c.index] = make_int2(__float_as_int(z), n);
 }
 
-// One CTA a sequence: the results of those that are made of several chunks.
+// One cluster a sequence: the results of those that are made of several chunks.
+// The CTAs share out the experts and, in each, the warps the chunks (one CTA
+// alone would draw all the partial sums through one SM: 7 us for 148 chunks of
+// 256 experts).
+constexpr int kFinishCluster = 8;
+constexpr int kFinishExperts = kRouterMaxExperts / kFinishCluster; // a CTA, at most
+
 __global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(BalanceLaunch a, int chunk)
 {
-    extern __shared__ float s_q[]; // [2 * kBalanceWarps, E] floats at most, as above
-    __shared__ float s_z, s_red[kBalanceWarps];
+    __shared__ float s_q[kBalanceWarps][kFinishExperts];
+    __shared__ int s_cnt[kBalanceWarps][kFinishExperts];
+    __shared__ float s_z, s_red[kBalanceWarps], s_sum;
     __shared__ int s_n;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int E = a.r.num_experts, T = a.r.num_tokens, S = a.num_seqs, s = blockIdx.x;
-    int* s_cnt = reinterpret_cast<int*>(s_q + kBalanceWarps * E);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = static_cast<int>(cluster.block_rank());
+    const int E = a.r.num_experts, T = a.r.num_tokens, S = a.num_seqs, s = blockIdx.x / kFinishCluster;
     const int64_t chunks = most_chunks(T, S);
     const BalanceSums part = balance_sums(a.workspace, chunks, E);
     // (what it reads before the wait is older than the kernel that it waits for)
     const SeqChunks c = find_seq_chunks(a.seq_offsets, T, S, chunk, s, lane);
     pdl_wait();
     if (c.of <= 1 || c.total > chunks)
-        return;
-    // the chunks in order: each run of `width` threads takes every runs-th one
-    const int width = (E + 31) / 32 * 32, runs = max(1, kBalanceThreads / width);
-    const int run = tid / width;
-    for (int e = tid % width; e < E && run < runs; e += kBalanceThreads) {
+        return; // the whole cluster
+    const int per = (E + kFinishCluster - 1) / kFinishCluster, e0 = min(rank * per, E), n_e = min(per, E - e0);
+    for (int x = lane; x < n_e; x += 32) {
         float q = 0.0f;
         int cnt = 0;
-#pragma unroll 16
-        for (int i = run; i < c.of; i += runs) {
-            const int2 o = __ldcg(part.sums + (c.first + i) * E + e);
+#pragma unroll 10
+        for (int i = warp; i < c.of; i += kBalanceWarps) {
+            const int2 o = __ldcg(part.sums + (c.first + i) * E + e0 + x);
             q += __int_as_float(o.x);
             cnt += o.y;
         }
-        s_q[run * E + e] = q;
-        s_cnt[run * E + e] = cnt;
+        s_q[warp][x] = q;
+        s_cnt[warp][x] = cnt;
     }
-    if (warp == 0) {
+    if (warp == 0) { // every CTA needs the tokens
         float z = 0.0f;
         int n = 0;
         for (int i = lane; i < c.of; i += 32) {
@@ -835,27 +853,53 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(Balance
         }
     }
     __syncthreads();
-    if (runs > 1) {
+    const int tokens = s_n;
+    const float nf = static_cast<float>(tokens);
+    float fp = 0.0f;
+    if (tid < n_e) {
         float q = 0.0f;
         int cnt = 0;
-        if (tid < E) {
-            for (int i = 0; i < runs; ++i) {
-                q += s_q[i * E + tid];
-                cnt += s_cnt[i * E + tid];
-            }
+#pragma unroll
+        for (int w = 0; w < kBalanceWarps; ++w) {
+            q += s_q[w][tid];
+            cnt += s_cnt[w][tid];
         }
-        __syncthreads();
-        if (tid < E) {
-            s_q[tid] = q;
-            s_cnt[tid] = cnt;
-        }
-        __syncthreads();
+        const float mean = tokens > 0 ? q / nf : 0.0f;
+        const int64_t at = static_cast<int64_t>(s) * E + e0 + tid;
+        a.counts[at] = tokens > 0 ? cnt : 0;
+        if (a.mean_scores != nullptr)
+            a.mean_scores[at] = mean;
+        fp = static_cast<float>(cnt) * mean;
     }
-    write_balance(a, s, s_n, s_z, s_q, s_cnt, s_red);
+    fp = warp_sum(fp);
+    if (lane == 0)
+        s_red[warp] = fp;
+    __syncthreads();
+    if (tid == 0) {
+        float sum = 0.0f;
+        for (int w = 0; w < kBalanceWarps; ++w)
+            sum += s_red[w];
+        s_sum = sum;
+    }
+    cluster.sync();
+    if (rank == 0 && tid == 0) {
+        float sum = 0.0f;
+        for (int i = 0; i < kFinishCluster; ++i)
+            sum += *cluster.map_shared_rank(&s_sum, i);
+        a.losses[2 * s] = tokens > 0 ? sum * (static_cast<float>(E) / (static_cast<float>(a.r.num_topk) * nf)) : 0.0f;
+        a.losses[2 * s + 1] = tokens > 0 ? s_z / nf : 0.0f;
+        a.seq_tokens[s] = tokens;
+    }
+    cluster.sync(); // no CTA leaves while its sum is read
 }
 
 // ---------------------------------------------------------------- backward
 constexpr int kBackwardWarps = 4;
+#ifndef EP_BW_FILL
+#define EP_BW_FILL 16
+#endif
+constexpr int kBackwardFill = 148 * EP_BW_FILL; // warps that the device holds at once
+constexpr int kMostRun = 16;
 
 // The sequence of token t (the last one that begins at or before it), -1 when
 // it is in none: each step reads 32 offsets spread over what is left.
@@ -878,208 +922,273 @@ __device__ __forceinline__ int find_seq(const int32_t* offsets, int S, int t, in
     return s < S ? s : -1;
 }
 
-template <int NPL, bool BF16>
-__global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(RouterBackwardLaunch a, bool vec)
+// 16 bytes of shared or global memory at a time where the lane's experts lie
+// together.
+template <int NPL, bool BF16, bool VEC, typename F4, typename F1>
+__device__ __forceinline__ void each_expert(const RowMap<NPL, BF16, false, VEC>& map, F4&& four, F1&& one)
 {
-    extern __shared__ float s_add[]; // [kBackwardWarps, E]: the chosen experts' part
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_wait();
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kBackwardWarps + warp;
-    if (t >= a.r.num_tokens)
-        return;
-    const int E = a.r.num_experts, K = a.r.num_topk;
-    const bool softmax = a.r.score == EP_SCORE_SOFTMAX;
-    const RowMap<NPL, BF16, false> map(a.r, lane, vec);
-    using Map = RowMap<NPL, BF16, false>;
-    float* add = s_add + static_cast<size_t>(warp) * E;
-
-    float d[NPL];
+    using Map = RowMap<NPL, BF16, false, VEC>;
+    if (VEC) {
 #pragma unroll
-    for (int j = 0; j < NPL; ++j)
-        d[j] = 0.0f;
-    const bool on = a.token_mask == nullptr || __ldg(a.token_mask + t) != 0;
-    float v[NPL];
-    float m = kNegInf;
-    if (on) {
-        load_row(v, a.logits, t, map);
-        m = row_max(v);
-    }
-    if (m > kNegInf) {
-        // softmax of the row
-        float p[NPL];
-        float z = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) {
-            p[j] = v[j] > kNegInf ? __expf(v[j] - m) : 0.0f;
-            z += p[j];
-        }
-        z = warp_sum(z);
-        const float inv_z = 1.0f / z;
+        for (int j = 0; j < NPL; j += 4)
+            if (map.holds(j))
+                four(j, map.e0 + Map::offset(j));
+    } else {
 #pragma unroll
         for (int j = 0; j < NPL; ++j)
-            p[j] *= inv_z;
+            if (map.holds(j))
+                one(j, map.e0 + Map::offset(j));
+    }
+}
 
-        if (a.d_topk_weights != nullptr) {
-            // lane k: slot k's expert, logit and gradient
-            int64_t e = -1;
-            float l = kNegInf, g = 0.0f;
-            if (lane < K) {
-                e = __ldg(a.topk_idx + t * K + lane);
-                if (e >= 0 && e < E)
-                    l = clean_logit(load_logit<BF16>(a.logits, t * E + e));
-            }
-            const bool got = l > kNegInf;
-            if (got)
-                g = a.r.scale * __ldg(a.d_topk_weights + t * K + lane);
-            float part = 0.0f; // what slot k adds at its expert
-            float through = 0.0f; // softmax without normalize: sum of g p, for the whole row
-            if (a.r.normalize != 0) {
-                const float lm = warp_max(l);
-                const bool tail = lm < kSigmoidTail;
-                float w = got ? (softmax || tail ? expf(l - lm) : sigmoid(l)) : 0.0f;
-                const float total = warp_sum(w);
-                w = got ? w / total : 0.0f;
-                const float mean = warp_sum(g * w);
-                part = w * (g - mean);
-                if (!softmax && got)
-                    part *= 1.0f / (1.0f + expf(l)); // 1 - s
-            } else if (softmax) {
-                part = got ? g * (expf(l - m) * inv_z) : 0.0f;
-                through = warp_sum(part);
-            } else if (got) {
-                part = g * sigmoid(l) * (1.0f / (1.0f + expf(l)));
-            }
-#pragma unroll
-            for (int j = 0; j < NPL; ++j)
-                if (map.holds(j))
-                    add[map.e0 + map.offset(j)] = 0.0f;
-            __syncwarp();
-            // slots of one expert (a caller's own ids) are added in slot order
-            const uint32_t same = __match_any_sync(kFullMask, got ? static_cast<int>(e) : -1 - lane);
-            if (__all_sync(kFullMask, __popc(same) == 1)) {
-                if (got)
-                    add[e] = part;
-            } else {
-                for (int k = 0; k < K; ++k) {
-                    if (lane == k && got)
-                        add[e] += part;
-                    __syncwarp();
-                }
-            }
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < NPL; ++j)
-                if (map.holds(j))
-                    d[j] = add[map.e0 + map.offset(j)] - p[j] * through;
+// A warp has `run` consecutive tokens: the next one's row, mask, ids and
+// gradients are on their way while one is worked on, and the counts of a
+// sequence stay in registers until its last token.
+template <int NPL, bool BF16, bool VEC>
+__global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(RouterBackwardLaunch a, int run)
+{
+    extern __shared__ __align__(16) float s_add[]; // [kBackwardWarps, E]: the chosen experts' part
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int E = a.r.num_experts, K = a.r.num_topk;
+    const bool softmax = a.r.score == EP_SCORE_SOFTMAX;
+    const RowMap<NPL, BF16, false, VEC> map(a.r, lane);
+    using Map = RowMap<NPL, BF16, false, VEC>;
+    float* add = s_add + static_cast<size_t>(warp) * E;
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * kBackwardWarps + warp) * run;
+    pdl_wait();
+    if (first >= a.r.num_tokens)
+        return;
+    const int begin = static_cast<int>(first), end = static_cast<int>(min(first + run, static_cast<int64_t>(a.r.num_tokens)));
+    RawRow<NPL, BF16, false, VEC> raw;
+    int64_t e_next = -1;
+    float g_next = 0.0f;
+    bool on_next = false;
+    const auto load = [&](int t) {
+        const bool in = t < end;
+        on_next = in && (a.token_mask == nullptr || __ldg(a.token_mask + t) != 0);
+        raw.load(a.logits, t, map, in);
+        if (a.d_topk_weights != nullptr && in && lane < K) {
+            e_next = __ldg(a.topk_idx + static_cast<int64_t>(t) * K + lane);
+            g_next = __ldg(a.d_topk_weights + static_cast<int64_t>(t) * K + lane);
         }
+    };
+    load(begin);
+    // the sequence at hand: its end, its losses' gradients over its tokens, its counts
+    int seq_end = begin;
+    float gb = 0.0f, gz = 0.0f, cnt[NPL];
+    const auto enter = [&](int t) {
+        const int s = find_seq(a.seq_offsets, a.num_seqs, t, lane);
+        const int n = s >= 0 ? __ldg(a.seq_tokens + s) : 0;
+        // (a sequence that does not hold t has no tokens here; look again at the next one)
+        seq_end = a.seq_offsets == nullptr ? a.r.num_tokens : (s >= 0 ? max(__ldg(a.seq_offsets + s + 1), t + 1) : t + 1);
+        gb = gz = 0.0f;
+        if (s < 0)
+            return;
+        const float nf = static_cast<float>(max(n, 1)); // (no token of a sequence with n = 0 gets here)
+        gb = __ldg(a.d_losses + 2 * s) * (static_cast<float>(E) / (static_cast<float>(K) * nf)) / nf;
+        gz = __ldg(a.d_losses + 2 * s + 1) * 2.0f / nf;
+        const int32_t* from = a.counts + static_cast<int64_t>(s) * E;
+        each_expert<NPL, BF16, VEC>(
+            map,
+            [&](int j, int e) {
+                const int4 c = __ldg(reinterpret_cast<const int4*>(from + e));
+                cnt[j] = static_cast<float>(c.x);
+                cnt[(j + 1) % NPL] = static_cast<float>(c.y);
+                cnt[(j + 2) % NPL] = static_cast<float>(c.z);
+                cnt[(j + 3) % NPL] = static_cast<float>(c.w);
+            },
+            [&](int j, int e) { cnt[j] = static_cast<float>(__ldg(from + e)); });
+    };
+#pragma unroll
+    for (int j = 0; j < NPL; ++j)
+        cnt[j] = 0.0f;
 
-        if (a.d_losses != nullptr) {
-            const int s = find_seq(a.seq_offsets, a.num_seqs, static_cast<int>(t), lane);
-            const int n = s >= 0 ? __ldg(a.seq_tokens + s) : 0;
-            if (n > 0) {
-                const float nf = static_cast<float>(n);
-                const float gb = __ldg(a.d_losses + 2 * s) * (static_cast<float>(E) / (static_cast<float>(K) * nf)) / nf;
-                const float gz = __ldg(a.d_losses + 2 * s + 1) * 2.0f * (m + logf(z)) / nf;
-                const int32_t* cnt = a.counts + static_cast<int64_t>(s) * E + map.e0;
-                float c[NPL], q[NPL];
+    if (a.d_losses != nullptr)
+        enter(begin);
+    for (int t = begin; t < end; ++t) {
+        float v[NPL], d[NPL];
+        const int64_t e = e_next;
+        float g = g_next;
+        const bool on = on_next;
+        float l = kNegInf; // lane k: slot k's logit
+        if (on && lane < K && e >= 0 && e < E)
+            l = clean_logit(load_logit<BF16>(a.logits, static_cast<int64_t>(t) * E + e));
+        raw.take(v);
+        load(t + 1);
+#pragma unroll
+        for (int j = 0; j < NPL; ++j)
+            d[j] = 0.0f;
+        const float m = on ? row_max(v) : kNegInf;
+        if (m > kNegInf) {
+            // softmax of the row
+            float p[NPL];
+            float z = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) {
+                p[j] = __expf(v[j] - m); // 0 for -inf
+                z += p[j];
+            }
+            z = warp_sum(z);
+            const float inv_z = 1.0f / z;
+#pragma unroll
+            for (int j = 0; j < NPL; ++j)
+                p[j] *= inv_z;
+
+            if (a.d_topk_weights != nullptr) {
+                const bool got = l > kNegInf;
+                g = got ? a.r.scale * g : 0.0f;
+                float part = 0.0f;    // what slot k adds at its expert
+                float through = 0.0f; // softmax without normalize: sum of g p, for the whole row
+                if (a.r.normalize != 0) {
+                    const float lm = warp_max(l);
+                    const bool tail = lm < kSigmoidTail;
+                    float w = got ? (softmax || tail ? expf(l - lm) : sigmoid(l)) : 0.0f;
+                    const float total = warp_sum(w);
+                    w = got ? w / total : 0.0f;
+                    const float mean = warp_sum(g * w);
+                    part = w * (g - mean);
+                    if (!softmax && got)
+                        part *= 1.0f / (1.0f + expf(l)); // 1 - s
+                } else if (softmax) {
+                    part = got ? g * (expf(l - m) * inv_z) : 0.0f;
+                    through = warp_sum(part);
+                } else if (got) {
+                    part = g * sigmoid(l) * (1.0f / (1.0f + expf(l)));
+                }
+                each_expert<NPL, BF16, VEC>(
+                    map, [&](int, int x) { *reinterpret_cast<float4*>(add + x) = make_float4(0.0f, 0.0f, 0.0f, 0.0f); },
+                    [&](int, int x) { add[x] = 0.0f; });
+                __syncwarp();
+                // slots of one expert (a caller's own ids) are added in slot order
+                const uint32_t same = __match_any_sync(kFullMask, got ? static_cast<int>(e) : -1 - lane);
+                if (__all_sync(kFullMask, __popc(same) == 1)) {
+                    if (got)
+                        add[e] = part;
+                } else {
+                    for (int k = 0; k < K; ++k) {
+                        if (lane == k && got)
+                            add[e] += part;
+                        __syncwarp();
+                    }
+                }
+                __syncwarp();
+                each_expert<NPL, BF16, VEC>(
+                    map,
+                    [&](int j, int x) {
+                        const float4 f = *reinterpret_cast<const float4*>(add + x);
+                        d[j] = f.x;
+                        d[(j + 1) % NPL] = f.y;
+                        d[(j + 2) % NPL] = f.z;
+                        d[(j + 3) % NPL] = f.w;
+                    },
+                    [&](int j, int x) { d[j] = add[x]; });
+                __syncwarp(); // read before the next token's zeros
 #pragma unroll
                 for (int j = 0; j < NPL; ++j)
-                    c[j] = map.holds(j) ? static_cast<float>(__ldg(cnt + map.offset(j))) : 0.0f;
-                float rest[NPL]; // ds / dl = s * rest
-#pragma unroll
-                for (int j = 0; j < NPL; ++j)
-                    rest[j] = 1.0f;
+                    d[j] -= p[j] * through;
+            }
+
+            if (a.d_losses != nullptr) {
+                if (t >= seq_end)
+                    enter(t);
+                const float gzt = gz * (m + logf(z));
                 if (softmax || m < kSigmoidTail) { // there 1 - s is 1 too
+                    float mean = 0.0f;
 #pragma unroll
                     for (int j = 0; j < NPL; ++j)
-                        q[j] = p[j];
+                        mean += cnt[j] * p[j];
+                    const float flat = gzt - gb * warp_sum(mean);
+#pragma unroll
+                    for (int j = 0; j < NPL; ++j)
+                        d[j] += p[j] * (gb * cnt[j] + flat);
                 } else {
+                    float q[NPL];
                     float total = 0.0f;
 #pragma unroll
                     for (int j = 0; j < NPL; ++j) {
                         q[j] = v[j] > kNegInf ? fast_sigmoid(v[j]) : 0.0f;
-                        rest[j] = fast_sigmoid(-v[j]);
                         total += q[j];
                     }
                     const float inv = 1.0f / warp_sum(total);
+                    float mean = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < NPL; ++j)
+                    for (int j = 0; j < NPL; ++j) {
                         q[j] *= inv;
+                        mean += cnt[j] * q[j];
+                    }
+                    mean = warp_sum(mean);
+#pragma unroll
+                    for (int j = 0; j < NPL; ++j) // 1 - s, kept exact where s is near 1
+                        d[j] += gb * q[j] * fast_sigmoid(-v[j]) * (cnt[j] - mean) + gzt * p[j];
                 }
-                float mean = 0.0f;
-#pragma unroll
-                for (int j = 0; j < NPL; ++j)
-                    mean += c[j] * q[j];
-                mean = warp_sum(mean);
-#pragma unroll
-                for (int j = 0; j < NPL; ++j)
-                    d[j] += gb * q[j] * rest[j] * (c[j] - mean) + gz * p[j];
             }
         }
-    }
-    const int64_t at = t * E + map.e0;
-    if (Map::kVec == Map::kFull && vec) {
+        const int64_t at = static_cast<int64_t>(t) * E + map.e0;
+        if (VEC) {
 #pragma unroll
-        for (int j = 0; j < NPL; j += Map::kVec) {
-            if (!map.holds(j))
-                continue;
-            uint4 w;
-            if (BF16) {
-                w = make_uint4(pack_bf16x2(d[j], d[(j + 1) % NPL]), pack_bf16x2(d[(j + 2) % NPL], d[(j + 3) % NPL]),
-                               pack_bf16x2(d[(j + 4) % NPL], d[(j + 5) % NPL]),
-                               pack_bf16x2(d[(j + 6) % NPL], d[(j + 7) % NPL]));
-                st_v4(static_cast<uint16_t*>(a.d_logits) + at + map.offset(j), w);
-            } else {
-                w = make_uint4(__float_as_uint(d[j]), __float_as_uint(d[(j + 1) % NPL]),
-                               __float_as_uint(d[(j + 2) % NPL]), __float_as_uint(d[(j + 3) % NPL]));
-                st_v4(static_cast<float*>(a.d_logits) + at + map.offset(j), w);
+            for (int j = 0; j < NPL; j += Map::kFull) {
+                if (!map.holds(j))
+                    continue;
+                uint4 w;
+                if (BF16) {
+                    w = make_uint4(pack_bf16x2(d[j], d[(j + 1) % NPL]), pack_bf16x2(d[(j + 2) % NPL], d[(j + 3) % NPL]),
+                                   pack_bf16x2(d[(j + 4) % NPL], d[(j + 5) % NPL]),
+                                   pack_bf16x2(d[(j + 6) % NPL], d[(j + 7) % NPL]));
+                    st_v4(static_cast<uint16_t*>(a.d_logits) + at + Map::offset(j), w);
+                } else {
+                    w = make_uint4(__float_as_uint(d[j]), __float_as_uint(d[(j + 1) % NPL]),
+                                   __float_as_uint(d[(j + 2) % NPL]), __float_as_uint(d[(j + 3) % NPL]));
+                    st_v4(static_cast<float*>(a.d_logits) + at + Map::offset(j), w);
+                }
             }
-        }
-    } else {
+        } else {
 #pragma unroll
-        for (int j = 0; j < NPL; ++j) {
-            if (!map.holds(j))
-                continue;
-            if (BF16)
-                static_cast<uint16_t*>(a.d_logits)[at + map.offset(j)] = static_cast<uint16_t>(pack_bf16x2(d[j], 0.0f));
-            else
-                static_cast<float*>(a.d_logits)[at + map.offset(j)] = d[j];
+            for (int j = 0; j < NPL; ++j) {
+                if (!map.holds(j))
+                    continue;
+                if (BF16)
+                    static_cast<uint16_t*>(a.d_logits)[at + Map::offset(j)] =
+                        static_cast<uint16_t>(pack_bf16x2(d[j], 0.0f));
+                else
+                    static_cast<float*>(a.d_logits)[at + Map::offset(j)] = d[j];
+            }
         }
     }
 }
 
 // ----------------------------------------------------------------- launches
-// <<<grid, block, smem, stream>>> as a programmatic dependent: the launch is
-// ready when the kernel before it ends, and every kernel here waits (pdl_wait)
-// before it reads what that one may have written.
+// A launch as a programmatic dependent, in clusters of `cluster`: it is ready
+// when the kernel before it ends, and every kernel here waits (pdl_wait) before
+// it reads what that one may have written.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_after(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
-                         Args... args)
+cudaError_t launch_after(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, int cluster,
+                         cudaStream_t stream, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Calls f<NPL, BF16>(vec) for the smallest NPL that holds a lane's logits; vec:
-// by 16-byte loads, where E is a multiple of that many logits and both arrays
-// start on 16 bytes.
+// Calls f<NPL, BF16, VEC> for the smallest NPL that holds a lane's logits; VEC:
+// by 16-byte loads, where E is a multiple of that many logits and the arrays
+// (`align`: their addresses, or'ed) start on 16 bytes.
 template <typename F>
-cudaError_t with_row_shape(const ep_router_desc_t& r, const void* in, const void* out, F&& f)
+cudaError_t with_row_shape(const ep_router_desc_t& r, uintptr_t align, F&& f)
 {
     const bool bf16 = r.logits_dtype == EP_BF16;
     const int full = bf16 ? 8 : 4;
-    const bool fits = ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
     int need = (r.num_experts + 31) / 32;
-    bool vec = fits && r.num_experts % full == 0;
+    bool vec = (align & 15u) == 0 && r.num_experts % full == 0;
     if (r.num_groups > 1) { // runs of c, each of whole vectors
         need = groups_run(r);
         vec = vec && need >= full && (need & (need - 1)) == 0 && r.num_experts == 32 * need;
@@ -1087,9 +1196,14 @@ cudaError_t with_row_shape(const ep_router_desc_t& r, const void* in, const void
         need = (r.num_experts / full + 31) / 32 * full;
     }
 #define EP_ROW_SHAPE(N)                                                                                               \
-    if (need <= N)                                                                                                    \
-        return bf16 ? f(std::integral_constant<int, N>{}, std::true_type{}, vec)                                      \
-                    : f(std::integral_constant<int, N>{}, std::false_type{}, vec)
+    if (need <= N) {                                                                                                  \
+        using Npl = std::integral_constant<int, N>;                                                                   \
+        if (bf16)                                                                                                     \
+            return vec ? f(Npl{}, std::true_type{}, std::integral_constant<bool, (N >= 8)>{})                         \
+                       : f(Npl{}, std::true_type{}, std::false_type{});                                               \
+        return vec ? f(Npl{}, std::false_type{}, std::integral_constant<bool, (N >= 4)>{})                            \
+                   : f(Npl{}, std::false_type{}, std::false_type{});                                                  \
+    }
     EP_ROW_SHAPE(1);
     EP_ROW_SHAPE(2);
     EP_ROW_SHAPE(4);
@@ -1100,18 +1214,24 @@ cudaError_t with_row_shape(const ep_router_desc_t& r, const void* in, const void
     return cudaErrorInvalidValue;
 }
 
+uintptr_t address(const void* p)
+{
+    return reinterpret_cast<uintptr_t>(p);
+}
+
 } // namespace
 
 cudaError_t launch_router_topk(const RouterTopkLaunch& a, cudaStream_t stream)
 {
     if (a.r.num_tokens == 0)
         return cudaSuccess;
-    return with_row_shape(a.r, a.logits, nullptr, [&](auto npl, auto bf16, bool vec) {
+    return with_row_shape(a.r, address(a.logits), [&](auto npl, auto bf16, auto vec) {
         const bool grouped = a.r.num_groups > 1;
         const size_t smem = grouped || a.bias != nullptr ? sizeof(double) * kTopkWarps * a.r.num_experts : 0;
         const unsigned grid = (a.r.num_tokens + kTopkWarps - 1) / kTopkWarps;
-        return launch_after(grouped ? router_topk_kernel<npl(), bf16(), true> : router_topk_kernel<npl(), bf16(), false>,
-                            grid, kTopkWarps * 32, smem, stream, a, vec);
+        return launch_after(grouped ? router_topk_kernel<npl(), bf16(), true, vec()>
+                                    : router_topk_kernel<npl(), bf16(), false, vec()>,
+                            grid, kTopkWarps * 32, smem, 1, stream, a);
     });
 }
 
@@ -1125,26 +1245,23 @@ cudaError_t launch_balance_loss(const BalanceLaunch& a, cudaStream_t stream)
 {
     ep_router_desc_t r = a.r;
     r.num_groups = 1; // the groups are the choice's alone
-    return with_row_shape(r, a.logits, nullptr, [&](auto npl, auto bf16, bool vec) {
-        const auto kernel = balance_kernel<npl(), bf16()>;
+    return with_row_shape(r, address(a.logits), [&](auto npl, auto bf16, auto vec) {
+        const auto kernel = balance_kernel<npl(), bf16(), vec()>;
         const size_t smem = sizeof(float) * 2 * kBalanceWarps * a.r.num_experts;
         if (smem > 48 * 1024) {
-            cudaError_t e =
+            const cudaError_t e =
                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(balance_finish_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
             if (e != cudaSuccess)
                 return e;
         }
         const int T = a.r.num_tokens, chunk = chunk_tokens(std::max(T, 1));
         const unsigned grid = static_cast<unsigned>(most_chunks(T, a.num_seqs));
         const bool finish = T > chunk; // else no sequence has a second chunk
-        const cudaError_t e = launch_after(kernel, grid, kBalanceThreads, smem, stream, a, chunk, vec, finish);
+        const cudaError_t e = launch_after(kernel, grid, kBalanceThreads, smem, 1, stream, a, chunk, finish);
         if (e != cudaSuccess || !finish)
             return e;
-        return launch_after(balance_finish_kernel, static_cast<unsigned>(a.num_seqs), kBalanceThreads, smem, stream, a,
-                            chunk);
+        return launch_after(balance_finish_kernel, static_cast<unsigned>(a.num_seqs) * kFinishCluster, kBalanceThreads, 0,
+                            kFinishCluster, stream, a, chunk);
     });
 }
 
@@ -1154,10 +1271,12 @@ cudaError_t launch_router_backward(const RouterBackwardLaunch& a, cudaStream_t s
         return cudaSuccess;
     ep_router_desc_t r = a.r;
     r.num_groups = 1;
-    return with_row_shape(r, a.logits, a.d_logits, [&](auto npl, auto bf16, bool vec) {
+    const uintptr_t align = address(a.logits) | address(a.d_logits) | (a.d_losses != nullptr ? address(a.counts) : 0);
+    return with_row_shape(r, align, [&](auto npl, auto bf16, auto vec) {
         const size_t smem = sizeof(float) * kBackwardWarps * a.r.num_experts;
-        const unsigned grid = (a.r.num_tokens + kBackwardWarps - 1) / kBackwardWarps;
-        return launch_after(router_backward_kernel<npl(), bf16()>, grid, kBackwardWarps * 32, smem, stream, a, vec);
+        const int run = std::max(1, std::min(kMostRun, a.r.num_tokens / kBackwardFill));
+        const unsigned grid = (a.r.num_tokens + kBackwardWarps * run - 1) / (kBackwardWarps * run);
+        return launch_after(router_backward_kernel<npl(), bf16(), vec()>, grid, kBackwardWarps * 32, smem, 1, stream, a, run);
     });
 }
 
