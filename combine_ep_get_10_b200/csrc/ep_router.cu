@@ -266,6 +266,53 @@ __device__ __noinline__ int choose_wide(const RouterTopkLaunch& a, int64_t row, 
     return chosen;
 }
 
+// Does the lane's group stay in the choice: in fp64, for the rows whose groups'
+// fp32 values lie too close together.
+template <int NPL, bool BF16, bool VEC>
+__device__ __noinline__ bool stays_wide(const RouterTopkLaunch& a, int64_t row, int lane)
+{
+    const RowMap<NPL, BF16, true, VEC> map(a.r, lane);
+    const int G = a.r.num_groups, bits = 5 - (31 - __clz(G));
+    const bool softmax = a.r.score == EP_SCORE_SOFTMAX;
+    const double none = -INFINITY;
+    RawRow<NPL, BF16, true, VEC> raw;
+    float v[NPL];
+    raw.load(a.logits, row, map, true);
+    raw.take(v);
+    double m = 0.0, z = 1.0;
+    if (softmax) {
+        m = fmaxf(row_max(v), -FLT_MAX);
+        z = 0.0;
+#pragma unroll 4
+        for (int j = 0; j < NPL; ++j)
+            z += exp(v[j] - m);
+        for (int d = 16; d >= 1; d >>= 1)
+            z += __shfl_xor_sync(kFullMask, z, d);
+    }
+    double t1 = none, t2 = none;
+#pragma unroll 4
+    for (int j = 0; j < NPL; ++j) {
+        double c = softmax ? exp(v[j] - m) / z : 1.0 / (1.0 + exp(-static_cast<double>(v[j])));
+        if (a.bias != nullptr && map.holds(j))
+            c += __ldg(a.bias + map.e0 + map.offset(j));
+        c = v[j] > kNegInf && c > none ? c : none;
+        t2 = fmax(t2, fmin(t1, c));
+        t1 = fmax(t1, c);
+    }
+    for (int d = (1 << bits) >> 1; d >= 1; d >>= 1) {
+        const double o1 = __shfl_xor_sync(kFullMask, t1, d), o2 = __shfl_xor_sync(kFullMask, t2, d);
+        t2 = fmax(fmin(t1, o1), fmax(t2, o2));
+        t1 = fmax(t1, o1);
+    }
+    const double value = a.r.group_top == 2 && t2 > none ? t1 + t2 : t1;
+    int before = 0;
+    for (int g = 0; g < G; ++g) {
+        const double o = __shfl_sync(kFullMask, value, g << bits);
+        before += (o > value || (o == value && g < lane >> bits)) ? 1 : 0;
+    }
+    return before < a.r.topk_groups;
+}
+
 // Lane i of the first `count` gives its value and id: the lane's place in
 // descending order, equal values by id.
 template <typename T>
@@ -298,13 +345,18 @@ __device__ __forceinline__ int place_in_order(T value, int e, int count)
 //            (|l - max| exp(l - max) <= 0.37), 2 ulp of ex2, the sum of E terms
 //            NPL + 5 roundings and the same errors inside (the mean of |l -
 //            max| under p is at most log E <= 7), the quotient: < 64 * 2^-24 / Z;
-// a row whose order those errors could change is decided in fp64: the gathered
-// values alone where only their order is open, else (a value below t, or a
-// group, could come in) the whole row.  Values that are equal because logit
-// and bias are equal need no second look.
-template <int NPL, bool BF16, bool GROUPED, bool VEC>
+// a row whose order those errors could change is decided in fp64: the groups,
+// the gathered values alone where only their order is open, or (a value below t
+// could come in) the whole row.  Such rows are few and slow, and a kernel lasts
+// as long as its slowest row: at 4096 x 256 in 8 groups 10.5 us where every such
+// row is done whole.  Values that are equal because logit and bias are equal
+// need no second look.
+enum class Choice { kLogit, kScore, kGrouped }; // by the logits, by scores, by scores in groups
+
+template <int NPL, bool BF16, Choice CHOICE, bool VEC>
 __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopkLaunch a)
 {
+    constexpr bool GROUPED = CHOICE == Choice::kGrouped, by_logit = CHOICE == Choice::kLogit;
     extern __shared__ double s_wide[];
     __shared__ float2 s_list[kTopkWarps][2][32]; // (value, expert): as gathered, in order
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -326,7 +378,6 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
         return;
     }
     const bool softmax = a.r.score == EP_SCORE_SOFTMAX;
-    const bool by_logit = !GROUPED && a.bias == nullptr;
     float c[NPL]; // the values chosen by; -inf: not to be chosen
     raw.take(c);
 
@@ -341,7 +392,6 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
     }
     const float es = softmax ? 4e-6f / z : 5e-7f;
     const auto err = [es](float x) { return es + 1.3e-7f * fabsf(x); };
-    bool sure = true; // no group's place is open
     if (!by_logit) {
         const float inv_z = 1.0f / z;
 #pragma unroll
@@ -372,10 +422,11 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
                 const float o = __shfl_sync(kFullMask, value, g << bits);
                 before += (o > value || (o == value && g < mine)) ? 1 : 0;
             }
-            const bool stay = before < a.r.topk_groups;
+            bool stay = before < a.r.topk_groups;
             const float low = warp_min(stay ? value - ge : INFINITY);
             const float high = warp_max(stay || value == kNegInf ? kNegInf : value + ge);
-            sure = high == kNegInf || low > high;
+            if (high > kNegInf && low <= high) // a group's place is open
+                stay = stays_wide<NPL, BF16, VEC>(a, t, lane);
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
                 c[j] = stay ? c[j] : kNegInf;
@@ -477,14 +528,14 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
                                                      my_c - err(my_c) > n + err(n));
         // what was not gathered is below `least`
         const bool closed = all || count > 32 || last - err(last) > least + err(least);
-        if (!sure || !closed || (!order && count > 32)) {
+        if (!closed || (!order && count > 32)) {
             my_idx = choose_wide<BF16>(a, t, s_wide + static_cast<size_t>(warp) * E, lane);
             l = my_idx >= 0 ? clean_logit(load_logit<BF16>(a.logits, t * E + my_idx)) : 0.0f;
         } else if (!order) {
             double sum = 1.0;
             if (softmax) {
                 sum = 0.0;
-#pragma unroll 1
+#pragma unroll 4
                 for (int e = lane; e < E; e += 32)
                     sum += exp(static_cast<double>(clean_logit(load_logit<BF16>(a.logits, t * E + e))) - m);
                 for (int d = 16; d >= 1; d >>= 1)
@@ -1229,8 +1280,9 @@ cudaError_t launch_router_topk(const RouterTopkLaunch& a, cudaStream_t stream)
         const bool grouped = a.r.num_groups > 1;
         const size_t smem = grouped || a.bias != nullptr ? sizeof(double) * kTopkWarps * a.r.num_experts : 0;
         const unsigned grid = (a.r.num_tokens + kTopkWarps - 1) / kTopkWarps;
-        return launch_after(grouped ? router_topk_kernel<npl(), bf16(), true, vec()>
-                                    : router_topk_kernel<npl(), bf16(), false, vec()>,
+        return launch_after(grouped             ? router_topk_kernel<npl(), bf16(), Choice::kGrouped, vec()>
+                            : a.bias != nullptr ? router_topk_kernel<npl(), bf16(), Choice::kScore, vec()>
+                                                : router_topk_kernel<npl(), bf16(), Choice::kLogit, vec()>,
                             grid, kTopkWarps * 32, smem, 1, stream, a);
     });
 }
