@@ -197,7 +197,7 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:  # the current device's current stream, without building a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -573,28 +573,31 @@ def ep_combine_peers(routing: Routing, layout: Layout, rank_layout: RankLayout, 
 
 
 # ------------------------------------------------------------------ router
-def _arg(name: str, t, dtype, shape: tuple, device=None):
+def _arg(name: str, t, dtype, shape: tuple, index=None):
     """Address of a dense tensor argument of the given type and shape (None
-    stays None); `device`: the device it has to be on."""
+    stays None); `index`: the device it has to be on."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and (index is None or t.get_device() == index):
+        return t.data_ptr()
     if t.dtype != dtype or t.shape != shape:
         raise TypeError("%s must be a %s tensor of shape %s, got %s %s"
                         % (name, dtype, shape, t.dtype, tuple(t.shape)))
     if not t.is_contiguous():
         raise ValueError("the C ABI takes dense row-major tensors; %s is a strided view" % name)
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, the other tensors are on %s" % (name, t.device, device))
-    return t.data_ptr()
+    raise ValueError("%s is on %s, the other tensors are on cuda:%d" % (name, t.device, index))
 
 
-def _on_current_device(device) -> None:
-    """A call runs on the current device and its current stream."""
-    if device.type != "cuda":
-        raise ValueError("the tensors are on %s; the library takes CUDA tensors" % (device,))
-    if device.index != torch.cuda.current_device():
+def _device_of(t) -> int:
+    """The tensor's device, which has to be the current one: a call runs on the
+    current device and its current stream."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("the tensors are on %s; the library takes CUDA tensors" % (t.device,))
+    if index != torch._C._cuda_getDevice():
         raise ValueError("the tensors are on %s, the current device is cuda:%d (use torch.cuda.device)"
-                         % (device, torch.cuda.current_device()))
+                         % (t.device, torch.cuda.current_device()))
+    return index
 
 
 class Router:
@@ -606,72 +609,98 @@ class Router:
         self._fields = (self.num_experts, self.num_topk, int(num_groups), int(topk_groups), int(group_top),
                         1 if normalize else 0, float(scale))
         self._score = int(score)
-        self._last = (None, None, None)  # the descriptor of the last number of tokens and type
+        self._last = (None, None, None, None)  # the descriptor of the last number of tokens and type
 
     def desc(self, num_tokens: int, dtype) -> RouterDesc:
         return RouterDesc(self._score, EP_BF16 if dtype == torch.bfloat16 else EP_FP32, num_tokens, *self._fields)
 
-    def of(self, logits: torch.Tensor) -> RouterDesc:
-        """The C descriptor for these logits, after checking them."""
-        if logits.dtype not in (torch.bfloat16, torch.float32) or logits.dim() != 2 or \
-                logits.shape[1] != self.num_experts:
+    def of(self, logits: torch.Tensor):
+        """(number of tokens, device, the C descriptor by reference) for these
+        logits, after checking them."""
+        shape, dtype = logits.shape, logits.dtype
+        if (dtype is not torch.bfloat16 and dtype is not torch.float32) or len(shape) != 2 or \
+                shape[1] != self.num_experts:
             raise TypeError("logits must be a bfloat16 or float32 tensor of shape (T, %d), got %s %s"
-                            % (self.num_experts, logits.dtype, tuple(logits.shape)))
+                            % (self.num_experts, dtype, tuple(shape)))
         if not logits.is_contiguous():
             raise ValueError("the C ABI takes dense row-major tensors; logits is a strided view")
-        _on_current_device(logits.device)
-        T, dtype, d = self._last
-        if T != logits.shape[0] or dtype != logits.dtype:
-            d = self.desc(logits.shape[0], logits.dtype)
-            self._last = (logits.shape[0], logits.dtype, d)
-        return d
+        index = _device_of(logits)
+        T, last, _, ref = self._last
+        if T != shape[0] or last is not dtype:
+            T = shape[0]
+            d = self.desc(T, dtype)
+            ref = ctypes.byref(d)
+            self._last = (T, dtype, d, ref)
+        return T, index, ref
 
 
 def ep_router_topk(logits: torch.Tensor, router: Router, topk_idx: torch.Tensor, topk_weights: torch.Tensor, *,
                    bias=None, token_mask=None, stream=None) -> None:
     """logits [T, E] (bf16 or fp32) -> topk_idx int64 [T, K], topk_weights fp32 [T, K]."""
-    d, dev = router.of(logits), logits.device
-    T, E, K = d.num_tokens, d.num_experts, d.num_topk
-    _check(lib().ep_router_topk(ctypes.byref(d), logits.data_ptr(), _arg("bias", bias, torch.float32, (E,), dev),
-                                _arg("token_mask", token_mask, torch.uint8, (T,), dev),
-                                _arg("topk_idx", topk_idx, torch.int64, (T, K), dev),
-                                _arg("topk_weights", topk_weights, torch.float32, (T, K), dev), _stream(stream)),
+    T, dev, ref = router.of(logits)
+    TK = (T, router.num_topk)
+    _check(lib().ep_router_topk(ref, logits.data_ptr(),
+                                None if bias is None else _arg("bias", bias, torch.float32, (router.num_experts,), dev),
+                                None if token_mask is None else _arg("token_mask", token_mask, torch.uint8, (T,), dev),
+                                _arg("topk_idx", topk_idx, torch.int64, TK, dev),
+                                _arg("topk_weights", topk_weights, torch.float32, TK, dev), _stream(stream)),
            "ep_router_topk")
 
 
 class BalanceStats:
     """Device buffers of ep_balance_loss for up to num_tokens tokens in
     num_seqs sequences: losses fp32 [S, 2] (balance, z), counts int32 [S, E],
-    seq_tokens int32 [S], mean_scores fp32 [S, E], and the workspace."""
+    seq_tokens int32 [S], mean_scores fp32 [S, E], and the workspace.  They are
+    checked, and their addresses taken, when they are set."""
 
     def __init__(self, router: Router, num_tokens: int, num_seqs: int = 1, device="cuda"):
         S, E = int(num_seqs), router.num_experts
-        self.num_seqs = S
         need = lib().ep_balance_workspace_bytes(ctypes.byref(router.desc(num_tokens, torch.float32)), S)
         if need == 0:
             raise EPError(EP_ERR_INVALID_ARG, "ep_balance_workspace_bytes")
-        self.losses = torch.empty((S, 2), dtype=torch.float32, device=device)
-        self.counts = torch.empty((S, E), dtype=torch.int32, device=device)
-        self.seq_tokens = torch.empty(S, dtype=torch.int32, device=device)
-        self.mean_scores = torch.empty((S, E), dtype=torch.float32, device=device)
-        self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        self.num_seqs, self.num_experts = S, E
+        self._shapes = {"losses": (torch.float32, (S, 2)), "counts": (torch.int32, (S, E)),
+                        "seq_tokens": (torch.int32, (S,)), "mean_scores": (torch.float32, (S, E)),
+                        "workspace": (torch.uint8, (need,))}
+        self._at = {}
+        for name, (dtype, shape) in self._shapes.items():
+            setattr(self, name, torch.empty(shape, dtype=dtype, device=device))
+
+    def __setattr__(self, name, value):
+        shapes = self.__dict__.get("_shapes", {})
+        if name in shapes:
+            dtype, shape = shapes[name]
+            if name == "workspace" and value.dim() == 1 and value.shape[0] >= shape[0]:
+                shape = tuple(value.shape)  # a larger one will do
+            self._at[name] = _arg(name, value, dtype, shape)
+            index = value.get_device()
+            if any(getattr(self, n).get_device() != index for n in shapes if n != name and n in self.__dict__):
+                index = -2  # not all on one device: no call takes them
+            object.__setattr__(self, "index", index)
+        object.__setattr__(self, name, value)
+
+    def at(self, router: Router, index: int) -> dict:
+        """The buffers' addresses, for a call of this router on this device."""
+        if self.index != index:
+            raise ValueError("the statistics' buffers are not on cuda:%d, where the logits are" % index)
+        if self.num_experts != router.num_experts:
+            raise ValueError("the statistics are of %d experts, the router has %d"
+                             % (self.num_experts, router.num_experts))
+        return self._at
 
 
 def ep_balance_loss(logits: torch.Tensor, router: Router, topk_idx: torch.Tensor, stats: BalanceStats, *,
                     token_mask=None, seq_offsets=None, stream=None) -> BalanceStats:
     """Balance and z losses and expert counts of each sequence, into `stats`.
     seq_offsets: int32 [S + 1], or None for one sequence of all tokens."""
-    d, dev = router.of(logits), logits.device
-    T, E, K, S = d.num_tokens, d.num_experts, d.num_topk, stats.num_seqs
-    _check(lib().ep_balance_loss(ctypes.byref(d), logits.data_ptr(), _arg("topk_idx", topk_idx, torch.int64, (T, K), dev),
-                                 _arg("token_mask", token_mask, torch.uint8, (T,), dev),
-                                 _arg("seq_offsets", seq_offsets, torch.int32, (S + 1,), dev), S,
-                                 _arg("losses", stats.losses, torch.float32, (S, 2), dev),
-                                 _arg("counts", stats.counts, torch.int32, (S, E), dev),
-                                 _arg("seq_tokens", stats.seq_tokens, torch.int32, (S,), dev),
-                                 _arg("mean_scores", stats.mean_scores, torch.float32, (S, E), dev),
-                                 stats.workspace.data_ptr(), stats.workspace.numel(), _stream(stream)),
-           "ep_balance_loss")
+    T, dev, ref = router.of(logits)
+    S, at = stats.num_seqs, stats.at(router, dev)
+    _check(lib().ep_balance_loss(
+        ref, logits.data_ptr(), _arg("topk_idx", topk_idx, torch.int64, (T, router.num_topk), dev),
+        None if token_mask is None else _arg("token_mask", token_mask, torch.uint8, (T,), dev),
+        None if seq_offsets is None else _arg("seq_offsets", seq_offsets, torch.int32, (S + 1,), dev), S,
+        at["losses"], at["counts"], at["seq_tokens"], at["mean_scores"], at["workspace"], stats.workspace.shape[0],
+        _stream(stream)), "ep_balance_loss")
     return stats
 
 
@@ -680,23 +709,21 @@ def ep_router_backward(logits: torch.Tensor, router: Router, topk_idx, d_logits:
                        seq_offsets=None, stream=None) -> None:
     """d_logits (the logits' type and shape) from d_topk_weights fp32 [T, K]
     and / or d_losses fp32 [S, 2] (with the `stats` of ep_balance_loss)."""
-    d, dev = router.of(logits), logits.device
-    T, E, K = d.num_tokens, d.num_experts, d.num_topk
-    if d_losses is not None and stats is None:
-        raise ValueError("d_losses needs the stats of ep_balance_loss")
-    S = stats.num_seqs if d_losses is not None else 1
-    counts = seq_tokens = offsets = None
+    T, dev, ref = router.of(logits)
+    TK = (T, router.num_topk)
+    S, counts, seq_tokens, offsets, dl = 1, None, None, None, None
     if d_losses is not None:
-        counts = _arg("counts", stats.counts, torch.int32, (S, E), dev)
-        seq_tokens = _arg("seq_tokens", stats.seq_tokens, torch.int32, (S,), dev)
-        offsets = _arg("seq_offsets", seq_offsets, torch.int32, (S + 1,), dev)
-    _check(lib().ep_router_backward(ctypes.byref(d), logits.data_ptr(),
-                                    _arg("topk_idx", topk_idx, torch.int64, (T, K), dev),
-                                    _arg("token_mask", token_mask, torch.uint8, (T,), dev),
-                                    _arg("d_topk_weights", d_topk_weights, torch.float32, (T, K), dev), offsets, S,
-                                    counts, seq_tokens, _arg("d_losses", d_losses, torch.float32, (S, 2), dev),
-                                    _arg("d_logits", d_logits, logits.dtype, (T, E), dev), _stream(stream)),
-           "ep_router_backward")
+        if stats is None:
+            raise ValueError("d_losses needs the stats of ep_balance_loss")
+        S, at = stats.num_seqs, stats.at(router, dev)
+        counts, seq_tokens = at["counts"], at["seq_tokens"]
+        offsets = None if seq_offsets is None else _arg("seq_offsets", seq_offsets, torch.int32, (S + 1,), dev)
+        dl = _arg("d_losses", d_losses, torch.float32, (S, 2), dev)
+    _check(lib().ep_router_backward(
+        ref, logits.data_ptr(), _arg("topk_idx", topk_idx, torch.int64, TK, dev),
+        None if token_mask is None else _arg("token_mask", token_mask, torch.uint8, (T,), dev),
+        _arg("d_topk_weights", d_topk_weights, torch.float32, TK, dev), offsets, S, counts, seq_tokens, dl,
+        _arg("d_logits", d_logits, logits.dtype, logits.shape, dev), _stream(stream)), "ep_router_backward")
 
 
 # ------------------------------------------------------ low-rank adapters
@@ -710,11 +737,12 @@ class Lora:
         E, r, hin = a.shape
         hout = b.shape[1]
         self.E, self.rank, self.hidden_in, self.hidden_out = E, r, hin, hout
-        self.device = a.device
+        self.index = a.get_device()
         self.a, self.b, self.scales = a, b, scales  # kept alive with the descriptor
         self.desc = LoraDesc(r, hin, hout, _arg("a", a, torch.bfloat16, (E, r, hin)),
-                             _arg("b", b, torch.bfloat16, (E, hout, r), a.device),
-                             _arg("scales", scales, torch.float32, (E,), a.device))
+                             _arg("b", b, torch.bfloat16, (E, hout, r), self.index),
+                             _arg("scales", scales, torch.float32, (E,), self.index))
+        self.ref = ctypes.byref(self.desc)
 
 
 def ep_row_tokens(routing: Routing, layout: Layout, row_token: torch.Tensor, *, mode=EP_LAYOUT_COMPACT,
@@ -727,23 +755,23 @@ def ep_row_tokens(routing: Routing, layout: Layout, row_token: torch.Tensor, *, 
            "ep_row_tokens")
 
 
-def _row_token(t, layout, device):
-    """Address of the row table.  An empty one has none: any other stands in,
-    so that the call still is the one in token order (0 rows are read)."""
-    return None if t is None else _arg("row_token", t, torch.int32, (t.shape[0],), device) or layout.desc.workspace
-
-
-def _lora_rows(routing: Routing, lora: Lora, first: torch.Tensor, h: torch.Tensor, row_token):
-    """(rows of the row buffer, rows of x / base / out), after checking them."""
-    _on_current_device(first.device)
+def _lora_rows(routing: Routing, layout: Layout, lora: Lora, first: torch.Tensor, h: torch.Tensor, row_token):
+    """(device, rows of the row buffer, rows of x / base / out, address of the
+    row table), after checking them."""
+    dev = _device_of(first)
     if routing.E != lora.E:
         raise ValueError("the routing names %d adapters, the factors are of %d" % (routing.E, lora.E))
-    if lora.device != first.device:
-        raise ValueError("the factors are on %s, the rows are on %s" % (lora.device, first.device))
-    if h.dim() != 2 or (row_token is not None and row_token.shape[0] < h.shape[0]):
-        raise ValueError("the fp32 row buffer has shape %s, row_token %d entries"
-                         % (tuple(h.shape), -1 if row_token is None else row_token.shape[0]))
-    return h.shape[0], routing.T if row_token is not None else h.shape[0]
+    if lora.index != dev:
+        raise ValueError("the factors are on another device than the rows, which are on cuda:%d" % dev)
+    rows = h.shape[0]
+    if row_token is None:
+        return dev, rows, rows, None
+    if row_token.dim() != 1 or row_token.shape[0] < rows:
+        raise ValueError("row_token has shape %s, the fp32 row buffer %s" % (tuple(row_token.shape), tuple(h.shape)))
+    # an empty table has no address: any other stands in, so that the call
+    # still is the one in token order (0 rows are read)
+    return dev, rows, routing.T, (_arg("row_token", row_token, torch.int32, row_token.shape, dev)
+                                  or layout.desc.workspace)
 
 
 def ep_lora(x: torch.Tensor, routing: Routing, layout: Layout, lora: Lora, out: torch.Tensor, h: torch.Tensor, *,
@@ -753,13 +781,13 @@ def ep_lora(x: torch.Tensor, routing: Routing, layout: Layout, lora: Lora, out: 
     the scaled products with the first factor.  With row_token (int32, at least
     num_rows entries) x, base and out are [T, ...] in token order, without it
     they are the num_rows dispatched rows.  base may be out itself."""
-    rows, n = _lora_rows(routing, lora, x, h, row_token)
-    dev, bf = x.device, torch.bfloat16
-    _check(lib().ep_lora(_arg("x", x, bf, (n, lora.hidden_in), dev), _arg("base", base, bf, (n, lora.hidden_out), dev),
-                         ctypes.byref(routing.desc), ctypes.byref(layout.desc), int(mode), int(max_tokens_per_expert),
-                         rows, _row_token(row_token, layout, dev), ctypes.byref(lora.desc),
-                         _arg("out", out, bf, (n, lora.hidden_out), dev),
-                         _arg("h", h, torch.float32, (h.shape[0], lora.rank), dev), _stream(stream)), "ep_lora")
+    dev, rows, n, table = _lora_rows(routing, layout, lora, x, h, row_token)
+    bf, wide = torch.bfloat16, (n, lora.hidden_out)
+    _check(lib().ep_lora(_arg("x", x, bf, (n, lora.hidden_in), dev),
+                         None if base is None else _arg("base", base, bf, wide, dev),
+                         ctypes.byref(routing.desc), ctypes.byref(layout.desc), mode, max_tokens_per_expert, rows, table,
+                         lora.ref, _arg("out", out, bf, wide, dev), _arg("h", h, torch.float32, (rows, lora.rank), dev),
+                         _stream(stream)), "ep_lora")
 
 
 def ep_lora_backward(dy: torch.Tensor, x, h, routing: Routing, layout: Layout, lora: Lora, dh: torch.Tensor, *,
@@ -768,17 +796,17 @@ def ep_lora_backward(dy: torch.Tensor, x, h, routing: Routing, layout: Layout, l
                      mode=EP_LAYOUT_COMPACT, max_tokens_per_expert=0, stream=None) -> None:
     """dh fp32 [num_rows, rank] (scratch), dx (added to dx_base), da and db from
     dy, x and the h of the forward call (x and h may be None without da, db)."""
-    rows, n = _lora_rows(routing, lora, dy, dh, row_token)
-    dev, bf = dy.device, torch.bfloat16
-    E, r, hin, hout = lora.E, lora.rank, lora.hidden_in, lora.hidden_out
-    hp = None if h is None else _arg("h", h, torch.float32, (max(rows, h.shape[0]), r), dev)
-    _check(lib().ep_lora_backward(_arg("dy", dy, bf, (n, hout), dev), _arg("x", x, bf, (n, hin), dev), hp,
-                                  _arg("dx_base", dx_base, bf, (n, hin), dev), ctypes.byref(routing.desc),
-                                  ctypes.byref(layout.desc), int(mode), int(max_tokens_per_expert), rows,
-                                  _row_token(row_token, layout, dev), ctypes.byref(lora.desc),
-                                  _arg("dh", dh, torch.float32, (dh.shape[0], r), dev),
-                                  _arg("dx", dx, bf, (n, hin), dev), _arg("da", da, bf, (E, r, hin), dev),
-                                  _arg("db", db, bf, (E, hout, r), dev), _stream(stream)), "ep_lora_backward")
+    dev, rows, n, table = _lora_rows(routing, layout, lora, dy, dh, row_token)
+    bf, E, r, hin, hout = torch.bfloat16, lora.E, lora.rank, lora.hidden_in, lora.hidden_out
+    inner = (n, hin)
+    _check(lib().ep_lora_backward(
+        _arg("dy", dy, bf, (n, hout), dev), None if x is None else _arg("x", x, bf, inner, dev),
+        None if h is None else _arg("h", h, torch.float32, (max(rows, h.shape[0]), r), dev),
+        None if dx_base is None else _arg("dx_base", dx_base, bf, inner, dev), ctypes.byref(routing.desc),
+        ctypes.byref(layout.desc), mode, max_tokens_per_expert, rows, table, lora.ref,
+        _arg("dh", dh, torch.float32, (rows, r), dev), None if dx is None else _arg("dx", dx, bf, inner, dev),
+        None if da is None else _arg("da", da, bf, (E, r, hin), dev),
+        None if db is None else _arg("db", db, bf, (E, hout, r), dev), _stream(stream)), "ep_lora_backward")
 
 
 def ep_get_layout_no_alloc(routing: Routing, layout: Layout, device_error_flags: torch.Tensor | None = None,

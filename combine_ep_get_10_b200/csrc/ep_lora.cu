@@ -11,6 +11,7 @@
 // Tensor-core products of bf16 operands with fp32 sums; u (fp32) enters as
 // hi + lo (ep_mma.cuh).
 #include <algorithm>
+#include <atomic>
 
 #include <cooperative_groups.h>
 
@@ -1052,14 +1053,22 @@ cudaError_t with_rank(int rank, F&& f)
 
 // A launch as a programmatic dependent, in clusters of `cluster`: every kernel
 // here waits (pdl_wait) before it reads what the kernel before may have written.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_after(void (*kernel)(KArgs...), unsigned grid, unsigned block, int smem, int cluster,
-                         cudaStream_t stream, const Args&... args)
+template <auto KERNEL, typename... Args>
+cudaError_t launch_after(unsigned grid, unsigned block, int smem, int cluster, cudaStream_t stream, const Args&... args)
 {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the devices on which the kernel may use its shared memory already (host
+    // threads may race to set a bit; they set the same attribute)
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (smem > 48 * 1024 && (ready.load(std::memory_order_relaxed) & bit) == 0) {
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess)
             return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -1073,7 +1082,7 @@ cudaError_t launch_after(void (*kernel)(KArgs...), unsigned grid, unsigned block
     attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    return cudaLaunchKernelEx(&cfg, KERNEL, args...);
 }
 
 } // namespace
@@ -1095,7 +1104,7 @@ cudaError_t launch_lora_shrink(const LoraShrinkLaunch& a, cudaStream_t stream)
     if (a.rows.pairs == 0)
         return cudaSuccess;
     if (a.rows.num_rows == 0)
-        return launch_after(overflow_kernel, 1, 32, 0, 1, stream, a.rows);
+        return launch_after<overflow_kernel>(1, 32, 0, 1, stream, a.rows);
     const int tiles = most_tiles(a.rows, kShrinkTile);
     return with_rank(a.rank, [&](auto rp) {
         constexpr int RP = decltype(rp)::value;
@@ -1107,8 +1116,9 @@ cudaError_t launch_lora_shrink(const LoraShrinkLaunch& a, cudaStream_t stream)
             return st;
         const int steps = (a.K + kDepth - 1) / kDepth;
         const int parts = std::max(1, std::min({8, EP_SHRINK_CTAS / tiles, steps / 4}));
-        return launch_after(a.transposed ? lora_shrink_kernel<RP, true> : lora_shrink_kernel<RP, false>,
-                            static_cast<unsigned>(tiles) * parts, kShrinkThreads, S::kBytes, parts, stream, w_map, a);
+        const unsigned grid = static_cast<unsigned>(tiles) * parts;
+        return a.transposed ? launch_after<lora_shrink_kernel<RP, true>>(grid, kShrinkThreads, S::kBytes, parts, stream, w_map, a)
+                            : launch_after<lora_shrink_kernel<RP, false>>(grid, kShrinkThreads, S::kBytes, parts, stream, w_map, a);
     });
 }
 
@@ -1129,8 +1139,10 @@ cudaError_t launch_lora_expand(const LoraExpandLaunch& a, cudaStream_t stream)
                                            : encode_map(&w_map, a.w, a.rank, a.N, a.rows.E, S::kBox, kExpandCols);
         if (e != cudaSuccess)
             return e;
-        return launch_after(a.transposed ? lora_expand_kernel<RP, true> : lora_expand_kernel<RP, false>,
-                            static_cast<unsigned>(grid), kExpandThreads, S::kBytes, 1, stream, w_map, a, shares);
+        const unsigned ctas = static_cast<unsigned>(grid);
+        return a.transposed
+                   ? launch_after<lora_expand_kernel<RP, true>>(ctas, kExpandThreads, S::kBytes, 1, stream, w_map, a, shares)
+                   : launch_after<lora_expand_kernel<RP, false>>(ctas, kExpandThreads, S::kBytes, 1, stream, w_map, a, shares);
     });
 }
 
@@ -1143,7 +1155,7 @@ cudaError_t launch_lora_outer(const LoraOuterLaunch& a, cudaStream_t stream)
         const int out_tiles = (a.hidden_out + kOuterCols - 1) / kOuterCols;
         const int64_t total = static_cast<int64_t>(a.rows.E) * (in_tiles + out_tiles);
         const unsigned grid = static_cast<unsigned>(std::min<int64_t>(total, 148 * S::kCtas));
-        return launch_after(lora_outer_kernel<RP>, grid, kOuterThreads, S::kBytes, 1, stream, a, in_tiles, out_tiles);
+        return launch_after<lora_outer_kernel<RP>>(grid, kOuterThreads, S::kBytes, 1, stream, a, in_tiles, out_tiles);
     });
 }
 
