@@ -157,14 +157,11 @@ __device__ __forceinline__ int row_at(const LoraRows& g, int row, int end)
 // ------------------------------------------------------------------ shrink
 constexpr int kShrinkThreads = 192; // four warps that load x and store, one that multiplies, one that loads w
 constexpr int kShrinkTile = 64; // rows
-#ifndef EP_SHRINK_STAGES
-#define EP_SHRINK_STAGES 4
-#endif
 constexpr int kDepth = 128;     // hidden channels a stage, in tiles of 64
 
 template <int RP>
 struct ShrinkShape {
-    static constexpr int kStages = RP <= 32 ? EP_SHRINK_STAGES : (RP == 64 ? 3 : 2);
+    static constexpr int kStages = RP <= 32 ? 4 : (RP == 64 ? 3 : 2); // two CTAs an SM
     static constexpr int kHalfBytes = kShrinkTile * 128; // 64 channels of x
     static constexpr int kXBytes = kShrinkTile * kDepth * 2;
     static constexpr int kWBytes = RP * kDepth * 2;
@@ -221,6 +218,30 @@ __global__ void __launch_bounds__(kShrinkThreads)
     const int live = rows.end - rows.begin;
     const int steps = (a.K + kDepth - 1) / kDepth;
     const int n = (steps - part + parts - 1) / parts; // steps part, part + parts, ..: the cluster reads along the rows
+    // 16-byte chunk tid % 16 of rows tid / 16 + 8 j (warps 0 .. 3); rows past the
+    // group's end are left out (what their rows of the product hold is not
+    // used), rows without data are zeros in every stage
+    const int c = tid % 16;
+    const uint32_t to = base + (c >> 3) * S::kHalfBytes + swizzled<8>((tid / 16) & 7, c & 7); // + 1024 j
+    const uint16_t* x_row[8];
+    uint32_t on = 0u; // rows with data
+    if (warp < 4) {
+        int entry[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            entry[j] = row_entry(a.rows, rows.begin + tid / 16 + 8 * j, rows.end);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int row = rows.begin + tid / 16 + 8 * j;
+            const int at = row_index(a.rows, entry[j], row, rows.end);
+            on |= (at >= 0 ? 1u : 0u) << j;
+            x_row[j] = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(max(at, 0)) * a.K + c * 8 + part * kDepth;
+            if (at < 0 && row < rows.end)
+                for (int i = 0; i < S::kStages; ++i)
+                    sts_v4(to + i * S::kStageBytes + 1024u * j, make_uint4(0u, 0u, 0u, 0u));
+        }
+        fence_proxy_async_shared();
+    }
     if (warp == 4)
         tmem_alloc(&s_tmem, S::kCols);
     tc_fence_before_sync();
@@ -229,31 +250,6 @@ __global__ void __launch_bounds__(kShrinkThreads)
     const uint32_t tmem = s_tmem;
 
     if (warp < 4) {
-        // 16-byte chunk tid % 16 of rows tid / 16 + 8 i; rows past the group's
-        // end are left out (what their rows of the product hold is not used)
-        const int c = tid % 16;
-        const uint16_t* x_row[8];
-        uint32_t on = 0u, none = 0u; // rows with data; rows that count as zeros
-        int entry[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            entry[i] = row_entry(a.rows, rows.begin + tid / 16 + 8 * i, rows.end);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = rows.begin + tid / 16 + 8 * i;
-            const int at = row_index(a.rows, entry[i], row, rows.end);
-            on |= (at >= 0 ? 1u : 0u) << i;
-            none |= (at < 0 && row < rows.end ? 1u : 0u) << i;
-            x_row[i] = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(max(at, 0)) * a.K + c * 8;
-        }
-        const uint32_t to = base + (c >> 3) * S::kHalfBytes + swizzled<8>(tid / 16, c & 7); // + 1024 j
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x_row[j] += part * kDepth;
-            if ((none >> j & 1u) != 0u)
-                for (int i = 0; i < S::kStages; ++i)
-                    sts_v4(to + i * S::kStageBytes + 1024u * j, make_uint4(0u, 0u, 0u, 0u));
-        }
         bool alive = true; // no wait has run out
         for (int i = 0; i < n; ++i) {
             const int stage = i % S::kStages;
@@ -356,13 +352,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
 constexpr int kExpandThreads = 288; // eight warps that add and store, one that loads w and multiplies
 constexpr int kExpandTile = 128;    // rows: the product's M
 constexpr int kExpandCols = 64;     // columns a step: the product's N
-constexpr int kExpandGrid = 2 * 148;
-#ifndef EP_STEP_ROWS
-#define EP_STEP_ROWS 128
-#endif
-#ifndef EP_SHRINK_CTAS
-#define EP_SHRINK_CTAS 296
-#endif
+constexpr int kExpandGrid = 2 * 148; // two CTAs an SM, the first beside the shrink's
 
 // A CTA's share of a call: one tile of rows, and every parts-th column step of
 // it from step `part` on.
@@ -377,10 +367,10 @@ struct ExpandShare {
 // more tiles than that).  One warp; all lanes get the answer.
 __device__ __forceinline__ bool find_share(const LoraRows& g, int i, int steps, int lane, ExpandShare& s)
 {
-    constexpr int kStepRows = EP_STEP_ROWS;
+    constexpr int kStepRows = 128; // 4096 rows of 16 adapters: 52 us, with 64 58 us, with 160 52 us
     const int per = (g.E + 31) / 32; // adapters a lane, consecutive
     const int e0 = min(lane * per, g.E), e1 = min(e0 + per, g.E);
-    int64_t cost = 0;
+    uint32_t cost = 0; // below 2^26: at most 2^24 rows
     int tiles = 0;
 #pragma unroll 8
     for (int j = e0; j < e1; ++j) {
@@ -394,10 +384,9 @@ __device__ __forceinline__ bool find_share(const LoraRows& g, int i, int steps, 
         tiles += __shfl_xor_sync(kFullMask, tiles, d);
         cost += __shfl_xor_sync(kFullMask, cost, d);
     }
-    const float spare = static_cast<float>(max(kExpandGrid - tiles, 0)) / static_cast<float>(max(cost, int64_t{1}));
-    // (the product's rounding moves a share's border at most: never more than `spare` and one a tile)
-    const auto shares = [&](int rows) {
-        return min(steps, static_cast<int>(static_cast<float>(rows + kStepRows) * spare) + 1);
+    const uint32_t spare = max(kExpandGrid - tiles, 0);
+    const auto shares = [&](int rows) { // rounded down they add up to `spare` at most, and one a tile
+        return min(steps, static_cast<int>((rows + kStepRows) * spare / max(cost, 1u)) + 1);
     };
     const int full = shares(kExpandTile);
     const auto of = [&](const RowRange& r) { // of an adapter
@@ -874,6 +863,8 @@ __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
                 continue;
             for (int i = 0; i < t.stages; ++i, ++at_stage) {
                 stage_free();
+                if (!alive)
+                    break;
                 const int first = t.rows.begin + i * kOuterRows, stage = at_stage % S::kStages;
                 const uint32_t bytes = static_cast<uint32_t>(min(kOuterRows, t.rows.end - first)) * a.rank * 4;
                 mbar_arrive_expect_tx(&s_u[stage], bytes);
@@ -1115,7 +1106,9 @@ cudaError_t launch_lora_shrink(const LoraShrinkLaunch& a, cudaStream_t stream)
         if (st != cudaSuccess)
             return st;
         const int steps = (a.K + kDepth - 1) / kDepth;
-        const int parts = std::max(1, std::min({8, EP_SHRINK_CTAS / tiles, steps / 4}));
+        // One resident wave of clusters: at 4096 rows of 8 adapters 18 us, with
+        // room for 444 CTAs 25 us (the last clusters wait for eight free places).
+        const int parts = std::max(1, std::min({8, 2 * 148 / tiles, steps / 4}));
         const unsigned grid = static_cast<unsigned>(tiles) * parts;
         return a.transposed ? launch_after<lora_shrink_kernel<RP, true>>(grid, kShrinkThreads, S::kBytes, parts, stream, w_map, a)
                             : launch_after<lora_shrink_kernel<RP, false>>(grid, kShrinkThreads, S::kBytes, parts, stream, w_map, a);

@@ -581,11 +581,10 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
 // order, no floating-point atomics, nothing that one call leaves for the next).
 constexpr int kBalanceWarps = 16;
 constexpr int kBalanceThreads = kBalanceWarps * 32;
-#ifndef EP_BAL_CTAS
-#define EP_BAL_CTAS 148
-#endif
-constexpr int kBalanceCtas = EP_BAL_CTAS; // chunks of a long batch: one a CTA and SM
-constexpr int kFewTokens = 256;
+// Chunks of a long batch, one an SM: at 4096 x 256 20.8 us a loss and gradient,
+// with two an SM 28.5 us.
+constexpr int kBalanceCtas = 148;
+constexpr int kFewTokens = 256; // one chunk a sequence: 128 x 8 3 us less of a caller's time
 
 // Tokens a chunk, a multiple of the warps.  Few tokens make one chunk each
 // sequence: the second launch would cost more than the longer sums.
@@ -946,10 +945,9 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(Balance
 
 // ---------------------------------------------------------------- backward
 constexpr int kBackwardWarps = 4;
-#ifndef EP_BW_FILL
-#define EP_BW_FILL 16
-#endif
-constexpr int kBackwardFill = 148 * EP_BW_FILL; // warps that the device holds at once
+// Warps to keep before runs get longer: at 16384 x 256 29.5 us a loss and
+// gradient, with 24 an SM 32.3 us, with 48 31.5 us.
+constexpr int kBackwardFill = 148 * 16;
 constexpr int kMostRun = 16;
 
 // The sequence of token t (the last one that begins at or before it), -1 when

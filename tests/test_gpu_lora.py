@@ -390,3 +390,44 @@ def test_long_runs_of_stages(rank):
     c = Case(ids(1500, 2, 29), 2, rank, 136, 264, 30)
     c.check_forward()
     c.check_backward()
+
+
+def test_shares_of_uneven_tiles():
+    """Adapters of very different sizes, where the column steps of a tile are
+    shared out by its rows: every share is worked on."""
+    g = torch.Generator().manual_seed(31)
+    for E, sizes in ((9, (1, 127, 128, 129, 3, 260, 64, 0, 31)), (40, None)):
+        if sizes is None:
+            sizes = torch.randint(0, 90, (E,), generator=g).tolist()
+        idx = torch.cat([torch.full((n,), e, dtype=torch.int64) for e, n in enumerate(sizes)])
+        idx = idx[torch.randperm(idx.numel(), generator=g)][:, None]
+        for hout in (2056, 8):
+            c = Case(idx, E, 16, 72, hout, 32)
+            c.check_forward()
+            c.check_backward(want=("dx",))
+
+
+@pytest.mark.parametrize("rank", [8, 40, 64, 96])
+def test_bad_row_tokens_at_every_rank(rank):
+    """Entries of no token in several stages and tiles: their rows are zeros in
+    h, their tokens keep what they held, no gradient sees them."""
+    c = Case(ids(400, 2, 33, none=0.0), 2, rank, 264, 136, 34)
+    out, h = c.forward()
+    dx, da, db = c.backward(h)
+    bad = torch.tensor([0, 5, 63, 64, 130, 199, 200, 399])
+    tokens = c.row_token.cpu()[bad].long()
+    c.row_token[bad.cuda()] = torch.tensor([-1, 400, -5, 2 ** 31 - 1, -2 ** 31, 400, 401, -1], dtype=torch.int32,
+                                           device="cuda")
+    out2, h2 = c.forward()
+    assert B.ep_get_device_error(c.layout) == B.EP_DEVERR_BAD_INDEX
+    keep = torch.ones(400, dtype=torch.bool)
+    keep[tokens] = False
+    assert torch.equal(out2.cpu()[keep], out.cpu()[keep]) and bool((out2.cpu()[tokens] == 5.0).all())
+    assert not bool(h2.cpu()[bad].any())
+    c.x[tokens] = math.nan
+    c.dy[tokens] = math.inf
+    h2[bad.cuda()] = math.nan
+    dx2, da2, db2 = c.backward(h2)
+    assert B.ep_get_device_error(c.layout) == B.EP_DEVERR_BAD_INDEX
+    assert torch.equal(dx2.cpu()[keep], dx.cpu()[keep])
+    assert bool(torch.isfinite(da2).all()) and bool(torch.isfinite(db2).all())

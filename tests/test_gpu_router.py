@@ -389,3 +389,62 @@ def test_offsets_that_are_not_sorted_stay_in_bounds():
                              seq_offsets=o)
     torch.cuda.synchronize()
     check_balance(logits, K, False, True, offsets=[0, 10, 20, 30, T])
+
+
+def test_a_workspace_holds_nothing_between_calls():
+    """The workspace needs no initialisation, and one workspace serves calls of
+    other sizes and numbers of sequences in turn."""
+    E, K = 48, 3
+    router = B.Router(E, K)
+    big = B.BalanceStats(router, 4000, num_seqs=40).workspace
+    g = torch.Generator().manual_seed(21)
+    for fill in (0xff, 0x00, 0x7f):
+        big.fill_(fill)
+        for T, S in ((4000, 1), (3000, 40), (10, 3), (4000, 2), (600, 40)):
+            logits, _ = make(T, E, torch.float32, T + S)
+            cuts = sorted(torch.randint(0, T + 1, (S - 1,), generator=g).tolist())
+            off = [0] + cuts + [T]
+            stats = B.BalanceStats(router, T, num_seqs=S)
+            stats.workspace = big
+            idx = logits.topk(K, dim=1).indices.cuda()
+            B.ep_balance_loss(logits.cuda(), router, idx, stats, seq_offsets=torch.tensor(off, dtype=torch.int32).cuda())
+            for s in range(S):
+                want = torch.bincount(idx[off[s]:off[s + 1]].reshape(-1).cpu(), minlength=E)
+                assert torch.equal(stats.counts[s].cpu().long(), want)
+                p = torch.softmax(logits[off[s]:off[s + 1]].double(), dim=1)
+                mean = p.sum(dim=0) / max(1, off[s + 1] - off[s])
+                assert torch.all((stats.mean_scores[s].cpu().double() - mean).abs() <= 2 * RTOL * mean)
+
+
+def test_groups_closer_than_fp32_tells_apart():
+    """Groups whose values differ by parts of an fp32 ulp, in every size of
+    group: the order is that of 64 bits, ties to the lower group."""
+    g = torch.Generator().manual_seed(22)
+    for E, G in ((64, 8), (256, 8), (48, 16), (1024, 4), (8, 8)):
+        base = torch.randn((1, E // G), generator=g)
+        logits = base.repeat(1, G).repeat(40, 1) + 2e-7 * torch.randn((40, E), generator=g)
+        logits[0] = base.repeat(1, G)  # all groups alike
+        bias = 1e-8 * torch.randn(E, generator=g)
+        for sigmoid in (False, True):
+            for top in (1, 2):
+                check_route(logits, 2, sigmoid=sigmoid, groups=G, topk_groups=max(1, G // 2), group_top=top)
+                check_route(logits, 2, sigmoid=sigmoid, groups=G, topk_groups=max(1, G // 2), group_top=top, bias=bias)
+
+
+def test_statistics_buffers_are_checked_when_set():
+    r = B.Router(8, 2)
+    stats = B.BalanceStats(r, 64, num_seqs=2)
+    with pytest.raises(TypeError):
+        stats.losses = torch.empty((3, 2), device="cuda")
+    with pytest.raises(TypeError):
+        stats.counts = torch.empty((2, 8), device="cuda")
+    with pytest.raises(ValueError):
+        stats.mean_scores = torch.empty((8, 2), device="cuda").T
+    with pytest.raises(TypeError):
+        stats.workspace = stats.workspace[:-256]
+    stats.seq_tokens = torch.empty(2, dtype=torch.int32)  # another device
+    logits, idx = torch.zeros((4, 8), device="cuda"), torch.zeros((4, 2), dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        B.ep_balance_loss(logits, r, idx, stats, seq_offsets=torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):  # of another number of experts
+        B.ep_balance_loss(torch.zeros((4, 9), device="cuda"), B.Router(9, 2), idx, B.BalanceStats(r, 64))
