@@ -36,32 +36,53 @@ struct RowRange {
 // Rows of adapter e, within [0, num_rows).
 __device__ __forceinline__ RowRange group_rows(const LoraRows& g, int e)
 {
-    int64_t b, n;
     if (g.mode == EP_LAYOUT_COMPACT) {
-        b = __ldg(g.offsets + e);
-        n = __ldg(g.offsets + e + 1) - b;
-    } else {
-        b = static_cast<int64_t>(e) * g.max_tokens;
-        n = min(__ldg(g.counts + e), g.max_tokens);
+        const int b = min(max(__ldg(g.offsets + e), 0), g.num_rows);
+        return {b, max(min(__ldg(g.offsets + e + 1), g.num_rows), b)};
     }
-    b = min(max(b, int64_t{0}), static_cast<int64_t>(g.num_rows));
-    n = min(max(n, int64_t{0}), static_cast<int64_t>(g.num_rows) - b);
+    const int64_t b = min(static_cast<int64_t>(e) * g.max_tokens, static_cast<int64_t>(g.num_rows));
+    const int64_t n = min(max(min(__ldg(g.counts + e), g.max_tokens), 0), g.num_rows - static_cast<int>(b));
     return {static_cast<int>(b), static_cast<int>(b + n)};
 }
 
-// Tiles of TILE rows are numbered adapter after adapter: the adapter and rows of
-// tile i; false when there are fewer.  One warp; all lanes get the answer.
-template <int TILE>
-__device__ __forceinline__ bool find_tile(const LoraRows& g, int i, int lane, int& e, RowRange& rows)
-{
-    const int per = (g.E + 31) / 32; // adapters a lane, consecutive
-    const int e0 = min(lane * per, g.E), e1 = min(e0 + per, g.E);
-    int n = 0;
-#pragma unroll 8
-    for (int j = e0; j < e1; ++j) {
-        const RowRange r = group_rows(g, j);
-        n += (r.end - r.begin + TILE - 1) / TILE;
+// The adapters that a lane has of a call's, `per` consecutive ones: the rows of
+// the first kHeld (all of them up to 256 adapters) stay in registers.
+struct LaneGroups {
+    static constexpr int kHeld = 8;
+    int e0, per; // adapters e0 .. e0 + per - 1
+    RowRange held[kHeld];
+
+    __device__ __forceinline__ LaneGroups(const LoraRows& g, int lane)
+    {
+        const int most = (g.E + 31) / 32;
+        e0 = min(lane * most, g.E);
+        per = min(most, g.E - e0);
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+            if (j < per)
+                held[j] = group_rows(g, e0 + j);
     }
+    // f(adapter, its rows) for each of the lane's; f returns true to stop.
+    template <typename F>
+    __device__ __forceinline__ void each(const LoraRows& g, F&& f) const
+    {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            if (j >= per)
+                return;
+            if (f(e0 + j, held[j]))
+                return;
+        }
+        for (int j = kHeld; j < per; ++j)
+            if (f(e0 + j, group_rows(g, e0 + j)))
+                return;
+    }
+};
+
+// The lane in whose run of `n` item i lies, and the items before that lane's;
+// -1 when there are fewer items.  One warp.
+__device__ __forceinline__ int find_lane(int n, int i, int lane, int& before)
+{
     int inc = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -70,27 +91,43 @@ __device__ __forceinline__ bool find_tile(const LoraRows& g, int i, int lane, in
             inc += o;
     }
     const uint32_t past = __ballot_sync(kFullMask, inc > i);
-    if (past == 0u)
+    before = inc - n;
+    return past == 0u ? -1 : __ffs(past) - 1;
+}
+
+// Tiles of TILE rows are numbered adapter after adapter: the adapter and rows of
+// tile i; false when there are fewer.  One warp; all lanes get the answer.
+template <int TILE>
+__device__ __forceinline__ bool find_tile(const LoraRows& g, int i, int lane, int& e, RowRange& rows)
+{
+    const LaneGroups groups(g, lane);
+    const auto tiles = [](const RowRange& r) { return (r.end - r.begin + TILE - 1) / TILE; };
+    int n = 0;
+    groups.each(g, [&](int, const RowRange& r) {
+        n += tiles(r);
         return false;
-    const int from = __ffs(past) - 1;
-    int found = 0, b = 0, end = 0;
-    if (lane == from) {
-        int left = i - (inc - n);
-        for (int j = e0; j < e1; ++j) {
-            const RowRange r = group_rows(g, j);
-            const int tiles = (r.end - r.begin + TILE - 1) / TILE;
-            if (left < tiles) {
-                found = j;
-                b = r.begin + left * TILE;
-                end = min(r.end, b + TILE);
-                break;
+    });
+    int before;
+    const int from = find_lane(n, i, lane, before);
+    if (from < 0)
+        return false;
+    int found = 0, left = i - before;
+    RowRange mine{0, 0};
+    if (lane == from)
+        groups.each(g, [&](int j, const RowRange& r) {
+            const int t = tiles(r);
+            if (left >= t) {
+                left -= t;
+                return false;
             }
-            left -= tiles;
-        }
-    }
+            found = j;
+            mine.begin = r.begin + left * TILE;
+            mine.end = min(r.end, mine.begin + TILE);
+            return true;
+        });
     e = __shfl_sync(kFullMask, found, from);
-    rows.begin = __shfl_sync(kFullMask, b, from);
-    rows.end = __shfl_sync(kFullMask, end, from);
+    rows.begin = __shfl_sync(kFullMask, mine.begin, from);
+    rows.end = __shfl_sync(kFullMask, mine.end, from);
     return true;
 }
 
@@ -368,64 +405,52 @@ struct ExpandShare {
 __device__ __forceinline__ bool find_share(const LoraRows& g, int i, int steps, int lane, ExpandShare& s)
 {
     constexpr int kStepRows = 128; // 4096 rows of 16 adapters: 52 us, with 64 58 us, with 160 52 us
-    const int per = (g.E + 31) / 32; // adapters a lane, consecutive
-    const int e0 = min(lane * per, g.E), e1 = min(e0 + per, g.E);
+    const LaneGroups groups(g, lane);
+    const auto tiles_of = [](const RowRange& r) { return (r.end - r.begin + kExpandTile - 1) / kExpandTile; };
     uint32_t cost = 0; // below 2^26: at most 2^24 rows
-    int tiles = 0;
-#pragma unroll 8
-    for (int j = e0; j < e1; ++j) {
-        const RowRange r = group_rows(g, j);
-        const int t = (r.end - r.begin + kExpandTile - 1) / kExpandTile;
-        tiles += t;
-        cost += r.end - r.begin + t * kStepRows;
-    }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) {
-        tiles += __shfl_xor_sync(kFullMask, tiles, d);
-        cost += __shfl_xor_sync(kFullMask, cost, d);
-    }
-    const uint32_t spare = max(kExpandGrid - tiles, 0);
+    uint32_t tiles = 0;
+    groups.each(g, [&](int, const RowRange& r) {
+        tiles += tiles_of(r);
+        cost += r.end - r.begin + tiles_of(r) * kStepRows;
+        return false;
+    });
+    tiles = __reduce_add_sync(kFullMask, tiles);
+    cost = max(__reduce_add_sync(kFullMask, cost), 1u);
+    const uint32_t spare = max(kExpandGrid - static_cast<int>(tiles), 0);
     const auto shares = [&](int rows) { // rounded down they add up to `spare` at most, and one a tile
-        return min(steps, static_cast<int>((rows + kStepRows) * spare / max(cost, 1u)) + 1);
+        return min(steps, static_cast<int>((rows + kStepRows) * spare / cost) + 1);
     };
     const int full = shares(kExpandTile);
     const auto of = [&](const RowRange& r) { // of an adapter
-        const int n = r.end - r.begin, t = (n + kExpandTile - 1) / kExpandTile;
-        return t == 0 ? 0 : (t - 1) * full + shares(n - (t - 1) * kExpandTile);
+        const int t = tiles_of(r);
+        return t == 0 ? 0 : (t - 1) * full + shares(r.end - r.begin - (t - 1) * kExpandTile);
     };
     int n = 0;
-#pragma unroll 8
-    for (int j = e0; j < e1; ++j)
-        n += of(group_rows(g, j));
-    int inc = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(kFullMask, inc, d);
-        if (lane >= d)
-            inc += o;
-    }
-    const uint32_t past = __ballot_sync(kFullMask, inc > i);
-    if (past == 0u)
+    groups.each(g, [&](int, const RowRange& r) {
+        n += of(r);
         return false;
-    const int from = __ffs(past) - 1;
+    });
+    int before;
+    const int from = find_lane(n, i, lane, before);
+    if (from < 0)
+        return false;
     ExpandShare mine{};
-    if (lane == from) {
-        int left = i - (inc - n);
-        for (int j = e0; j < e1; ++j) {
-            const RowRange r = group_rows(g, j);
+    int left = i - before;
+    if (lane == from)
+        groups.each(g, [&](int j, const RowRange& r) {
             const int here = of(r);
-            if (left < here) {
-                const int t = (r.end - r.begin + kExpandTile - 1) / kExpandTile, tile = min(left / full, t - 1);
-                mine.e = j;
-                mine.rows.begin = r.begin + tile * kExpandTile;
-                mine.rows.end = min(r.end, mine.rows.begin + kExpandTile);
-                mine.part = left - tile * full;
-                mine.parts = shares(mine.rows.end - mine.rows.begin);
-                break;
+            if (left >= here) {
+                left -= here;
+                return false;
             }
-            left -= here;
-        }
-    }
+            const int tile = min(left / full, tiles_of(r) - 1);
+            mine.e = j;
+            mine.rows.begin = r.begin + tile * kExpandTile;
+            mine.rows.end = min(r.end, mine.rows.begin + kExpandTile);
+            mine.part = left - tile * full;
+            mine.parts = shares(mine.rows.end - mine.rows.begin);
+            return true;
+        });
     s.e = __shfl_sync(kFullMask, mine.e, from);
     s.rows.begin = __shfl_sync(kFullMask, mine.rows.begin, from);
     s.rows.end = __shfl_sync(kFullMask, mine.rows.end, from);
