@@ -74,6 +74,37 @@ __device__ __forceinline__ float load_logit(const void* logits, int64_t i)
     return __ldg(static_cast<const float*>(logits) + i);
 }
 
+// Loads that are not waited for before their value is used: predicated, into
+// the register that holds the value otherwise.  (A load in a branch is copied at
+// the branch's end, and the copy, like any use, waits for it.)
+__device__ __forceinline__ void load_u8_if(uint32_t& r, const uint8_t* p, bool on)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.nc.u8 %0, [%1];\n\t}"
+                 : "+r"(r)
+                 : "l"(p), "r"(on ? 1u : 0u));
+}
+
+__device__ __forceinline__ void load_u16_if(uint32_t& r, const void* p, bool on)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}"
+                 : "+r"(r)
+                 : "l"(p), "r"(on ? 1u : 0u));
+}
+
+__device__ __forceinline__ void load_u32_if(uint32_t& r, const void* p, bool on)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}"
+                 : "+r"(r)
+                 : "l"(p), "r"(on ? 1u : 0u));
+}
+
+__device__ __forceinline__ void load_s64_if(int64_t& r, const int64_t* p, bool on)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.nc.s64 %0, [%1];\n\t}"
+                 : "+l"(r)
+                 : "l"(p), "r"(on ? 1u : 0u));
+}
+
 // A lane's part of a row as it lies in memory, so that the next row can be on
 // its way while one is worked on.
 template <int NPL, bool BF16, bool GROUPED, bool VEC>
@@ -81,7 +112,7 @@ struct RawRow {
     using Map = RowMap<NPL, BF16, GROUPED, VEC>;
     static constexpr int kWords = VEC ? NPL * (BF16 ? 2 : 4) / 16 : NPL;
     uint4 vec[VEC ? kWords : 1];
-    float one[VEC ? 1 : NPL];
+    uint32_t one[VEC ? 1 : NPL];
 
     __device__ __forceinline__ void load(const void* logits, int64_t row, const Map& map, bool on)
     {
@@ -101,8 +132,13 @@ struct RawRow {
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < NPL; ++j)
-                one[j] = on && map.holds(j) ? load_logit<BF16>(logits, at + Map::offset(j)) : kNegInf;
+            for (int j = 0; j < NPL; ++j) {
+                one[j] = BF16 ? 0xff80u : 0xff800000u; // -inf
+                if (BF16)
+                    load_u16_if(one[j], static_cast<const uint16_t*>(logits) + at + Map::offset(j), on && map.holds(j));
+                else
+                    load_u32_if(one[j], static_cast<const float*>(logits) + at + Map::offset(j), on && map.holds(j));
+            }
         }
     }
     // The logits, closed ones and registers that hold nothing as -inf.
@@ -117,7 +153,7 @@ struct RawRow {
                 const uint32_t u = k == 0 ? w.x : (k == 1 ? w.y : (k == 2 ? w.z : w.w));
                 l = BF16 ? (i % 2 == 0 ? bf16_lo(u) : bf16_hi(u)) : __uint_as_float(u);
             } else {
-                l = one[j];
+                l = __uint_as_float(BF16 ? one[j] << 16 : one[j]);
             }
             v[j] = clean_logit(l);
         }
@@ -772,20 +808,22 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch 
     int live = 0;
     // one token a warp: its row, mask and ids are loaded while the one before is summed
     RawRow<NPL, BF16, false, VEC> raw;
-    int64_t e_next = -1;
-    bool on_next = false;
+    int64_t e_next;
+    uint32_t mask_next;
     const auto load = [&](int t) {
         const bool in = t < c.tokens.end;
-        on_next = in && (a.token_mask == nullptr || __ldg(a.token_mask + t) != 0);
-        e_next = in && lane < K ? __ldg(a.topk_idx + static_cast<int64_t>(t) * K + lane) : -1;
         raw.load(a.logits, t, map, in);
+        mask_next = 1u;
+        load_u8_if(mask_next, a.token_mask + t, in && a.token_mask != nullptr);
+        e_next = -1;
+        load_s64_if(e_next, a.topk_idx + static_cast<int64_t>(t) * K + lane, in && lane < K);
     };
     load(c.tokens.begin + warp);
     for (int t = c.tokens.begin + warp; t < c.tokens.end; t += kBalanceWarps) {
         float v[NPL];
         raw.take(v);
         const int64_t e = e_next;
-        const bool on = on_next;
+        const bool on = mask_next != 0u;
         load(t + kBalanceWarps);
         if (!on)
             continue;
@@ -856,6 +894,7 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch 
 // alone would draw all the partial sums through one SM: 7 us for 148 chunks of
 // 256 experts).
 constexpr int kFinishCluster = 8;
+constexpr int kFinishLoads = 10; // 16 warps: 160 chunks in one go, the most a sequence of a long batch has
 constexpr int kFinishExperts = kRouterMaxExperts / kFinishCluster; // a CTA, at most
 
 __global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(BalanceLaunch a, int chunk)
@@ -878,22 +917,35 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(Balance
     for (int x = lane; x < n_e; x += 32) {
         float q = 0.0f;
         int cnt = 0;
-#pragma unroll 10
-        for (int i = warp; i < c.of; i += kBalanceWarps) {
-            const int2 o = __ldcg(part.sums + (c.first + i) * E + e0 + x);
-            q += __int_as_float(o.x);
-            cnt += o.y;
+        for (int base = warp; base < c.of; base += kFinishLoads * kBalanceWarps) {
+            int2 o[kFinishLoads]; // all on their way at once
+#pragma unroll
+            for (int u = 0; u < kFinishLoads; ++u) {
+                const int i = base + u * kBalanceWarps;
+                o[u] = i < c.of ? __ldcg(part.sums + (c.first + i) * E + e0 + x) : make_int2(0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < kFinishLoads; ++u) {
+                q += __int_as_float(o[u].x);
+                cnt += o[u].y;
+            }
         }
         s_q[warp][x] = q;
         s_cnt[warp][x] = cnt;
     }
-    if (warp == 0) { // every CTA needs the tokens
+    if (warp == kBalanceWarps - 1) { // every CTA needs the tokens
         float z = 0.0f;
         int n = 0;
-        for (int i = lane; i < c.of; i += 32) {
-            const int2 o = __ldcg(part.tails + c.first + i);
-            z += __int_as_float(o.x);
-            n += o.y;
+        for (int base = lane; base < c.of; base += 5 * 32) {
+            int2 o[5];
+#pragma unroll
+            for (int u = 0; u < 5; ++u)
+                o[u] = base + 32 * u < c.of ? __ldcg(part.tails + c.first + base + 32 * u) : make_int2(0, 0);
+#pragma unroll
+            for (int u = 0; u < 5; ++u) {
+                z += __int_as_float(o[u].x);
+                n += o[u].y;
+            }
         }
         z = warp_sum(z);
         n = __reduce_add_sync(kFullMask, n);
@@ -945,9 +997,9 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(Balance
 
 // ---------------------------------------------------------------- backward
 constexpr int kBackwardWarps = 4;
-// Warps to keep before runs get longer: at 16384 x 256 29.5 us a loss and
-// gradient, with 24 an SM 32.3 us, with 48 31.5 us.
-constexpr int kBackwardFill = 148 * 16;
+// Warps to keep before runs get longer: at 16384 x 256 24.9 us a loss and
+// gradient, with 16 an SM 26.6 us, with 32 27.2 us.
+constexpr int kBackwardFill = 148 * 24;
 constexpr int kMostRun = 16;
 
 // The sequence of token t (the last one that begins at or before it), -1 when
@@ -992,9 +1044,11 @@ __device__ __forceinline__ void each_expert(const RowMap<NPL, BF16, false, VEC>&
 
 // A warp has `run` consecutive tokens: the next one's row, mask, ids and
 // gradients are on their way while one is worked on, and the counts of a
-// sequence stay in registers until its last token.
+// sequence stay in registers until its last token.  Latencies bound it: 64
+// registers, for 32 warps an SM, take 15.7 us for loss and gradient of 4096 x
+// 256, 80 registers 17.3 us.
 template <int NPL, bool BF16, bool VEC>
-__global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(RouterBackwardLaunch a, int run)
+__global__ void __launch_bounds__(kBackwardWarps * 32, NPL <= 8 ? 8 : 1) router_backward_kernel(RouterBackwardLaunch a, int run)
 {
     extern __shared__ __align__(16) float s_add[]; // [kBackwardWarps, E]: the chosen experts' part
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1009,17 +1063,18 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(Ro
         return;
     const int begin = static_cast<int>(first), end = static_cast<int>(min(first + run, static_cast<int64_t>(a.r.num_tokens)));
     RawRow<NPL, BF16, false, VEC> raw;
-    int64_t e_next = -1;
-    float g_next = 0.0f;
-    bool on_next = false;
+    int64_t e_next;
+    uint32_t mask_next, g_next;
     const auto load = [&](int t) {
-        const bool in = t < end;
-        on_next = in && (a.token_mask == nullptr || __ldg(a.token_mask + t) != 0);
+        const bool in = t < end, slot = in && a.d_topk_weights != nullptr && lane < K;
+        const int64_t at = static_cast<int64_t>(t) * K + lane;
         raw.load(a.logits, t, map, in);
-        if (a.d_topk_weights != nullptr && in && lane < K) {
-            e_next = __ldg(a.topk_idx + static_cast<int64_t>(t) * K + lane);
-            g_next = __ldg(a.d_topk_weights + static_cast<int64_t>(t) * K + lane);
-        }
+        mask_next = 1u;
+        load_u8_if(mask_next, a.token_mask + t, in && a.token_mask != nullptr);
+        e_next = -1;
+        load_s64_if(e_next, a.topk_idx + at, slot);
+        g_next = 0u;
+        load_u32_if(g_next, a.d_topk_weights + at, slot);
     };
     load(begin);
     // the sequence at hand: its end, its losses' gradients over its tokens, its counts
@@ -1057,11 +1112,15 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(Ro
     for (int t = begin; t < end; ++t) {
         float v[NPL], d[NPL];
         const int64_t e = e_next;
-        float g = g_next;
-        const bool on = on_next;
-        float l = kNegInf; // lane k: slot k's logit
-        if (on && lane < K && e >= 0 && e < E)
-            l = clean_logit(load_logit<BF16>(a.logits, static_cast<int64_t>(t) * E + e));
+        float g = __uint_as_float(g_next);
+        const bool on = mask_next != 0u;
+        // lane k: slot k's logit
+        uint32_t slot_l = BF16 ? 0xff80u : 0xff800000u;
+        const bool slot = on && e >= 0 && e < E;
+        if (BF16)
+            load_u16_if(slot_l, static_cast<const uint16_t*>(a.logits) + static_cast<int64_t>(t) * E + e, slot);
+        else
+            load_u32_if(slot_l, static_cast<const float*>(a.logits) + static_cast<int64_t>(t) * E + e, slot);
         raw.take(v);
         load(t + 1);
 #pragma unroll
@@ -1084,6 +1143,7 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) router_backward_kernel(Ro
                 p[j] *= inv_z;
 
             if (a.d_topk_weights != nullptr) {
+                const float l = clean_logit(__uint_as_float(BF16 ? slot_l << 16 : slot_l));
                 const bool got = l > kNegInf;
                 g = got ? a.r.scale * g : 0.0f;
                 float part = 0.0f;    // what slot k adds at its expert
