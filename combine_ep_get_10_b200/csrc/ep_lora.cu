@@ -1,15 +1,26 @@
 // ep_lora.cu -- low-rank adapters on the rows of a token-choice layout.
 //
-// The layout groups rows by adapter, so a tile of kRowTile rows of one group is
-// an ordinary matrix product with that adapter's factors: the rows are read
-// where they are (row_token, or the dispatched rows themselves).  Three
-// products, all memory-bound at the ranks they are for (rank flops a byte of
-// row data):
+// The layout groups rows by adapter, so a tile of rows of one group is an
+// ordinary matrix product with that adapter's factors: the rows are read where
+// they are (row_token, or the dispatched rows themselves).  Three products, all
+// bound by memory at the ranks they are for (4 rank flops a byte of row data
+// and less; the tensor cores are busy 8 to 12 % of the time at rank 32):
 //   shrink  u = s_e X W        long sum over the hidden width, rank columns
 //   expand  out = base + u W   rank-long sum, hidden columns, base and out move
 //   outer   dW = sum of rows   sum over a group's rows
-// Tensor-core products of bf16 operands with fp32 sums; u (fp32) enters as
-// hi + lo (ep_mma.cuh).
+// All on tcgen05 with bf16 operands and fp32 sums in tensor memory; u (fp32)
+// enters as hi + lo (ep_mma.cuh), which keeps 16 bits of it.
+//
+// Rows come by cp.async, 16 bytes a lane: as fast for 128 bytes a row at a time
+// as for 512 (4.75 TB/s for 4096 x 7168 read, 5.2 TB/s read and written), and
+// any row may be anywhere.  Factors come through tensor maps, which lay them
+// out as the tensor core reads them and fill what is past the rank, the width
+// or the last column with zeros.
+//
+// The kernels of a call are programmatic dependents of one another: what does
+// not depend on the kernel before (which rows, the first tiles of base and of
+// the factors) is done while that one runs.  Only the products' own results are
+// read after the wait, through L2.
 #include <algorithm>
 #include <atomic>
 
@@ -214,6 +225,10 @@ struct ShrinkShape {
     static constexpr int kWBox = RP < 64 ? RP : 64; // ranks a box of w [K, rank]
 };
 
+// Bound by the rows' bytes: 4096 x 7168, 8 adapters of rank 32, 18 us with the
+// launch (59 MB, 3.3 TB/s; a kernel that only copies such rows 12.4 us).  What is
+// left are the ends: 2 us to find the tile and its rows, 2 us for the sums.
+//
 // A cluster has one tile of rows; its CTAs split the hidden width, and each
 // adds up its share of the tile's rows over the cluster, in CTA order (the
 // same sum every time, no atomics, no partial sums in HBM).  Four warps copy
@@ -476,6 +491,11 @@ __device__ __forceinline__ uint32_t add_to_bf16x2(uint32_t base, float a, float 
     return pack_bf16x2(bf16_lo(base) + a, bf16_hi(base) + b);
 }
 
+// Bound by base and out: 4096 x 7168, 8 adapters of rank 32, 30 us after the
+// product before it (117 MB, 4 TB/s; a copy of such rows alone 22.6 us).  A CTA
+// that starts when the kernel before it ends needs 8 us to its first store, so
+// the first of an SM's two starts beside the shrink's CTAs.
+//
 // A CTA has one tile of rows and every parts-th column step.  u stays in shared
 // memory as two bf16 tiles (hi, lo).  While one thread has the factor's next
 // columns multiplied into one of two places in tensor memory, eight warps take the other one (32 rows and 32 columns each):
@@ -796,6 +816,10 @@ __device__ __forceinline__ bool split_warps_any(bool mine)
     return any != 0u;
 }
 
+// Bound by x and dy: 4096 x 7168 each, 8 adapters of rank 32, 30 us after the
+// product before it (117 MB, 3.9 TB/s), and by the chains that turn u into its
+// terms, 1200 cycles a stage, of which three CTAs an SM hide most.
+//
 // dW of one adapter and kOuterCols columns of x or dy, tile after tile: the
 // columns are the product's rows (M), the rank its columns (N), and the sum
 // runs over the adapter's rows, kOuterRows a stage.  Both operands are MN-major:

@@ -22,6 +22,10 @@
  *            Solutions", Solution 1 (token_indices [num_experts, capacity]
  *            and its dispatch/combine pair) and Solution 2 (skip -1 padding).
  *
+ * Beside this header: ep_router.h (the step before the layout: experts and
+ * weights from router logits, the balance losses, the logits' gradient) and
+ * ep_lora.h (low-rank adapters on the rows of a layout, and their gradients).
+ *
  * Notation: T tokens, H hidden, K top-k width, E experts, R logical ranks
  * (rank r owns experts [r*E/R, (r+1)*E/R)), C expert capacity.
  *

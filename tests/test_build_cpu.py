@@ -83,3 +83,16 @@ def test_layout_kernels_do_not_spill():
                     r"ec_(count|scan|fill|sort)_kernel"):
         for name, (_, spill) in _pick(k, pattern).items():
             assert spill == 0, "%s spills %d bytes" % (name, spill)
+
+
+def test_adapter_kernels_keep_their_residency():
+    k = _report("ep_lora.cu")
+    # three 320-thread CTAs per SM for the factors' gradients up to rank 64
+    for name, (regs, _) in _pick(k, r"lora_outer_kernelILi(16|32|64)E").items():
+        assert regs <= 64, "%s: %d registers > 64" % (name, regs)
+    # two 288-thread CTAs per SM (five warps on one of its quarters): 96 registers, and no spill, since
+    # shared memory leaves a spill no first-level cache
+    for name, (regs, spill) in _pick(k, r"lora_expand_kernelILi(16|32|64)E").items():
+        assert regs <= 96 and spill == 0, "%s: %d registers, %d bytes spilled" % (name, regs, spill)
+    for name, (regs, _) in _pick(k, r"lora_shrink_kernel").items():
+        assert regs <= 64, "%s: %d registers > 64 (beside an expand CTA)" % (name, regs)
