@@ -1120,12 +1120,17 @@ ep_status_t ep_lora(const void* x, const void* base, const ep_routing_desc_t* ro
         return EP_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const ep::LoraRows rows = lora_rows(routing, layout, mode, max_tokens_per_expert, num_rows, row_token);
+    const int32_t* copied = row_token != nullptr && out != base ? layout->slot : nullptr; // tokens without an adapter
+    if (ep::lora_few(rows)) {
+        ep::LoraFewLaunch few{rows, x, lora->a, lora->b, lora->scales, base, out, h, lora->hidden_in, lora->hidden_out,
+                              lora->rank, copied};
+        return from_cuda(ep::launch_lora_few(few, s));
+    }
     ep::LoraShrinkLaunch down{rows, x, lora->a, lora->scales, lora->hidden_in, lora->rank, 0, h, 1};
     const cudaError_t e = ep::launch_lora_shrink(down, s);
     if (e != cudaSuccess)
         return EP_ERR_CUDA;
-    ep::LoraExpandLaunch up{rows, h, lora->b, base, out, lora->hidden_out, lora->rank, 0,
-                            row_token != nullptr && out != base ? layout->slot : nullptr, rows.pairs > 0 ? 1 : 0};
+    ep::LoraExpandLaunch up{rows, h, lora->b, base, out, lora->hidden_out, lora->rank, 0, copied, 1};
     return from_cuda(ep::launch_lora_expand(up, s));
 }
 

@@ -167,6 +167,38 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void* p)
     return r;
 }
 
+// Loads that are not waited for before their value is used: predicated, zeros
+// where `on` is false.  (A load in a branch is copied at the branch's end, and
+// the copy, like any use, waits for it.)
+__device__ __forceinline__ uint4 ld_nc_v4_if(const void* p, bool on)
+{
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                 "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)
+                 : "l"(p), "r"(on ? 1u : 0u));
+    return r;
+}
+
+__device__ __forceinline__ uint2 ld_nc_v2_if(const void* p, bool on)
+{
+    uint2 r = make_uint2(0u, 0u);
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+                 "@p ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
+                 : "+r"(r.x), "+r"(r.y)
+                 : "l"(p), "r"(on ? 1u : 0u));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t ld_nc_u32_if(const void* p, bool on)
+{
+    uint32_t r = 0u;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}"
+                 : "+r"(r)
+                 : "l"(p), "r"(on ? 1u : 0u));
+    return r;
+}
+
 // 32 bytes (256-bit load, sm_100) into two 16-byte halves; p 32-byte aligned.
 __device__ __forceinline__ void ld_nc_v8(const void* p, uint4& lo, uint4& hi)
 {

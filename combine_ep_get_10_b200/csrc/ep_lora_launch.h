@@ -63,6 +63,24 @@ struct LoraExpandLaunch {
 };
 cudaError_t launch_lora_expand(const LoraExpandLaunch& a, cudaStream_t stream);
 
+// Both products of a forward call in one kernel, for few rows an adapter
+// (lora_few): u as LoraShrinkLaunch gives it with w = a [rank, K], out as
+// LoraExpandLaunch does with w = b [N, rank].
+struct LoraFewLaunch {
+    LoraRows rows;
+    const void* x;
+    const void* a;
+    const void* b;
+    const float* scales; // or nullptr
+    const void* base;    // or nullptr
+    void* out;
+    float* u;
+    int32_t K, N, rank;
+    const int32_t* slot; // as for LoraExpandLaunch
+};
+bool lora_few(const LoraRows& rows);
+cudaError_t launch_lora_few(const LoraFewLaunch& a, cudaStream_t stream);
+
 // da[e][j, n] = sum over e's rows of dh[row, j] * x[row, n]  and
 // db[e][n, j] = sum over e's rows of dy[row, n] * h[row, j]
 struct LoraOuterLaunch {

@@ -1,6 +1,6 @@
 // ep_mma.cuh -- device helpers of the kernels that multiply: asynchronous
-// 16-byte copies, the two-term bf16 form of an fp32 operand, and the places of
-// 16-byte chunks in operand tiles.
+// 16-byte copies, the warp's matrix product, the two-term bf16 form of an fp32
+// operand, and the places of 16-byte chunks in operand tiles.
 #pragma once
 
 #include "ep_device.cuh"
@@ -36,6 +36,17 @@ __device__ __forceinline__ void cp_async_wait()
 __device__ __forceinline__ void cp_async_wait_all()
 {
     asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// d += a (16 x 16, rows) * b (16 x 8, columns), bf16 operands, fp32 sums, by one
+// warp from registers.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // An fp32 pair as bf16 pairs hi + lo: hi is the value rounded to bf16, lo what

@@ -431,3 +431,30 @@ def test_bad_row_tokens_at_every_rank(rank):
     assert B.ep_get_device_error(c.layout) == B.EP_DEVERR_BAD_INDEX
     assert torch.equal(dx2.cpu()[keep], dx.cpu()[keep])
     assert bool(torch.isfinite(da2).all()) and bool(torch.isfinite(db2).all())
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 40, 64, 88, 128])
+@pytest.mark.parametrize("T,E", [(1, 7), (16, 1), (90, 9), (130, 70)])
+def test_few_rows_an_adapter(rank, T, E):
+    """Sixteen rows an adapter and less, one more than that for some: widths that
+    end inside a block of 32, base in place, missing and separate, rows that no
+    pair names, entries of no token."""
+    for hin, hout in ((8, 40), (1000, 72), (4104, 1048)):
+        c = Case(ids(T, E, rank, none=0.15), E, rank, hin, hout, 35)
+        for base in ("separate", "in place", "none"):
+            c.check_forward(base)
+    c = Case(ids(T, E, rank, none=0.3), E, rank, 264, 136, 36, tokens=False, mode=B.EP_LAYOUT_PADDED, max_tokens=5)
+    c.check_forward()
+    assert (B.ep_get_device_error(c.layout) != 0) == bool(c.layout.num_tokens_per_expert.max() > 5)
+    if T > 20:
+        c = Case(ids(T, E, rank, none=0.0), E, rank, 264, 136, 37)
+        out, h = c.forward()
+        bad = torch.tensor([1, 8, T - 1])
+        tokens = c.row_token.cpu()[bad].long()
+        c.row_token[bad.cuda()] = torch.tensor([-1, T, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+        out2, h2 = c.forward()
+        assert B.ep_get_device_error(c.layout) == B.EP_DEVERR_BAD_INDEX
+        keep = torch.ones(T, dtype=torch.bool)
+        keep[tokens] = False
+        assert torch.equal(out2.cpu()[keep], out.cpu()[keep]) and bool((out2.cpu()[tokens] == 5.0).all())
+        assert not bool(h2.cpu()[bad].any())
