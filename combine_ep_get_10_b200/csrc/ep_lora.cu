@@ -724,10 +724,14 @@ constexpr int kFewCluster = 8;
 
 template <int RP>
 struct FewShape {
-    static constexpr int kPitch = RP + 4;                  // floats a row of sums
-    static constexpr int kSums = kFewTile * kPitch;        // floats
-    static constexpr int kBytes = (8 + 2) * kSums * 4;     // the warps' sums, the CTA's, the cluster's
-    static constexpr int kAhead = RP <= 16 ? 4 : (RP <= 32 ? 2 : 1); // blocks of 32 channels a warp loads at once
+    static constexpr int kRanks = 16;               // ranks a warp multiplies x with
+    static constexpr int kRankWarps = RP / kRanks;  // warps side by side in them
+    static constexpr int kWarpPitch = kRanks + 4;   // floats a row of a warp's sums
+    static constexpr int kPitch = RP + 4;           // of the CTA's and the cluster's
+    static constexpr int kWarpSums = kFewTile * kWarpPitch, kSums = kFewTile * kPitch; // floats
+    static constexpr int kBytes = (8 * kWarpSums + 2 * kSums) * 4;
+    static constexpr int kAhead = 4;                // blocks of 32 channels a warp loads at once
+    static constexpr bool kTwo = RP <= 32;          // two groups of output columns on their way
 };
 
 // Both products of a forward call for a tile of 16 rows, where an adapter has few
@@ -743,7 +747,7 @@ struct FewShape {
 // needs.  In the same way the columns of out are dealt to the products so that a
 // thread ends with 8 consecutive ones.
 template <int RP>
-__global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel(LoraFewLaunch a, int tiles)
+__global__ void __launch_bounds__(kFewThreads, RP <= 64 ? 2 : 1) lora_few_kernel(LoraFewLaunch a, int tiles)
 {
     using S = FewShape<RP>;
     extern __shared__ __align__(16) float s_few[];
@@ -772,29 +776,32 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
     const uint16_t* x0 = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(max(at0, 0)) * a.K;
     const uint16_t* x1 = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(max(at1, 0)) * a.K;
 
-    // u: blocks of 32 channels unit, unit + units, ..; lane: 8 channels from 8 q
-    float acc[RP / 8][4];
+    // u: ranks 16 (warp % kRankWarps).., every k_units-th block of 32 channels; lane:
+    // 8 channels from 8 q
+    const int j0 = warp % S::kRankWarps * S::kRanks;
+    const int k_unit = part * (8 / S::kRankWarps) + warp / S::kRankWarps, k_units = parts * (8 / S::kRankWarps);
+    float acc[2][4];
 #pragma unroll
-    for (int j = 0; j < RP / 8; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             acc[j][i] = 0.0f;
-    for (int k0 = unit * 32; k0 < a.K; k0 += S::kAhead * units * 32) {
-        uint4 xa[S::kAhead][2], w[S::kAhead][RP / 8];
+    for (int k0 = k_unit * 32; k0 < a.K; k0 += S::kAhead * k_units * 32) {
+        uint4 xa[S::kAhead][2], w[S::kAhead][2];
 #pragma unroll
         for (int i = 0; i < S::kAhead; ++i) {
-            const int k = k0 + i * units * 32 + q * 8;
+            const int k = k0 + i * k_units * 32 + q * 8;
             const bool in = k < a.K;
             xa[i][0] = ld_nc_v4_if(x0 + k, in && at0 >= 0);
             xa[i][1] = ld_nc_v4_if(x1 + k, in && at1 >= 0);
 #pragma unroll
-            for (int j = 0; j < RP / 8; ++j)
-                w[i][j] = ld_nc_v4_if(wa + static_cast<int64_t>(j * 8 + g) * a.K + k, in && j * 8 < a.rank);
+            for (int j = 0; j < 2; ++j)
+                w[i][j] = ld_nc_v4_if(wa + static_cast<int64_t>(j0 + j * 8 + g) * a.K + k, in && j0 + j * 8 < a.rank);
         }
 #pragma unroll
         for (int i = 0; i < S::kAhead; ++i)
 #pragma unroll
-            for (int j = 0; j < RP / 8; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 mma16816(acc[j], xa[i][0].x, xa[i][1].x, xa[i][0].y, xa[i][1].y, w[i][j].x, w[i][j].y);
                 mma16816(acc[j], xa[i][0].z, xa[i][1].z, xa[i][0].w, xa[i][1].w, w[i][j].z, w[i][j].w);
             }
@@ -824,29 +831,29 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
         }
     };
     const int groups = (a.N + 31) / 32;
-    constexpr bool kTwo = RP <= 64; // two groups of columns on their way
     Columns even, odd;
     load_columns(even, unit);
-    if (kTwo)
+    if (S::kTwo)
         load_columns(odd, unit + units); // (past the last: zeros, and nothing is read)
 
     // the warps' sums, the CTA's, the cluster's: each in a fixed order
-    float* s_cta = s_few + 8 * S::kSums;
+    float* s_cta = s_few + 8 * S::kWarpSums;
     float* s_u = s_cta + S::kSums;
 #pragma unroll
-    for (int j = 0; j < RP / 8; ++j) {
-        float* p = s_few + warp * S::kSums + g * S::kPitch + j * 8 + 2 * q;
+    for (int j = 0; j < 2; ++j) {
+        float* p = s_few + warp * S::kWarpSums + g * S::kWarpPitch + j * 8 + 2 * q;
         *reinterpret_cast<float2*>(p) = make_float2(acc[j][0], acc[j][1]);
-        *reinterpret_cast<float2*>(p + 8 * S::kPitch) = make_float2(acc[j][2], acc[j][3]);
+        *reinterpret_cast<float2*>(p + 8 * S::kWarpPitch) = make_float2(acc[j][2], acc[j][3]);
     }
     __syncthreads();
     for (int i = tid; i < kFewTile * RP; i += kFewThreads) {
-        const int at = i / RP * S::kPitch + i % RP;
+        const int row = i / RP, j = i % RP;
+        const float* p = s_few + j / S::kRanks * S::kWarpSums + row * S::kWarpPitch + j % S::kRanks;
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w)
-            sum += s_few[w * S::kSums + at];
-        s_cta[at] = sum;
+        for (int w = 0; w < 8; w += S::kRankWarps)
+            sum += p[w * S::kWarpSums];
+        s_cta[row * S::kPitch + j] = sum;
     }
     cluster.sync();
     for (int i = tid; i < kFewTile * RP; i += kFewThreads) {
@@ -889,7 +896,7 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
             }
         }
         const uint4 b0 = c.base[0], b1 = c.base[1];
-        load_columns(c, group + (kTwo ? 2 : 1) * units);
+        load_columns(c, group + (S::kTwo ? 2 : 1) * units);
         const int col = group * 32 + q * 8;
         if (col >= a.N)
             return;
@@ -902,9 +909,9 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
                   make_uint4(add_to_bf16x2(b1.x, d[0][2], d[0][3]), add_to_bf16x2(b1.y, d[1][2], d[1][3]),
                              add_to_bf16x2(b1.z, d[2][2], d[2][3]), add_to_bf16x2(b1.w, d[3][2], d[3][3])));
     };
-    for (int group = unit; group < groups; group += (kTwo ? 2 : 1) * units) {
+    for (int group = unit; group < groups; group += (S::kTwo ? 2 : 1) * units) {
         finish(even, group);
-        if (kTwo && group + units < groups)
+        if (S::kTwo && group + units < groups)
             finish(odd, group + units);
     }
     cluster.barrier_wait(std::move(left)); // no CTA leaves while its sums are read
