@@ -1121,7 +1121,7 @@ ep_status_t ep_lora(const void* x, const void* base, const ep_routing_desc_t* ro
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const ep::LoraRows rows = lora_rows(routing, layout, mode, max_tokens_per_expert, num_rows, row_token);
     const int32_t* copied = row_token != nullptr && out != base ? layout->slot : nullptr; // tokens without an adapter
-    if (ep::lora_few(rows)) {
+    if (ep::lora_few(rows, lora->rank)) {
         ep::LoraFewLaunch few{rows, x, lora->a, lora->b, lora->scales, base, out, h, lora->hidden_in, lora->hidden_out,
                               lora->rank, copied};
         return from_cuda(ep::launch_lora_few(few, s));

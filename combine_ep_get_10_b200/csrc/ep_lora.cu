@@ -721,6 +721,7 @@ __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
 constexpr int kFewThreads = 256;
 constexpr int kFewTile = 16; // rows: the warp product's M
 constexpr int kFewCluster = 8;
+constexpr int kFewRank = 64; // largest rank
 
 template <int RP>
 struct FewShape {
@@ -735,8 +736,8 @@ struct FewShape {
 };
 
 // Both products of a forward call for a tile of 16 rows, where an adapter has few
-// rows (a decode step): the bytes are the factors', each of them used once, and
-// what lasts is latency.  A cluster has a tile; its warps split the hidden
+// rows (a decode step): the bytes are the factors', each of them used once or
+// read again from L2, and what lasts is latency.  A cluster has a tile; its warps split the hidden
 // width, add their sums up over the cluster, and split the output columns.  One
 // launch, no shared memory between HBM and the warp product, the first columns'
 // factors and base on their way while u is added up: 128 rows of 64 adapters,
@@ -747,7 +748,7 @@ struct FewShape {
 // needs.  In the same way the columns of out are dealt to the products so that a
 // thread ends with 8 consecutive ones.
 template <int RP>
-__global__ void __launch_bounds__(kFewThreads, RP <= 64 ? 2 : 1) lora_few_kernel(LoraFewLaunch a, int tiles)
+__global__ void __launch_bounds__(kFewThreads, 2) lora_few_kernel(LoraFewLaunch a, int tiles)
 {
     using S = FewShape<RP>;
     extern __shared__ __align__(16) float s_few[];
@@ -807,10 +808,11 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 64 ? 2 : 1) lora_few_kernel
             }
     }
     // base and the factor's rows of 32 columns: column 8 (n / 2) + 2 j + n % 2 is
-    // row n of product j; of each 16 ranks a lane has 4 (of the last 8, 2)
+    // row n of product j; a lane has 8 of each 32 ranks, of what is left 4 of 16
+    // and 2 of 8
     struct Columns {
         uint4 base[2];
-        uint2 w[RP / 16][4];
+        uint2 w[RP / 16][4]; // of 16 ranks
     };
     const auto load_columns = [&](Columns& c, int group) {
         const int col = group * 32 + q * 8;
@@ -823,10 +825,25 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 64 ? 2 : 1) lora_few_kernel
             const int n = group * 32 + 8 * (g / 2) + 2 * j + g % 2;
             const uint16_t* row = wb + static_cast<int64_t>(n) * a.rank;
 #pragma unroll
-            for (int s = 0; s < RP / 16; ++s) {
-                c.w[s][j] = ld_nc_v2_if(row + s * 16 + q * 4, n < a.N && s * 16 + 16 <= a.rank);
-                if (s * 16 + 8 == a.rank) // (uniform: an odd number of eights)
-                    c.w[s][j].x = ld_nc_u32_if(row + s * 16 + q * 2, n < a.N);
+            for (int s = 0; s < RP / 16; s += 2) {
+                if (RP >= 32) {
+                    const uint4 v = ld_nc_v4_if(row + s * 16 + q * 8, n < a.N && s * 16 + 32 <= a.rank);
+                    c.w[s][j] = make_uint2(v.x, v.y);
+                    c.w[(s + 1) % (RP / 16)][j] = make_uint2(v.z, v.w);
+                }
+                if (RP < 32 || s * 16 + 32 > a.rank) { // (uniform) not a whole block
+                    const int whole = s * 16 + 16 <= a.rank ? 1 : 0; // steps of 16 in it
+                    c.w[s][j] = ld_nc_v2_if(row + s * 16 + q * 4, n < a.N && whole == 1);
+                    if (RP >= 32)
+                        c.w[(s + 1) % (RP / 16)][j] = make_uint2(0u, 0u);
+                    if (s * 16 + whole * 16 + 8 == a.rank) {
+                        const uint32_t v = ld_nc_u32_if(row + (s + whole) * 16 + q * 2, n < a.N);
+                        if (whole == 0)
+                            c.w[s][j].x = v;
+                        else if (RP >= 32)
+                            c.w[(s + 1) % (RP / 16)][j].x = v;
+                    }
+                }
             }
         }
     };
@@ -846,25 +863,38 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 64 ? 2 : 1) lora_few_kernel
         *reinterpret_cast<float2*>(p + 8 * S::kWarpPitch) = make_float2(acc[j][2], acc[j][3]);
     }
     __syncthreads();
-    for (int i = tid; i < kFewTile * RP; i += kFewThreads) {
-        const int row = i / RP, j = i % RP;
+    const auto add4 = [](float4& to, const float4& v) {
+        to.x += v.x;
+        to.y += v.y;
+        to.z += v.z;
+        to.w += v.w;
+    };
+    for (int i = tid; i < kFewTile * RP / 4; i += kFewThreads) {
+        const int row = i / (RP / 4), j = i % (RP / 4) * 4;
         const float* p = s_few + j / S::kRanks * S::kWarpSums + row * S::kWarpPitch + j % S::kRanks;
-        float sum = 0.0f;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < 8; w += S::kRankWarps)
-            sum += p[w * S::kWarpSums];
-        s_cta[row * S::kPitch + j] = sum;
+            add4(sum, *reinterpret_cast<const float4*>(p + w * S::kWarpSums));
+        *reinterpret_cast<float4*>(s_cta + row * S::kPitch + j) = sum;
     }
     cluster.sync();
-    for (int i = tid; i < kFewTile * RP; i += kFewThreads) {
-        const int row = i / RP, j = i % RP, at = row * S::kPitch + j;
-        float sum = 0.0f;
-        for (int c = 0; c < parts; ++c)
-            sum += cluster.map_shared_rank(s_cta, c)[at];
-        sum *= scale;
-        s_u[at] = j < a.rank ? sum : 0.0f;
+    for (int i = tid; i < kFewTile * RP / 4; i += kFewThreads) {
+        const int row = i / (RP / 4), j = i % (RP / 4) * 4, at = row * S::kPitch + j;
+        float4 v[kFewCluster]; // all on their way at once
+#pragma unroll
+        for (int c = 0; c < kFewCluster; ++c)
+            v[c] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(s_cta, min(c, parts - 1)) + at);
+        float4 sum = v[0];
+#pragma unroll
+        for (int c = 1; c < kFewCluster; ++c)
+            if (c < parts)
+                add4(sum, v[c]);
+        // (ranks past the last are zeros: their rows of the factor count as zeros)
+        sum = make_float4(scale * sum.x, scale * sum.y, scale * sum.z, scale * sum.w);
+        *reinterpret_cast<float4*>(s_u + at) = sum;
         if (row % parts == part && j < a.rank && rows.begin + row < rows.end)
-            a.u[static_cast<int64_t>(rows.begin + row) * a.rank + j] = sum;
+            *reinterpret_cast<float4*>(a.u + static_cast<int64_t>(rows.begin + row) * a.rank + j) = sum;
     }
     auto left = cluster.barrier_arrive(); // this CTA has read the others' sums
     __syncthreads();
@@ -873,10 +903,11 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 64 ? 2 : 1) lora_few_kernel
     uint32_t hi[RP / 16][4], lo[RP / 16][4];
 #pragma unroll
     for (int s = 0; s < RP / 16; ++s) {
-        const bool half = s * 16 + 8 == a.rank;
+        const bool half = s * 16 + 8 == a.rank, block = RP >= 32 && (s & ~1) * 16 + 32 <= a.rank;
+        const int k = block ? (s & ~1) * 16 + q * 8 + (s & 1) * 4 : s * 16 + q * (half ? 2 : 4); // the lane's first rank
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const float* p = s_u + (g + 8 * r) * S::kPitch + s * 16 + q * (half ? 2 : 4);
+            const float* p = s_u + (g + 8 * r) * S::kPitch + k;
             split_bf16x2(p[0], p[1], hi[s][r], lo[s][r]);
             split_bf16x2(half ? 0.0f : p[2], half ? 0.0f : p[3], hi[s][2 + r], lo[s][2 + r]);
         }
@@ -1395,10 +1426,17 @@ cudaError_t launch_lora_expand(const LoraExpandLaunch& a, cudaStream_t stream)
     });
 }
 
-// Few rows an adapter: no more than a warp product's, on average.
-bool lora_few(const LoraRows& rows)
+// Is a forward call one for lora_few_kernel: by the rows an adapter has on
+// average, the fewer the more ranks its registers have to hold.  Measured at
+// 4096 -> 4096 against the kernels for many rows, us:
+//   rank 16: 16 rows 7.2 / 14.6 and 14.6 / 25.5 (16, 64 adapters), 256 rows 28 / 33
+//   rank 32: 16 rows 8.9 / 15.1, 64 rows 37 / 42 (64 adapters), 256 rows 36 / 34
+//   rank 64: 16 rows 12.8 / 15.7 and 28 / 30, 64 rows 23.9 / 22.2 and 50 / 47
+//   rank 128: 16 rows 30 / 24
+bool lora_few(const LoraRows& rows, int rank)
 {
-    return rows.pairs > 0 && rows.num_rows > 0 && rows.pairs <= kFewTile * static_cast<int64_t>(rows.E);
+    const int most = rank <= 16 ? 256 : (rank <= 32 ? 64 : (rank <= kFewRank ? 16 : 0));
+    return rows.pairs > 0 && rows.num_rows > 0 && rows.pairs <= most * static_cast<int64_t>(rows.E);
 }
 
 cudaError_t launch_lora_few(const LoraFewLaunch& a, cudaStream_t stream)
@@ -1407,10 +1445,15 @@ cudaError_t launch_lora_few(const LoraFewLaunch& a, cudaStream_t stream)
     const int parts = std::max(1, std::min(kFewCluster, 2 * 148 / tiles)); // one resident wave
     const int copies = a.slot != nullptr ? (a.rows.T + kRowTile - 1) / kRowTile : 0;
     const unsigned grid = static_cast<unsigned>(tiles + (copies + parts - 1) / parts) * parts;
-    return with_rank(a.rank, [&](auto rp) {
+    const auto run = [&](auto rp) {
         constexpr int RP = decltype(rp)::value;
         return launch_after<lora_few_kernel<RP>>(grid, kFewThreads, FewShape<RP>::kBytes, parts, stream, a, tiles);
-    });
+    };
+    if (a.rank <= 16)
+        return run(std::integral_constant<int, 16>{});
+    if (a.rank <= 32)
+        return run(std::integral_constant<int, 32>{});
+    return run(std::integral_constant<int, kFewRank>{});
 }
 
 cudaError_t launch_lora_outer(const LoraOuterLaunch& a, cudaStream_t stream)

@@ -78,7 +78,7 @@ struct LoraFewLaunch {
     int32_t K, N, rank;
     const int32_t* slot; // as for LoraExpandLaunch
 };
-bool lora_few(const LoraRows& rows);
+bool lora_few(const LoraRows& rows, int rank);
 cudaError_t launch_lora_few(const LoraFewLaunch& a, cudaStream_t stream);
 
 // da[e][j, n] = sum over e's rows of dh[row, j] * x[row, n]  and
