@@ -952,6 +952,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) lora_few_kernel(LoraFewLaunch 
 constexpr int kOuterThreads = 320; // four warps that load x or dy, four that split u and store, one that multiplies, one that loads u
 constexpr int kOuterRows = 64;     // rows a stage
 constexpr int kOuterCols = 128;    // columns of x or dy a tile: the product's M
+constexpr int kOuterParts = 4;     // CTAs that share a tile's rows, at most
 
 template <int RP>
 struct OuterShape {
@@ -965,6 +966,8 @@ struct OuterShape {
     static constexpr int kCtas = RP <= 64 ? 3 : 2;
     static constexpr int kStages = RP <= 32 ? 3 : 2;
     static constexpr int kBytes = kStages * kStageBytes + 1024; // tiles start on 1024 bytes
+    static constexpr int kPitch = RP + 4;                       // floats a column of a part's sums
+    static_assert(kOuterCols * kPitch * 4 <= kStages * kStageBytes, "a part's sums take the stages' place");
     static constexpr int kTmem = 2 * RP;                        // both terms' sums
     static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
     static constexpr int kUChunks = RP < 64 ? RP / 8 : 8; // 16-byte chunks a row of u's terms
@@ -979,21 +982,27 @@ __device__ __forceinline__ uint32_t in_halves(int row, int c)
 // The output tiles of a call: adapter after adapter, in each the column tiles of
 // db and then of da.  Up to 32 adapters are taken in the order of their rows,
 // most first; CTAs take tiles in turn, forth and back, so that each gets long
-// and short ones.
+// and short ones.  Where there are fewer tiles than places, a cluster has a tile,
+// its CTAs a part of the tile's stages each.
 struct OuterTile {
     RowRange rows;
     int e, n0, stages;
     bool in; // da, from x and dh; else db, from dy and h
 };
 
+template <bool SPLIT>
 struct OuterTiles {
     int in_tiles, out_tiles, total;
+    int parts, part, places, place; // CTAs a tile, which of them; clusters, which of them
     int adapter;   // lane i: the i-th adapter by rows
     RowRange rows; // and its rows
 
     // One warp.
-    __device__ __forceinline__ OuterTiles(const LoraRows& g, int in_tiles_, int out_tiles_, int lane)
-        : in_tiles(in_tiles_), out_tiles(out_tiles_), total(g.E * (in_tiles_ + out_tiles_)), adapter(0), rows{0, 0}
+    __device__ __forceinline__ OuterTiles(const LoraRows& g, int in_tiles_, int out_tiles_, int parts_, int lane)
+        : in_tiles(in_tiles_), out_tiles(out_tiles_), total(g.E * (in_tiles_ + out_tiles_)), parts(SPLIT ? parts_ : 1),
+          part(SPLIT ? static_cast<int>(blockIdx.x) % parts_ : 0),
+          places(static_cast<int>(gridDim.x) / (SPLIT ? parts_ : 1)),
+          place(static_cast<int>(blockIdx.x) / (SPLIT ? parts_ : 1)), adapter(0), rows{0, 0}
     {
         if (g.E > 32)
             return;
@@ -1016,25 +1025,30 @@ struct OuterTiles {
     // Tile k of this CTA; false for none (a later one may be).  One warp.
     __device__ __forceinline__ bool get(const LoraRows& g, int k, OuterTile& t) const
     {
-        const int i = k * static_cast<int>(gridDim.x) +
-                      static_cast<int>((k & 1) != 0 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const int i = k * places + ((k & 1) != 0 ? places - 1 - place : place);
         if (i >= total)
             return false;
-        const int per = in_tiles + out_tiles, place = i / per, tile = i - place * per;
+        const int per = in_tiles + out_tiles, at = i / per, tile = i - at * per;
         t.in = tile >= out_tiles;
         t.n0 = (t.in ? tile - out_tiles : tile) * kOuterCols;
         if (g.E > 32) {
-            t.e = place;
-            t.rows = group_rows(g, place);
+            t.e = at;
+            t.rows = group_rows(g, at);
         } else {
-            t.e = __shfl_sync(kFullMask, adapter, place);
-            t.rows.begin = __shfl_sync(kFullMask, rows.begin, place);
-            t.rows.end = __shfl_sync(kFullMask, rows.end, place);
+            t.e = __shfl_sync(kFullMask, adapter, at);
+            t.rows.begin = __shfl_sync(kFullMask, rows.begin, at);
+            t.rows.end = __shfl_sync(kFullMask, rows.end, at);
         }
         t.stages = (t.rows.end - t.rows.begin + kOuterRows - 1) / kOuterRows;
+        if (SPLIT) {
+            const int mine = (t.stages + parts - 1) / parts;
+            t.rows.begin = min(t.rows.begin + part * mine * kOuterRows, t.rows.end);
+            t.rows.end = min(t.rows.end, t.rows.begin + mine * kOuterRows);
+            t.stages = (t.rows.end - t.rows.begin + kOuterRows - 1) / kOuterRows;
+        }
         return true;
     }
-    __device__ __forceinline__ int rounds() const { return (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x); }
+    __device__ __forceinline__ int rounds() const { return (total + places - 1) / places; }
 };
 
 // The four warps that split u.
@@ -1065,9 +1079,9 @@ __device__ __forceinline__ bool split_warps_any(bool mine)
 // two bf16 tiles (hi, lo) that one product takes side by side.  Sums stay in
 // tensor memory until the last row; there the two terms' are added.  The warps
 // that load run on into the next tile's stages while a tile is stored.
-template <int RP>
+template <int RP, bool SPLIT>
 __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
-    lora_outer_kernel(LoraOuterLaunch a, int in_tiles, int out_tiles)
+    lora_outer_kernel(LoraOuterLaunch a, int in_tiles, int out_tiles, int parts)
 {
     using S = OuterShape<RP>;
     extern __shared__ uint8_t smem_raw[];
@@ -1095,7 +1109,7 @@ __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = s_tmem;
-    const OuterTiles tiles(a.rows, in_tiles, out_tiles, lane);
+    const OuterTiles<SPLIT> tiles(a.rows, in_tiles, out_tiles, parts, lane);
     const int rounds = tiles.rounds();
     OuterTile t;
     bool alive = true; // no wait has run out
@@ -1243,6 +1257,26 @@ __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
                 ++sums;
                 tc_fence_after_sync();
             }
+            if (SPLIT) { // this part's sums, where the stages were
+#pragma unroll
+                for (int j0 = 0; j0 < RP; j0 += 16) {
+                    float hi[16], lo[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        hi[i] = lo[i] = 0.0f;
+                    if (t.stages > 0) {
+                        const uint32_t from = tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + j0;
+                        tmem_load16(hi, from);
+                        tmem_load16(lo, from + RP);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<float4*>(smem + (st * S::kPitch + j0 + i) * 4) =
+                            make_float4(hi[i] + lo[i], hi[i + 1] + lo[i + 1], hi[i + 2] + lo[i + 2], hi[i + 3] + lo[i + 3]);
+                }
+                tc_fence_before_sync();
+                break; // a cluster has one tile
+            }
             // thread: column n0 + st, every rank
             const int N = t.in ? a.hidden_in : a.hidden_out, col = t.n0 + st;
             uint16_t* out = static_cast<uint16_t*>(t.in ? a.da : a.db) + static_cast<int64_t>(t.e) * a.rank * N;
@@ -1287,6 +1321,43 @@ __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
     __syncthreads();
     if (warp == 8)
         tmem_free(tmem, S::kTmem);
+    if (SPLIT && tiles.get(a.rows, 0, t)) { // the parts' sums, in their order; a part has its share of the columns
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        const int N = t.in ? a.hidden_in : a.hidden_out;
+        const int share = (kOuterCols + parts - 1) / parts, c0 = tiles.part * share, cols = min(share, kOuterCols - c0);
+        uint16_t* out = static_cast<uint16_t*>(t.in ? a.da : a.db) + static_cast<int64_t>(t.e) * a.rank * N;
+        for (int i = tid; i < cols * (a.rank / 8); i += kOuterThreads) {
+            const int c = c0 + i % cols, j = i / cols * 8, col = t.n0 + c;
+            float4 v[kOuterParts][2]; // all on their way at once
+#pragma unroll
+            for (int p = 0; p < kOuterParts; ++p) {
+                const float4* from = reinterpret_cast<const float4*>(
+                    cluster.map_shared_rank(smem, min(p, parts - 1)) + (c * S::kPitch + j) * 4);
+                v[p][0] = from[0];
+                v[p][1] = from[1];
+            }
+            float4 s0 = v[0][0], s1 = v[0][1];
+#pragma unroll
+            for (int p = 1; p < kOuterParts; ++p)
+                if (p < parts) {
+                    s0 = make_float4(s0.x + v[p][0].x, s0.y + v[p][0].y, s0.z + v[p][0].z, s0.w + v[p][0].w);
+                    s1 = make_float4(s1.x + v[p][1].x, s1.y + v[p][1].y, s1.z + v[p][1].z, s1.w + v[p][1].w);
+                }
+            if (col >= N)
+                continue;
+            const uint32_t d[4] = {pack_bf16x2(s0.x, s0.y), pack_bf16x2(s0.z, s0.w), pack_bf16x2(s1.x, s1.y),
+                                   pack_bf16x2(s1.z, s1.w)};
+            if (t.in) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    out[static_cast<int64_t>(j + k) * N + col] = static_cast<uint16_t>(d[k / 2] >> (16 * (k & 1)));
+            } else {
+                st_v4(out + static_cast<int64_t>(col) * a.rank + j, make_uint4(d[0], d[1], d[2], d[3]));
+            }
+        }
+        cluster.sync(); // no CTA leaves while its sums are read
+    }
 }
 
 // -------------------------------------------------------------- row tokens
@@ -1464,8 +1535,19 @@ cudaError_t launch_lora_outer(const LoraOuterLaunch& a, cudaStream_t stream)
         const int in_tiles = (a.hidden_in + kOuterCols - 1) / kOuterCols;
         const int out_tiles = (a.hidden_out + kOuterCols - 1) / kOuterCols;
         const int64_t total = static_cast<int64_t>(a.rows.E) * (in_tiles + out_tiles);
-        const unsigned grid = static_cast<unsigned>(std::min<int64_t>(total, 148 * S::kCtas));
-        return launch_after<lora_outer_kernel<RP>>(grid, kOuterThreads, S::kBytes, 1, stream, a, in_tiles, out_tiles);
+        // Fewer tiles than places (one adapter, narrow layers): parts of kPartStages
+        // stages and more.  4096 rows of one adapter, rank 64, 4096 -> 4096: all
+        // gradients 66 us, whole tiles 99; 512 rows, rank 32, 7168 -> 7168: in two
+        // parts of four stages 28 us, whole 24 (a cluster starts later and joins).
+        constexpr int kPartStages = 8;
+        const int64_t places = 148 * S::kCtas, stages = a.rows.pairs / a.rows.E / kOuterRows;
+        const int parts = static_cast<int>(std::max<int64_t>(
+            1, std::min({static_cast<int64_t>(kOuterParts), places / total, stages / kPartStages})));
+        if (parts > 1)
+            return launch_after<lora_outer_kernel<RP, true>>(static_cast<unsigned>(total * parts), kOuterThreads, S::kBytes,
+                                                             parts, stream, a, in_tiles, out_tiles, parts);
+        return launch_after<lora_outer_kernel<RP, false>>(static_cast<unsigned>(std::min(total, places)), kOuterThreads,
+                                                          S::kBytes, 1, stream, a, in_tiles, out_tiles, 1);
     });
 }
 

@@ -458,3 +458,19 @@ def test_few_rows_an_adapter(rank, T, E):
         keep[tokens] = False
         assert torch.equal(out2.cpu()[keep], out.cpu()[keep]) and bool((out2.cpu()[tokens] == 5.0).all())
         assert not bool(h2.cpu()[bad].any())
+
+
+@pytest.mark.parametrize("rank", [8, 32, 56, 128])
+def test_gradients_of_long_groups_in_parts(rank):
+    """One adapter, or a few of very different sizes, whose rows several CTAs
+    share: every part counts, empty ones too, and the sums are the same bytes
+    every time."""
+    for idx in (torch.zeros((1900, 1), dtype=torch.int64), ids(1700, 1, 38, none=0.2),
+                torch.cat([torch.zeros(2400), torch.ones(3), torch.full((200,), 2.0), torch.full((70,), -1.0)])
+                .long()[torch.randperm(2673, generator=torch.Generator().manual_seed(39))][:, None]):
+        c = Case(idx, int(idx.max()) + 1, rank, 136, 328, 40)
+        c.check_backward()
+        _, h, _, _ = c.ref.forward(c.x, None, torch.zeros((c.x.shape[0], c.hout)))
+        first, again = (c.backward(h.float().cuda()) for _ in range(2))
+        for a, b in zip(first, again):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
