@@ -771,6 +771,8 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch 
     extern __shared__ float s_q[];
     __shared__ float s_z[kBalanceWarps], s_red[kBalanceWarps];
     __shared__ int s_n[kBalanceWarps];
+    __shared__ Chunk s_chunk;
+    __shared__ int64_t s_total;
     pdl_wait();
     if (finish)
         pdl_launch_dependents(); // balance_finish_kernel, which waits for this grid
@@ -779,8 +781,17 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch 
     int* s_cnt = reinterpret_cast<int*>(s_q + kBalanceWarps * E);
     const int64_t chunks = most_chunks(T, S);
     const BalanceSums part = balance_sums(a.workspace, chunks, E);
-    Chunk c{};
-    const int64_t total = find_chunk(a.seq_offsets, T, S, chunk, blockIdx.x, lane, c);
+    if (warp == 0) {
+        Chunk found{};
+        const int64_t n = find_chunk(a.seq_offsets, T, S, chunk, blockIdx.x, lane, found);
+        if (lane == 0) {
+            s_chunk = found;
+            s_total = n;
+        }
+    }
+    __syncthreads();
+    const Chunk c = s_chunk;
+    const int64_t total = s_total;
     const bool sound = total <= chunks; // else the offsets are not sorted: no sequence has tokens
     for (int64_t s = blockIdx.x; s < S; s += gridDim.x) { // sequences without tokens
         const TokenRange r = seq_range(a.seq_offsets, T, static_cast<int>(s));
@@ -913,10 +924,15 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(Balance
     const int64_t chunks = most_chunks(T, S);
     const BalanceSums part = balance_sums(a.workspace, chunks, E);
     // (what it reads before the wait is older than the kernel that it waits for)
+    const TokenRange own = seq_range(a.seq_offsets, T, s);
+    if (own.end - own.begin <= chunk) { // one chunk at most: there are many of these where there are many sequences
+        pdl_wait();
+        return; // the whole cluster
+    }
     const SeqChunks c = find_seq_chunks(a.seq_offsets, T, S, chunk, s, lane);
     pdl_wait();
-    if (c.of <= 1 || c.total > chunks)
-        return; // the whole cluster
+    if (c.total > chunks)
+        return;
     const int per = (E + kFinishCluster - 1) / kFinishCluster, e0 = min(rank * per, E), n_e = min(per, E - e0);
     for (int x = lane; x < n_e; x += 32) {
         float q = 0.0f;

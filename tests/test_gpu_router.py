@@ -448,3 +448,38 @@ def test_statistics_buffers_are_checked_when_set():
         B.ep_balance_loss(logits, r, idx, stats, seq_offsets=torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):  # of another number of experts
         B.ep_balance_loss(torch.zeros((4, 9), device="cuda"), B.Router(9, 2), idx, B.BalanceStats(r, 64))
+
+
+def test_many_sequences():
+    """More sequences than tokens: most are empty, each is right."""
+    T, E, K, S = 3000, 24, 3, 5000
+    logits, g = make(T, E, torch.float32, 23)
+    off = [0] + sorted(torch.randint(0, T + 1, (S - 1,), generator=g).tolist()) + [T]
+    off[10:20] = [off[9]] * 10
+    idx = logits.topk(K, dim=1).indices
+    router = B.Router(E, K)
+    stats = B.BalanceStats(router, T, num_seqs=S)
+    o = torch.tensor(off, dtype=torch.int32)
+    B.ep_balance_loss(logits.cuda(), router, idx.cuda(), stats, seq_offsets=o.cuda())
+    n = (o[1:] - o[:-1]).long()
+    assert torch.equal(stats.seq_tokens.cpu().long(), n)
+    seq = torch.repeat_interleave(torch.arange(S), n)
+    counts = torch.zeros((S, E), dtype=torch.int64).index_add_(0, seq, torch.nn.functional.one_hot(idx, E).sum(dim=1))
+    assert torch.equal(stats.counts.cpu().long(), counts)
+    p = torch.softmax(logits.double(), dim=1)
+    mean = torch.zeros((S, E), dtype=torch.float64).index_add_(0, seq, p) / n.clamp(min=1)[:, None]
+    assert torch.all((stats.mean_scores.cpu().double() - mean).abs() <= 2 * RTOL * mean)
+    want = (counts * mean).sum(dim=1) * E / (K * n.clamp(min=1))
+    assert torch.all((stats.losses[:, 0].cpu().double() - want).abs() <= 3 * RTOL * want)
+    d = torch.empty_like(logits, device="cuda")
+    dl = torch.rand((S, 2), generator=g)
+    B.ep_router_backward(logits.cuda(), router, idx.cuda(), d, stats=stats, d_losses=dl.cuda(), seq_offsets=o.cuda())
+    x = logits.double().requires_grad_(True)
+    q = torch.softmax(x, dim=1)
+    m = torch.zeros((S, E), dtype=torch.float64).index_add(0, seq, q) / n.clamp(min=1)[:, None]
+    z = torch.zeros(S, dtype=torch.float64).index_add(0, seq, torch.logsumexp(x, dim=1) ** 2) / n.clamp(min=1)
+    total = (dl[:, 0].double() * (counts * m).sum(dim=1) * E / (K * n.clamp(min=1)) + dl[:, 1].double() * z).sum()
+    rd, = torch.autograd.grad(total, x)
+    # a term is at most gb * counts, or 2 |lse| of the z loss (|lse| <= 16), over the sequence's tokens
+    size = (dl[seq, 0].double() * E / (K * n[seq] ** 2) * counts[seq].amax(dim=1) + dl[seq, 1].double() * 32 / n[seq])
+    assert torch.all((d.cpu().double() - rd).abs() <= 4 * RTOL * size[:, None])
