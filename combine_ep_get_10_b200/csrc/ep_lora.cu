@@ -9,7 +9,8 @@
 //   expand  out = base + u W   rank-long sum, hidden columns, base and out move
 //   outer   dW = sum of rows   sum over a group's rows
 // All on tcgen05 with bf16 operands and fp32 sums in tensor memory; u (fp32)
-// enters as hi + lo (ep_mma.cuh), which keeps 16 bits of it.
+// enters as hi + lo (ep_mma.cuh), which keeps 16 bits of it.  Where adapters have
+// few rows, a kernel of its own does shrink and expand at once (few).
 //
 // Rows come by cp.async, 16 bytes a lane: as fast for 128 bytes a row at a time
 // as for 512 (4.75 TB/s for 4096 x 7168 read, 5.2 TB/s read and written), and
@@ -1503,7 +1504,7 @@ cudaError_t launch_lora_expand(const LoraExpandLaunch& a, cudaStream_t stream)
 //   rank 16: 16 rows 7.2 / 14.6 and 14.6 / 25.5 (16, 64 adapters), 256 rows 28 / 33
 //   rank 32: 16 rows 8.9 / 15.1, 64 rows 37 / 42 (64 adapters), 256 rows 36 / 34
 //   rank 64: 16 rows 12.8 / 15.7 and 28 / 30, 64 rows 23.9 / 22.2 and 50 / 47
-//   rank 128: 16 rows 30 / 24
+//   rank 128: 16 rows 30 / 24 (not kept)
 bool lora_few(const LoraRows& rows, int rank)
 {
     const int most = rank <= 16 ? 256 : (rank <= 32 ? 64 : (rank <= kFewRank ? 16 : 0));
