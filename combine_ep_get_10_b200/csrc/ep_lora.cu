@@ -1499,16 +1499,22 @@ cudaError_t launch_lora_expand(const LoraExpandLaunch& a, cudaStream_t stream)
 }
 
 // Is a forward call one for lora_few_kernel: by the rows an adapter has on
-// average, the fewer the more ranks its registers have to hold.  Measured at
-// 4096 -> 4096 against the kernels for many rows, us:
+// average, the fewer the more ranks its registers have to hold, or by all rows,
+// where the other kernels' starts and ends weigh more.  Measured at 4096 -> 4096
+// against the kernels for many rows, us:
 //   rank 16: 16 rows 7.2 / 14.6 and 14.6 / 25.5 (16, 64 adapters), 256 rows 28 / 33
 //   rank 32: 16 rows 8.9 / 15.1, 64 rows 37 / 42 (64 adapters), 256 rows 36 / 34
 //   rank 64: 16 rows 12.8 / 15.7 and 28 / 30, 64 rows 23.9 / 22.2 and 50 / 47
 //   rank 128: 16 rows 30 / 24 (not kept)
+//   one adapter, rank 16: 1024 rows 10.4 / 16.3, 4096 rows 28 / 29 (and 45 / 42 at 7168)
+//   8 adapters, rank 32: 768 rows 13 / 17; 64 adapters 6144 rows 65 / 57
+//   one adapter, rank 64: 128 rows 9.2 / 10.9, 256 rows 12.0 / 11.7
 bool lora_few(const LoraRows& rows, int rank)
 {
-    const int most = rank <= 16 ? 256 : (rank <= 32 ? 64 : (rank <= kFewRank ? 16 : 0));
-    return rows.pairs > 0 && rows.num_rows > 0 && rows.pairs <= most * static_cast<int64_t>(rows.E);
+    if (rank > kFewRank || rows.pairs == 0 || rows.num_rows == 0)
+        return false;
+    const int64_t each = rank <= 16 ? 256 : (rank <= 32 ? 64 : 16), all = rank <= 32 ? 2048 : 128;
+    return rows.pairs <= std::max(each * rows.E, all);
 }
 
 cudaError_t launch_lora_few(const LoraFewLaunch& a, cudaStream_t stream)

@@ -474,3 +474,13 @@ def test_gradients_of_long_groups_in_parts(rank):
         first, again = (c.backward(h.float().cuda()) for _ in range(2))
         for a, b in zip(first, again):
             assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_both_sides_of_the_choice_of_kernels():
+    """Forward calls just within and just past the limits in rows at which the
+    kernel for few rows gives way to those for many."""
+    for rank, E, T in ((16, 1, 2048), (16, 1, 2049), (32, 3, 2048), (32, 3, 2049), (64, 2, 128), (64, 2, 129),
+                       (8, 9, 2304), (8, 9, 2305), (40, 20, 320), (40, 20, 321), (72, 20, 40)):
+        c = Case(ids(T, E, T, none=0.05), E, rank, 136, 200, 41)
+        c.check_forward()
+        c.check_forward("in place")
