@@ -759,6 +759,8 @@ def _lora_rows(routing: Routing, layout: Layout, lora: Lora, first: torch.Tensor
     """(device, rows of the row buffer, rows of x / base / out, address of the
     row table), after checking them."""
     dev = _device_of(first)
+    if isinstance(layout, LayoutView):
+        raise ValueError("the layout is a view of some of its tokens; the adapters' rows are those of a whole layout")
     if routing.E != lora.E:
         raise ValueError("the routing names %d adapters, the factors are of %d" % (routing.E, lora.E))
     if lora.index != dev:
@@ -785,7 +787,8 @@ def ep_lora(x: torch.Tensor, routing: Routing, layout: Layout, lora: Lora, out: 
     bf, wide = torch.bfloat16, (n, lora.hidden_out)
     _check(lib().ep_lora(_arg("x", x, bf, (n, lora.hidden_in), dev),
                          None if base is None else _arg("base", base, bf, wide, dev),
-                         ctypes.byref(routing.desc), ctypes.byref(layout.desc), mode, max_tokens_per_expert, rows, table,
+                         ctypes.byref(routing.desc), ctypes.byref(layout.desc), int(mode), int(max_tokens_per_expert),
+                         rows, table,
                          lora.ref, _arg("out", out, bf, wide, dev), _arg("h", h, torch.float32, (rows, lora.rank), dev),
                          _stream(stream)), "ep_lora")
 
@@ -803,7 +806,7 @@ def ep_lora_backward(dy: torch.Tensor, x, h, routing: Routing, layout: Layout, l
         _arg("dy", dy, bf, (n, hout), dev), None if x is None else _arg("x", x, bf, inner, dev),
         None if h is None else _arg("h", h, torch.float32, (max(rows, h.shape[0]), r), dev),
         None if dx_base is None else _arg("dx_base", dx_base, bf, inner, dev), ctypes.byref(routing.desc),
-        ctypes.byref(layout.desc), mode, max_tokens_per_expert, rows, table, lora.ref,
+        ctypes.byref(layout.desc), int(mode), int(max_tokens_per_expert), rows, table, lora.ref,
         _arg("dh", dh, torch.float32, (rows, r), dev), None if dx is None else _arg("dx", dx, bf, inner, dev),
         None if da is None else _arg("da", da, bf, (E, r, hin), dev),
         None if db is None else _arg("db", db, bf, (E, hout, r), dev), _stream(stream)), "ep_lora_backward")

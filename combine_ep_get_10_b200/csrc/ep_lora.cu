@@ -144,18 +144,28 @@ __device__ __forceinline__ bool find_tile(const LoraRows& g, int i, int lane, in
     return true;
 }
 
-// Rows that the routing fills past num_rows are left out; the first CTA of a
-// call's first kernel says so.  One warp.
+// Rows that the routing fills past num_rows are left out, and so may be rows
+// where the layout has more than the routing has pairs (it is another routing's,
+// or the routing is a part of the layout's); the first CTA of a call's first
+// kernel says so.  One warp.
 __device__ __forceinline__ void report_overflow(const LoraRows& g, int lane)
 {
     bool over = false;
+    int64_t total = 0;
     for (int e = lane; e < g.E; e += 32) {
-        const int64_t end = g.mode == EP_LAYOUT_COMPACT ? static_cast<int64_t>(__ldg(g.offsets + e + 1))
-                                                        : static_cast<int64_t>(e) * g.max_tokens + __ldg(g.counts + e);
-        const bool full = g.mode != EP_LAYOUT_COMPACT && __ldg(g.counts + e) > g.max_tokens;
-        over = over || full || (end > g.num_rows && (g.mode == EP_LAYOUT_COMPACT || __ldg(g.counts + e) > 0));
+        if (g.mode == EP_LAYOUT_COMPACT) {
+            const int end = __ldg(g.offsets + e + 1);
+            over = over || end > g.num_rows;
+            total += end - __ldg(g.offsets + e);
+        } else {
+            const int n = __ldg(g.counts + e);
+            over = over || n > g.max_tokens || (n > 0 && static_cast<int64_t>(e) * g.max_tokens + n > g.num_rows);
+            total += n;
+        }
     }
-    if (over)
+    for (int d = 16; d >= 1; d >>= 1)
+        total += __shfl_xor_sync(kFullMask, total, d);
+    if (over || total > g.pairs)
         flag_error(g.err, EP_DEVERR_OVERFLOW);
 }
 

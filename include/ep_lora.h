@@ -50,7 +50,9 @@ extern "C" {
  * Limits: rank a multiple of 8, 8 <= rank <= 128; hidden_in and hidden_out
  * positive multiples of 8; E <= 1024; x, a, b, base, out, h and the gradients
  * 16-byte aligned.  Rows at or past num_rows are skipped with
- * EP_DEVERR_OVERFLOW.
+ * EP_DEVERR_OVERFLOW.  The layout is the routing's own: one that has rows of
+ * more pairs than the routing (of which the routing is a part) is flagged so
+ * too, and some of its rows are skipped.
  * ---------------------------------------------------------------------- */
 typedef struct {
     int32_t rank;

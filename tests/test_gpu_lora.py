@@ -484,3 +484,15 @@ def test_both_sides_of_the_choice_of_kernels():
         c = Case(ids(T, E, T, none=0.05), E, rank, 136, 200, 41)
         c.check_forward()
         c.check_forward("in place")
+
+
+def test_a_part_of_a_routing_with_the_whole_layout_is_flagged_or_refused():
+    c = Case(ids(700, 4, 42, none=0.0), 4, 16, 128, 128, 43, tokens=False)
+    part = c.routing.tokens(0, 100)
+    out, h = torch.zeros((c.num_rows, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((c.num_rows, 16), device="cuda")
+    B.ep_lora(c.x.cuda(), c.routing, c.layout, c.lora, out, h)
+    assert B.ep_get_device_error(c.layout) == 0
+    B.ep_lora(c.x.cuda(), part, c.layout, c.lora, out, h)
+    assert B.ep_get_device_error(c.layout) == B.EP_DEVERR_OVERFLOW
+    with pytest.raises(ValueError):
+        B.ep_lora(c.x.cuda(), part, B.layout_tokens(c.layout, c.routing, 0, 100), c.lora, out, h)
