@@ -9,7 +9,10 @@
 //   expand  out = base + u W   rank-long sum, hidden columns, base and out move
 //   outer   dW = sum of rows   sum over a group's rows
 // All on tcgen05 with bf16 operands and fp32 sums in tensor memory; u (fp32)
-// enters as hi + lo (ep_mma.cuh), which keeps 16 bits of it.  Where adapters have
+// enters as three bf16 terms (ep_mma.cuh), which keep all of its 24 bits.  The
+// tensor core cuts a sum, where fp32 arithmetic rounds it: n additions in a row
+// are off by about n / 4 * 2^-24, all towards zero (256: 4e-6).  So a chain has 16
+// products, and chains are added up in fp32 registers.  Where adapters have
 // few rows, a kernel of its own does shrink and expand at once (few).
 //
 // Rows come by cp.async, 16 bytes a lane: as fast for 128 bytes a row at a time
@@ -17,6 +20,9 @@
 // any row may be anywhere.  Factors come through tensor maps, which lay them
 // out as the tensor core reads them and fill what is past the rank, the width
 // or the last column with zeros.
+//
+// Tensor memory is never waited for: no CTAs of these kernels that fit an SM
+// together need more than its 512 columns.
 //
 // The kernels of a call are programmatic dependents of one another: what does
 // not depend on the kernel before (which rows, the first tiles of base and of
@@ -215,12 +221,17 @@ __device__ __forceinline__ int row_at(const LoraRows& g, int row, int end)
 }
 
 // ------------------------------------------------------------------ shrink
-constexpr int kShrinkThreads = 192; // four warps that load x and store, one that multiplies, one that loads w
 constexpr int kShrinkTile = 64; // rows
 constexpr int kDepth = 128;     // hidden channels a stage, in tiles of 64
+constexpr int kShrinkChain = 2; // stages whose products are summed in tensor memory
 
 template <int RP>
 struct ShrinkShape {
+    // warps 0 .. 3 load x, 4 and 5 (and 8 and 9: ranks 64 ..) add the chains up, 6
+    // multiplies, 7 loads w
+    static constexpr int kSumWarps = RP <= 64 ? 2 : 4;
+    static constexpr int kThreads = RP <= 64 ? 256 : 320;
+    static constexpr int kSumRanks = RP <= 64 ? RP : 64; // a warp of those
     static constexpr int kStages = RP <= 32 ? 4 : (RP == 64 ? 3 : 2); // two CTAs an SM
     static constexpr int kHalfBytes = kShrinkTile * 128; // 64 channels of x
     static constexpr int kXBytes = kShrinkTile * kDepth * 2;
@@ -232,7 +243,7 @@ struct ShrinkShape {
     static constexpr int kBehind = kHalfBytes - kWBytes; // past the last stage
     static constexpr int kBytes = kStages * kStageBytes + (kBehind > 0 ? kBehind : 0) + 1024;
     static_assert(kSumBytes <= kStages * kStageBytes, "the sums take the stages' place");
-    static constexpr int kCols = RP < 32 ? 32 : RP; // tensor memory
+    static constexpr int kCols = 2 * RP; // tensor memory: two chains' sums
     static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
     static constexpr int kWBox = RP < 64 ? RP : 64; // ranks a box of w [K, rank]
 };
@@ -246,15 +257,17 @@ struct ShrinkShape {
 // same sum every time, no atomics, no partial sums in HBM).  Four warps copy
 // the rows of x from where they are, a thread brings the factor's slice, and
 // another multiplies from shared memory into tensor memory: what
-// is in flight is bounded by the stages alone.  The product has 128 rows: what lies behind a
-// stage's 64 gives sums that nobody reads.
+// is in flight is bounded by the stages alone.  Chains of kShrinkChain stages
+// alternate between two places in tensor memory; while one is summed, two warps
+// (rows 0 .. 31 and 32 .. 63) add the other one to their registers.  The product has
+// 128 rows: what lies behind a stage's 64 gives sums that nobody reads.
 template <int RP, bool TRANS>
-__global__ void __launch_bounds__(kShrinkThreads)
+__global__ void __launch_bounds__(ShrinkShape<RP>::kThreads, 2)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap w_map, LoraShrinkLaunch a)
 {
     using S = ShrinkShape<RP>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t s_full[S::kStages], s_free[S::kStages], s_done;
+    __shared__ uint64_t s_full[S::kStages], s_free[S::kStages], s_sums[2], s_taken[2];
     __shared__ uint32_t s_tmem;
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = static_cast<int>(cluster.num_blocks()), part = static_cast<int>(cluster.block_rank());
@@ -267,7 +280,10 @@ __global__ void __launch_bounds__(kShrinkThreads)
             mbar_init(&s_full[i], 129);
             mbar_init(&s_free[i], 1);
         }
-        mbar_init(&s_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_sums[i], 1);
+            mbar_init(&s_taken[i], S::kSumWarps);
+        }
         fence_mbar_init();
     }
     pdl_wait();
@@ -306,15 +322,18 @@ __global__ void __launch_bounds__(kShrinkThreads)
         }
         fence_proxy_async_shared();
     }
-    if (warp == 4)
+    if (warp == 6)
         tmem_alloc(&s_tmem, S::kCols);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = s_tmem;
 
+    const bool sums_up = warp == 4 || warp == 5 || warp >= 8;
+    const int ranks0 = warp >= 8 ? 64 : 0; // of a warp that adds up
+    float total[S::kSumRanks];
+    bool alive = true; // no wait has run out
     if (warp < 4) {
-        bool alive = true; // no wait has run out
         for (int i = 0; i < n; ++i) {
             const int stage = i % S::kStages;
             if (i >= S::kStages && alive)
@@ -329,7 +348,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
             cp_async_arrive(&s_full[stage]);
         }
         cp_async_wait_all();
-    } else if (warp == 5) {
+    } else if (warp == 7) {
         for (int i = 0; lane == 0 && i < n; ++i) {
             const int stage = i % S::kStages, k = (part + i * parts) * kDepth;
             if (i >= S::kStages && !mbar_wait_bounded(&s_free[stage], (i / S::kStages - 1) & 1, a.rows.err))
@@ -345,11 +364,35 @@ __global__ void __launch_bounds__(kShrinkThreads)
                     tma_load3(ws + j * kDepth * 2, &w_map, j, k, e, &s_full[stage]);
             }
         }
+    } else if (sums_up) {
+#pragma unroll
+        for (int j = 0; j < S::kSumRanks; ++j)
+            total[j] = 0.0f;
+        const uint32_t from = tmem + (static_cast<uint32_t>((warp & 1) * 32) << 16) + ranks0;
+        for (int chain = 0; chain * kShrinkChain < n; ++chain) {
+            if (alive)
+                alive = mbar_wait_bounded(&s_sums[chain & 1], (chain / 2) & 1, a.rows.err);
+            tc_fence_after_sync();
+#pragma unroll
+            for (int j = 0; j < S::kSumRanks; j += 16) {
+                float d[16];
+                tmem_load16(d, from + (chain & 1) * RP + j);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    total[j + i] += d[i];
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&s_taken[chain & 1]);
+        }
     } else if (lane == 0) {
         constexpr uint32_t desc = product_desc(128, RP, false, TRANS);
         for (int i = 0; i < n; ++i) {
-            const int stage = i % S::kStages;
+            const int stage = i % S::kStages, chain = i / kShrinkChain, link = i % kShrinkChain;
             if (!mbar_wait_bounded(&s_full[stage], (i / S::kStages) & 1, a.rows.err))
+                break;
+            if (link == 0 && chain >= 2 && !mbar_wait_bounded(&s_taken[chain & 1], (chain / 2 - 1) & 1, a.rows.err))
                 break;
             fence_proxy_async_shared(); // the copies were the other threads'
             tc_fence_after_sync();
@@ -360,43 +403,31 @@ __global__ void __launch_bounds__(kShrinkThreads)
                 const uint64_t wd = TRANS ? operand_desc(ws + kk * 2 * S::kWBox * 16, S::kSwizzle, kDepth * S::kWBox * 2,
                                                          S::kWBox * 16)
                                           : operand_desc(ws + kk / 4 * RP * 128 + kk % 4 * 32, Swizzle::k128, 0, 1024);
-                tc_product(tmem, xd, wd, desc, i > 0 || kk > 0);
+                tc_product(tmem + (chain & 1) * RP, xd, wd, desc, link > 0 || kk > 0);
             }
-            tc_commit(i == n - 1 ? &s_done : &s_free[stage]);
+            if (i + S::kStages < n)
+                tc_commit(&s_free[stage]);
+            if (link == kShrinkChain - 1 || i == n - 1)
+                tc_commit(&s_sums[chain & 1]);
         }
     }
     __syncwarp();
-    if (n > 0)
-        mbar_wait_bounded(&s_done, 0, a.rows.err);
-    tc_fence_after_sync();
-    __syncthreads();
+    __syncthreads(); // the last chain has been added: no product reads the stages any more
 
     // the tile's partial sums to shared memory, then the cluster's sums of them
     float* sums = reinterpret_cast<float*>(smem);
-    if (warp < 2) {
+    if (sums_up) {
+        float* row = sums + ((warp & 1) * 32 + lane) * S::kPitch + ranks0;
 #pragma unroll
-        for (int j = 0; j < RP; j += 16) {
-            float d[16];
-            if (n > 0) {
-                tmem_load16(d, tmem + (static_cast<uint32_t>(warp * 32) << 16) + j);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    d[i] = 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(sums + tid * S::kPitch + j + i) =
-                    make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
-        }
-        tc_fence_before_sync();
+        for (int j = 0; j < S::kSumRanks; j += 4)
+            *reinterpret_cast<float4*>(row + j) = make_float4(total[j], total[j + 1], total[j + 2], total[j + 3]);
     }
     cluster.sync();
-    if (warp == 4)
+    if (warp == 6)
         tmem_free(tmem, S::kCols);
     const float scale = a.scales != nullptr ? __ldg(a.scales + e) : 1.0f;
     const int vecs = a.rank / 4;
-    for (int i = part * kShrinkThreads + tid; i < live * vecs; i += parts * kShrinkThreads) {
+    for (int i = part * S::kThreads + tid; i < live * vecs; i += parts * S::kThreads) {
         const int row = i / vecs, v = i - row * vecs;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int c = 0; c < parts; ++c) {
@@ -504,13 +535,26 @@ __device__ __forceinline__ void copy_base_rows(const LoraRows& g, const int32_t*
     }
 }
 
+// The three terms of 8 consecutive values, `stride` bytes from term to term.
+__device__ __forceinline__ void store_terms(uint8_t* to, int stride, float4 f0, float4 f1)
+{
+    uint32_t x[3], y[3], z[3], w[3];
+    split_bf16x2(f0.x, f0.y, x);
+    split_bf16x2(f0.z, f0.w, y);
+    split_bf16x2(f1.x, f1.y, z);
+    split_bf16x2(f1.z, f1.w, w);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        *reinterpret_cast<uint4*>(to + i * stride) = make_uint4(x[i], y[i], z[i], w[i]);
+}
+
 template <int RP>
 struct ExpandShape {
     static constexpr int kTermBytes = kExpandTile * RP * 2; // one bf16 tile of u
     static constexpr int kWBytes = kExpandCols * RP * 2;
     static constexpr int kWStages = RP == 16 ? 6 : (RP == 32 ? 4 : 3); // three at least: one ahead of the step that loads
     static constexpr int kTileBytes = 8 * 32 * 64;          // base: 32 rows of 64 bytes a warp
-    static constexpr int kTilesAt = 2 * kTermBytes + kWStages * kWBytes;
+    static constexpr int kTilesAt = 3 * kTermBytes + kWStages * kWBytes;
     static constexpr int kBytes = kTilesAt + 2 * kTileBytes + 1024; // operands start on 1024 bytes
     static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
     static constexpr int kBox = RP < 64 ? RP : 64; // ranks a row of u's tiles, and of a box of w [N, rank]
@@ -527,7 +571,8 @@ __device__ __forceinline__ uint32_t add_to_bf16x2(uint32_t base, float a, float 
 // the first of an SM's two starts beside the shrink's CTAs.
 //
 // A CTA has one tile of rows and every parts-th column step.  u stays in shared
-// memory as two bf16 tiles (hi, lo).  While one thread has the factor's next
+// memory as three bf16 tiles, one a term; the small terms' products are summed
+// first, so that few additions cut the large sum.  While one thread has the factor's next
 // columns multiplied into one of two places in tensor memory, eight warps take the other one (32 rows and 32 columns each):
 // a thread adds a row's sums to base in shared memory, then the warp stores its
 // rows from there, four lanes 32 columns, and asks for base's tile after next.
@@ -548,7 +593,7 @@ __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
         return;
     }
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    const uint32_t us = smem_addr(smem), ws0 = us + 2 * S::kTermBytes;
+    const uint32_t us = smem_addr(smem), ws0 = us + 3 * S::kTermBytes;
     if (tid == 256) {
         prefetch_map(&w_map);
         for (int i = 0; i < S::kWStages; ++i)
@@ -617,25 +662,21 @@ __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
     if (a.after_u == 1)
         pdl_wait();
 
-    // u in two terms; rows past the group's end give sums that nobody reads
+    // u in three terms; rows past the group's end give sums that nobody reads
     const int live = rows.end - rows.begin;
     if (warp < 8) {
         const float* u = a.u + static_cast<int64_t>(rows.begin) * a.rank;
 #pragma unroll 4
         for (int t = tid; t < live * (RP / 8); t += 256) {
             const int row = t / (RP / 8), c = t % (RP / 8);
-            uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
+            float4 f0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), f1 = f0;
             if (c * 8 < a.rank) {
                 const float4* f = reinterpret_cast<const float4*>(u + static_cast<int64_t>(row) * a.rank + c * 8);
-                const float4 f0 = __ldcg(f), f1 = __ldcg(f + 1);
-                split_bf16x2(f0.x, f0.y, h.x, l.x);
-                split_bf16x2(f0.z, f0.w, h.y, l.y);
-                split_bf16x2(f1.x, f1.y, h.z, l.z);
-                split_bf16x2(f1.z, f1.w, h.w, l.w);
+                f0 = __ldcg(f);
+                f1 = __ldcg(f + 1);
             }
             const uint32_t place = (c >> 3) * (kExpandTile * 128u) + swizzled<S::kBox / 8>(row, c & 7);
-            *reinterpret_cast<uint4*>(smem + place) = h;
-            *reinterpret_cast<uint4*>(smem + S::kTermBytes + place) = l;
+            store_terms(smem + place, S::kTermBytes, f0, f1);
         }
         fence_proxy_async_shared();
     } else {
@@ -660,15 +701,15 @@ __global__ void __launch_bounds__(kExpandThreads, RP <= 64 ? 2 : 1)
             tc_fence_after_sync();
             const uint32_t ws = ws0 + stage * S::kWBytes;
 #pragma unroll
-            for (int kk = 0; kk < RP / 16; ++kk) {
-                const uint32_t k_at = kk / 4 * kExpandTile * 128 + kk % 4 * 32;
-                const uint64_t hi = operand_desc(us + k_at, S::kSwizzle, 0, group);
-                const uint64_t lo = operand_desc(us + S::kTermBytes + k_at, S::kSwizzle, 0, group);
-                const uint64_t w = TRANS ? operand_desc(ws + kk * 2048, Swizzle::k128, 0, 1024)
-                                         : operand_desc(ws + kk / 4 * kExpandCols * 128 + kk % 4 * 32, S::kSwizzle, 0, group);
-                tc_product(tmem + (i & 1) * kExpandCols, hi, w, desc, kk > 0);
-                tc_product(tmem + (i & 1) * kExpandCols, lo, w, desc, true);
-            }
+            for (int term = 2; term >= 0; --term)
+#pragma unroll
+                for (int kk = 0; kk < RP / 16; ++kk) {
+                    const uint64_t x = operand_desc(us + term * S::kTermBytes + kk / 4 * kExpandTile * 128 + kk % 4 * 32,
+                                                    S::kSwizzle, 0, group);
+                    const uint64_t w = TRANS ? operand_desc(ws + kk * 2048, Swizzle::k128, 0, 1024)
+                                             : operand_desc(ws + kk / 4 * kExpandCols * 128 + kk % 4 * 32, S::kSwizzle, 0, group);
+                    tc_product(tmem + (i & 1) * kExpandCols, x, w, desc, term < 2 || kk > 0);
+                }
             tc_commit(&s_sums[i & 1]); // frees w's stage too
             if (i >= 1 && i - 1 + S::kWStages < n) { // the step before is done, or nearly
                 alive = mbar_wait_bounded(&s_sums[(i - 1) & 1], ((i - 1) / 2) & 1, a.rows.err);
@@ -810,13 +851,19 @@ __global__ void __launch_bounds__(kFewThreads, 2) lora_few_kernel(LoraFewLaunch 
             for (int j = 0; j < 2; ++j)
                 w[i][j] = ld_nc_v4_if(wa + static_cast<int64_t>(j0 + j * 8 + g) * a.K + k, in && j0 + j * 8 < a.rank);
         }
+        float sum[2][4] = {}; // a chain of 8 products
 #pragma unroll
         for (int i = 0; i < S::kAhead; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                mma16816(acc[j], xa[i][0].x, xa[i][1].x, xa[i][0].y, xa[i][1].y, w[i][j].x, w[i][j].y);
-                mma16816(acc[j], xa[i][0].z, xa[i][1].z, xa[i][0].w, xa[i][1].w, w[i][j].z, w[i][j].w);
+                mma16816(sum[j], xa[i][0].x, xa[i][1].x, xa[i][0].y, xa[i][1].y, w[i][j].x, w[i][j].y);
+                mma16816(sum[j], xa[i][0].z, xa[i][1].z, xa[i][0].w, xa[i][1].w, w[i][j].z, w[i][j].w);
             }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[j][i] += sum[j][i];
     }
     // base and the factor's rows of 32 columns: column 8 (n / 2) + 2 j + n % 2 is
     // row n of product j; a lane has 8 of each 32 ranks, of what is left 4 of 16
@@ -911,7 +958,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) lora_few_kernel(LoraFewLaunch 
     __syncthreads();
 
     // out
-    uint32_t hi[RP / 16][4], lo[RP / 16][4];
+    uint32_t u[RP / 16][4][3]; // in three terms
 #pragma unroll
     for (int s = 0; s < RP / 16; ++s) {
         const bool half = s * 16 + 8 == a.rank, block = RP >= 32 && (s & ~1) * 16 + 32 <= a.rank;
@@ -919,8 +966,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) lora_few_kernel(LoraFewLaunch 
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const float* p = s_u + (g + 8 * r) * S::kPitch + k;
-            split_bf16x2(p[0], p[1], hi[s][r], lo[s][r]);
-            split_bf16x2(half ? 0.0f : p[2], half ? 0.0f : p[3], hi[s][2 + r], lo[s][2 + r]);
+            split_bf16x2(p[0], p[1], u[s][r]);
+            split_bf16x2(half ? 0.0f : p[2], half ? 0.0f : p[3], u[s][2 + r]);
         }
     }
     uint16_t* out = static_cast<uint16_t*>(a.out);
@@ -932,10 +979,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) lora_few_kernel(LoraFewLaunch 
             for (int i = 0; i < 4; ++i)
                 d[j][i] = 0.0f;
 #pragma unroll
-            for (int s = 0; s < RP / 16; ++s) {
-                mma16816(d[j], hi[s][0], hi[s][1], hi[s][2], hi[s][3], c.w[s][j].x, c.w[s][j].y);
-                mma16816(d[j], lo[s][0], lo[s][1], lo[s][2], lo[s][3], c.w[s][j].x, c.w[s][j].y);
-            }
+            for (int term = 2; term >= 0; --term) // the small ones first
+#pragma unroll
+                for (int s = 0; s < RP / 16; ++s)
+                    mma16816(d[j], u[s][0][term], u[s][1][term], u[s][2][term], u[s][3][term], c.w[s][j].x, c.w[s][j].y);
         }
         const uint4 b0 = c.base[0], b1 = c.base[1];
         load_columns(c, group + (S::kTwo ? 2 : 1) * units);
@@ -964,22 +1011,25 @@ constexpr int kOuterThreads = 320; // four warps that load x or dy, four that sp
 constexpr int kOuterRows = 64;     // rows a stage
 constexpr int kOuterCols = 128;    // columns of x or dy a tile: the product's M
 constexpr int kOuterParts = 4;     // CTAs that share a tile's rows, at most
+constexpr int kOuterChain = 4;     // stages whose products are summed in tensor memory
 
 template <int RP>
 struct OuterShape {
     static constexpr int kHalfBytes = kOuterRows * 128;    // 64 columns of x or dy, or of u's terms
     static constexpr int kVBytes = kOuterRows * kOuterCols * 2;
-    static constexpr int kUBytes = kOuterRows * RP * 4;    // u as it is in HBM, then its two terms
-    static constexpr int kTermBytes = kUBytes / 2;
-    static constexpr int kStageBytes = kVBytes + kUBytes;
-    // Three CTAs an SM (two at the largest rank), their stages in 72 KB each:
-    // at rank 32 77 us, against 81 us with two CTAs and 96 KB.
-    static constexpr int kCtas = RP <= 64 ? 3 : 2;
-    static constexpr int kStages = RP <= 32 ? 3 : 2;
-    static constexpr int kBytes = kStages * kStageBytes + 1024; // tiles start on 1024 bytes
+    static constexpr int kTermBytes = kOuterRows * RP * 2;
+    static constexpr int kUBytes = 3 * kTermBytes;         // u as it is in HBM, then its three terms
+    // Three CTAs an SM as far as the rank allows, the stages of a CTA in 72 KB: at
+    // rank 32 two CTAs with 87 KB take 96 us for all gradients of 4096 rows.
+    static constexpr int kCtas = RP <= 32 ? 3 : (RP == 64 ? 2 : 1);
+    static constexpr int kStages = RP == 128 ? 4 : 3;  // of x or dy
+    static constexpr int kUStages = RP == 16 || RP == 128 ? 3 : 2; // of u
+    static constexpr int kUAt = kStages * kVBytes;
+    static constexpr int kBytes = kUAt + kUStages * kUBytes + 1024; // tiles start on 1024 bytes
     static constexpr int kPitch = RP + 4;                       // floats a column of a part's sums
-    static_assert(kOuterCols * kPitch * 4 <= kStages * kStageBytes, "a part's sums take the stages' place");
-    static constexpr int kTmem = 2 * RP;                        // both terms' sums
+    static_assert(kOuterCols * kPitch * 4 + 1024 <= kBytes, "a part's sums take the stages' place");
+    static constexpr int kTmem = 4 * RP;                        // the three terms' sums, the chains' before
+    static constexpr int kSide = RP <= 64 ? 3 : 2; // terms that one product takes side by side (256 columns at most)
     static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
     static constexpr int kUChunks = RP < 64 ? RP / 8 : 8; // 16-byte chunks a row of u's terms
 };
@@ -1087,8 +1137,9 @@ __device__ __forceinline__ bool split_warps_any(bool mine)
 // columns are the product's rows (M), the rank its columns (N), and the sum
 // runs over the adapter's rows, kOuterRows a stage.  Both operands are MN-major:
 // the row data as it lies in HBM, and u, copied as fp32 and turned in place into
-// two bf16 tiles (hi, lo) that one product takes side by side.  Sums stay in
-// tensor memory until the last row; there the two terms' are added.  The warps
+// three bf16 tiles that one product takes side by side (at the largest rank two
+// do).  Sums stay in tensor memory: the terms' and, apart, those of the chains
+// before, to which the warps that split u add a chain when it is done.  The warps
 // that load run on into the next tile's stages while a tile is stored.
 template <int RP, bool SPLIT>
 __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
@@ -1096,7 +1147,7 @@ __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
 {
     using S = OuterShape<RP>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t s_v[S::kStages], s_u[S::kStages], s_split[S::kStages], s_free[S::kStages], s_done;
+    __shared__ uint64_t s_v[S::kStages], s_free[S::kStages], s_u[S::kUStages], s_split[S::kUStages], s_done, s_taken;
     __shared__ uint32_t s_tmem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -1104,11 +1155,14 @@ __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&s_v[i], 128);
-            mbar_init(&s_u[i], 1);
-            mbar_init(&s_split[i], 128);
             mbar_init(&s_free[i], 1);
         }
+        for (int i = 0; i < S::kUStages; ++i) {
+            mbar_init(&s_u[i], 1);
+            mbar_init(&s_split[i], 128);
+        }
         mbar_init(&s_done, 1);
+        mbar_init(&s_taken, 4);
         fence_mbar_init();
     }
     pdl_wait();
@@ -1125,9 +1179,11 @@ __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
     OuterTile t;
     bool alive = true; // no wait has run out
     int at_stage = 0;  // stages so far, over all tiles
-    const auto stage_free = [&] { // the products that read the stage's place before are done
-        if (at_stage >= S::kStages && alive)
-            alive = mbar_wait_bounded(&s_free[at_stage % S::kStages], (at_stage / S::kStages - 1) & 1, a.rows.err);
+    int chains = 0;    // chains waited for so far, over all tiles
+    const auto stage_free = [&](int stages) { // the products that read the place in a ring of `stages` before are done
+        const int before = at_stage - stages;
+        if (before >= 0 && alive)
+            alive = mbar_wait_bounded(&s_free[before % S::kStages], (before / S::kStages) & 1, a.rows.err);
     };
 
     if (warp < 4) {
@@ -1148,12 +1204,12 @@ __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
             const auto load = [&](int i, int& entry) {
                 const int index = row_index(a.rows, entry, t.rows.begin + i * kOuterRows + mine, end);
                 entry = find(i + 2);
-                stage_free();
+                stage_free(S::kStages);
                 int at[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     at[j] = __shfl_sync(kFullMask, index, j * 2 + (r0 & 1));
-                const uint32_t vs = base + at_stage % S::kStages * S::kStageBytes + to;
+                const uint32_t vs = base + at_stage % S::kStages * S::kVBytes + to;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) // rows that are none, and columns past the last, are zeros
                     cp_async16(vs + 1024u * j, from + static_cast<int64_t>(max(at[j], 0)) * N,
@@ -1174,47 +1230,80 @@ __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
             if (!tiles.get(a.rows, k, t) || lane != 0)
                 continue;
             for (int i = 0; i < t.stages; ++i, ++at_stage) {
-                stage_free();
+                stage_free(S::kUStages);
                 if (!alive)
                     break;
-                const int first = t.rows.begin + i * kOuterRows, stage = at_stage % S::kStages;
+                const int first = t.rows.begin + i * kOuterRows, stage = at_stage % S::kUStages;
                 const uint32_t bytes = static_cast<uint32_t>(min(kOuterRows, t.rows.end - first)) * a.rank * 4;
                 mbar_arrive_expect_tx(&s_u[stage], bytes);
-                bulk_load_g2s(smem + stage * S::kStageBytes + S::kVBytes,
+                bulk_load_g2s(smem + S::kUAt + stage * S::kUBytes,
                               (t.in ? a.dh : a.h) + static_cast<int64_t>(first) * a.rank, bytes, &s_u[stage]);
             }
         }
     } else if (warp == 8) {
-        constexpr uint32_t desc = product_desc(128, 2 * RP, true, true);
+        constexpr uint32_t desc = product_desc(128, S::kSide * RP, true, true), first_desc = product_desc(128, RP, true, true);
         constexpr uint32_t next = RP < 64 ? S::kTermBytes : S::kHalfBytes; // the following columns of u's terms
         constexpr uint32_t group = S::kUChunks * 128u;                     // 8 rows of u's terms
         for (int k = 0; k < rounds; ++k) {
             if (!tiles.get(a.rows, k, t) || lane != 0)
                 continue;
             for (int i = 0; i < t.stages && alive; ++i, ++at_stage) {
-                const int stage = at_stage % S::kStages;
-                const uint32_t parity = (at_stage / S::kStages) & 1;
-                alive = mbar_wait_bounded(&s_v[stage], parity, a.rows.err) &&
-                        mbar_wait_bounded(&s_split[stage], parity, a.rows.err);
+                const int link = i % kOuterChain;
+                const int stage = at_stage % S::kStages, u_stage = at_stage % S::kUStages;
+                alive = mbar_wait_bounded(&s_v[stage], (at_stage / S::kStages) & 1, a.rows.err) &&
+                        mbar_wait_bounded(&s_split[u_stage], (at_stage / S::kUStages) & 1, a.rows.err);
+                if (alive && link == 0 && i > 0)
+                    alive = mbar_wait_bounded(&s_taken, chains++ & 1, a.rows.err);
                 if (!alive)
                     break;
                 fence_proxy_async_shared(); // the copies were the other threads'
                 tc_fence_after_sync();
                 const int steps = (min(kOuterRows, t.rows.end - t.rows.begin - i * kOuterRows) + 15) / 16;
-                const uint32_t vs = base + stage * S::kStageBytes;
-                for (int kk = 0; kk < steps; ++kk)
-                    tc_product(tmem, operand_desc(vs + kk * 2048u, Swizzle::k128, S::kHalfBytes, 1024u),
-                               operand_desc(vs + S::kVBytes + kk * 2 * group, S::kSwizzle, next, group), desc,
-                               i > 0 || kk > 0);
+                const uint32_t vs = base + stage * S::kVBytes, us = base + S::kUAt + u_stage * S::kUBytes;
+                for (int kk = 0; kk < steps; ++kk) {
+                    const uint64_t v = operand_desc(vs + kk * 2048u, Swizzle::k128, S::kHalfBytes, 1024u);
+                    const uint32_t from = us + kk * 2 * group;
+                    if (S::kSide < 3)
+                        tc_product(tmem, v, operand_desc(from, S::kSwizzle, next, group), first_desc, link > 0 || kk > 0);
+                    tc_product(tmem + (3 - S::kSide) * RP, v,
+                               operand_desc(from + (3 - S::kSide) * S::kTermBytes, S::kSwizzle, next, group), desc,
+                               link > 0 || kk > 0);
+                }
                 tc_commit(&s_free[stage]);
-                if (i == t.stages - 1)
+                if (i == t.stages - 1 || link == kOuterChain - 1)
                     tc_commit(&s_done);
             }
         }
     } else {
         constexpr int kVecs = RP / 16; // pieces of 8 ranks a thread and stage
         const int st = tid - 128;
-        int sums = 0; // tiles with rows so far
+        const uint32_t here = tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16);
+        const auto chain_done = [&] {
+            if (alive)
+                alive = mbar_wait_bounded(&s_done, chains & 1, a.rows.err);
+            ++chains;
+            tc_fence_after_sync();
+        };
+        // 16 ranks' sums from j0 on: the terms' of the chain that is done, smallest
+        // first, and those of the chains before
+        const auto load_sums = [&](float (&v)[16], int j0, bool before) {
+            float d[16];
+            tmem_load16(v, here + 2 * RP + j0);
+            tmem_load16(d, here + RP + j0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v[i] += d[i];
+            tmem_load16(d, here + j0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v[i] += d[i];
+            if (before) {
+                tmem_load16(d, here + 3 * RP + j0);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    v[i] += d[i];
+            }
+        };
         for (int k = 0; k < rounds; ++k) {
             if (!tiles.get(a.rows, k, t))
                 continue;
@@ -1228,10 +1317,10 @@ __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
                 bad = split_warps_any(bad);
             }
             for (int i = 0; i < t.stages; ++i, ++at_stage) {
-                const int stage = at_stage % S::kStages;
+                const int stage = at_stage % S::kUStages;
                 if (alive)
-                    alive = mbar_wait_bounded(&s_u[stage], (at_stage / S::kStages) & 1, a.rows.err);
-                uint8_t* us = smem + stage * S::kStageBytes + S::kVBytes;
+                    alive = mbar_wait_bounded(&s_u[stage], (at_stage / S::kUStages) & 1, a.rows.err);
+                uint8_t* us = smem + S::kUAt + stage * S::kUBytes;
                 float4 f[kVecs][2];
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
@@ -1248,42 +1337,43 @@ __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
                     const int p = st + j * 128, row = p / (RP / 8), c = p % (RP / 8);
-                    uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
-                    if (first + row < t.rows.end && (!bad || row_at(a.rows, first + row, t.rows.end) >= 0)) {
-                        split_bf16x2(f[j][0].x, f[j][0].y, h.x, l.x);
-                        split_bf16x2(f[j][0].z, f[j][0].w, h.y, l.y);
-                        split_bf16x2(f[j][1].x, f[j][1].y, h.z, l.z);
-                        split_bf16x2(f[j][1].z, f[j][1].w, h.w, l.w);
-                    }
+                    if (first + row >= t.rows.end || (bad && row_at(a.rows, first + row, t.rows.end) < 0))
+                        f[j][0] = f[j][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     const uint32_t place = RP < 64 ? swizzled<S::kUChunks>(row, c) : in_halves(row, c);
-                    *reinterpret_cast<uint4*>(us + place) = h;
-                    *reinterpret_cast<uint4*>(us + S::kTermBytes + place) = l;
+                    store_terms(us + place, S::kTermBytes, f[j][0], f[j][1]);
                 }
                 fence_proxy_async_shared();
                 mbar_arrive(&s_split[stage]);
+                if (i > 0 && i % kOuterChain == 0) { // the chain before, while the next one's first stage is on its way
+                    chain_done();
+#pragma unroll 1
+                    for (int j0 = 0; j0 < RP; j0 += 16) {
+                        float v[16];
+                        load_sums(v, j0, i > kOuterChain);
+                        tmem_store16(here + 3 * RP + j0, v);
+                    }
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&s_taken);
+                }
             }
-            if (t.stages > 0) {
-                if (alive)
-                    alive = mbar_wait_bounded(&s_done, sums & 1, a.rows.err);
-                ++sums;
-                tc_fence_after_sync();
-            }
+            const bool before = t.stages > kOuterChain; // the rows made several chains
+            if (t.stages > 0)
+                chain_done();
             if (SPLIT) { // this part's sums, where the stages were
 #pragma unroll
                 for (int j0 = 0; j0 < RP; j0 += 16) {
-                    float hi[16], lo[16];
+                    float v[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        hi[i] = lo[i] = 0.0f;
-                    if (t.stages > 0) {
-                        const uint32_t from = tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + j0;
-                        tmem_load16(hi, from);
-                        tmem_load16(lo, from + RP);
-                    }
+                        v[i] = 0.0f;
+                    if (t.stages > 0)
+                        load_sums(v, j0, before);
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
                         *reinterpret_cast<float4*>(smem + (st * S::kPitch + j0 + i) * 4) =
-                            make_float4(hi[i] + lo[i], hi[i + 1] + lo[i + 1], hi[i + 2] + lo[i + 2], hi[i + 3] + lo[i + 3]);
+                            make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
                 tc_fence_before_sync();
                 break; // a cluster has one tile
@@ -1297,13 +1387,11 @@ __global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
                     break;
                 uint32_t d[8]; // two ranks each
                 if (t.stages > 0) {
-                    const uint32_t from = tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + j0;
-                    float hi[16], lo[16];
-                    tmem_load16(hi, from);
-                    tmem_load16(lo, from + RP);
+                    float v[16];
+                    load_sums(v, j0, before);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        d[i] = pack_bf16x2(hi[2 * i] + lo[2 * i], hi[2 * i + 1] + lo[2 * i + 1]);
+                        d[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -1479,8 +1567,8 @@ cudaError_t launch_lora_shrink(const LoraShrinkLaunch& a, cudaStream_t stream)
         // room for 444 CTAs 25 us (the last clusters wait for eight free places).
         const int parts = std::max(1, std::min({8, 2 * 148 / tiles, steps / 4}));
         const unsigned grid = static_cast<unsigned>(tiles) * parts;
-        return a.transposed ? launch_after<lora_shrink_kernel<RP, true>>(grid, kShrinkThreads, S::kBytes, parts, stream, w_map, a)
-                            : launch_after<lora_shrink_kernel<RP, false>>(grid, kShrinkThreads, S::kBytes, parts, stream, w_map, a);
+        return a.transposed ? launch_after<lora_shrink_kernel<RP, true>>(grid, S::kThreads, S::kBytes, parts, stream, w_map, a)
+                            : launch_after<lora_shrink_kernel<RP, false>>(grid, S::kThreads, S::kBytes, parts, stream, w_map, a);
     });
 }
 

@@ -1,5 +1,5 @@
 // ep_mma.cuh -- device helpers of the kernels that multiply: asynchronous
-// 16-byte copies, the warp's matrix product, the two-term bf16 form of an fp32
+// 16-byte copies, the warp's matrix product, the three-term bf16 form of an fp32
 // operand, and the places of 16-byte chunks in operand tiles.
 #pragma once
 
@@ -49,14 +49,20 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// An fp32 pair as bf16 pairs hi + lo: hi is the value rounded to bf16, lo what
-// is left, rounded again, so 16 bits of the value survive (2^-17 of it at
-// most is lost).  An infinite value leaves no rest (inf - inf).
-__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uint32_t& lo)
+// An fp32 pair as bf16 pairs t[0] + t[1] + t[2], exactly: each term is what the
+// upper half of the word holds, 8 of the 24 significant bits, and the next one is
+// taken from what is left (cut, not rounded: a rest of the value's own sign, never
+// an infinity where the value is finite; below 2^-133 nothing is kept).  An
+// infinite value leaves no rest (inf - inf).
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t (&t)[3])
 {
-    hi = pack_bf16x2(a, b);
-    const float ra = a - bf16_lo(hi), rb = b - bf16_hi(hi);
-    lo = pack_bf16x2(ra == ra ? ra : 0.0f, rb == rb ? rb : 0.0f);
+    t[0] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    a = fabsf(a) == INFINITY ? 0.0f : a - bf16_lo(t[0]);
+    b = fabsf(b) == INFINITY ? 0.0f : b - bf16_hi(t[0]);
+    t[1] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    a -= bf16_lo(t[1]);
+    b -= bf16_hi(t[1]);
+    t[2] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
 
 // Place of 16-byte chunk c of a row in a shared-memory tile of PC (a power of

@@ -45,8 +45,9 @@ extern "C" {
  *   base    NULL: zeros.  out may be the same buffer as base; otherwise no
  *           output may overlap an input.
  * The products run on the tensor cores with fp32 sums; fp32 operands (h, dh)
- * enter them as two bf16 terms, hi + lo, which keeps 16 bits of them.  Sums are
- * taken in a fixed order: the same call gives the same bytes.
+ * enter them as three bf16 terms, which keep all of their bits, and no more than
+ * 24 products in a row are summed there before fp32 arithmetic adds them up.
+ * Sums are taken in a fixed order: the same call gives the same bytes.
  * Limits: rank a multiple of 8, 8 <= rank <= 128; hidden_in and hidden_out
  * positive multiples of 8; E <= 1024; x, a, b, base, out, h and the gradients
  * 16-byte aligned.  Rows at or past num_rows are skipped with
