@@ -919,6 +919,8 @@ ep_status_t check_router(const ep_router_desc_t* r)
         return EP_ERR_INVALID_ARG;
     if (!std::isfinite(r->scale) || static_cast<int64_t>(r->num_tokens) * r->num_experts >= (int64_t{1} << 31))
         return EP_ERR_INVALID_ARG; // num_topk <= num_experts: T * K is below 2^31 too
+    if (r->num_tokens > ep::kRouterMaxTokens)
+        return EP_ERR_INVALID_ARG;
     if (r->num_experts > ep::kRouterMaxExperts || r->num_topk > ep::kRouterMaxTopk ||
         r->num_groups > ep::kRouterMaxGroups || (r->num_groups & (r->num_groups - 1)) != 0)
         return EP_ERR_UNSUPPORTED;

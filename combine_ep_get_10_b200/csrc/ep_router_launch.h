@@ -1,6 +1,5 @@
 // ep_router_launch.h -- launch interfaces of the router kernels (ep_router.cu),
-// called by the C-ABI layer (ep_router_api.cu), which has checked the
-// arguments.
+// called by the C-ABI layer (ep_api.cu), which has checked the arguments.
 #pragma once
 
 #include <cstddef>
@@ -14,6 +13,7 @@ namespace ep {
 constexpr int kRouterMaxExperts = 1024; // 32 logits a lane
 constexpr int kRouterMaxTopk = 32;      // one slot a lane
 constexpr int kRouterMaxGroups = 32;
+constexpr int kRouterMaxTokens = 1 << 30; // a token past the last, and a chunk more, is still an int
 
 struct RouterTopkLaunch {
     ep_router_desc_t r;

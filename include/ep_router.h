@@ -43,7 +43,7 @@ extern "C" {
  * experts' s); the bias is not part of them.  Where fewer than K experts can
  * be chosen, the slots left over get id -1 and weight 0.
  *
- * Limits: T >= 0, T * E and T * K below 2^31; 1 <= E <= 1024; 1 <= K <= 32,
+ * Limits: 0 <= T <= 2^30, T * E and T * K below 2^31; 1 <= E <= 1024; 1 <= K <= 32,
  * K <= E; num_groups a power of two up to 32 that divides E; 1 <= topk_groups
  * <= num_groups; group_top 1 or 2; scale finite.  logits aligned to their
  * element size.

@@ -1,0 +1,27 @@
+"""The limits that the router's and the adapters' headers state, on the host (no
+GPU here): what lies past them is refused by every call, what lies at them is not."""
+import ctypes
+
+import pytest
+
+from combine_ep_get_10_b200 import binding as B
+from test_router_cpu import back, desc, loss, topk
+
+
+@pytest.fixture(scope="module")
+def L():
+    from combine_ep_get_10_b200 import build
+
+    build.build()
+    return B.lib()
+
+
+def test_more_tokens_than_an_index_holds_are_refused(L):
+    """One expert allows the most tokens: T * E < 2^31 alone would let token
+    indices a chunk past the last one overflow."""
+    most = desc(num_tokens=1 << 30, num_experts=1, num_topk=1)
+    assert L.ep_balance_workspace_bytes(ctypes.byref(most), 1) > 0
+    for T in ((1 << 30) + 1, 2132973617, (1 << 31) - 1):
+        d = ctypes.byref(desc(num_tokens=T, num_experts=1, num_topk=1))
+        assert L.ep_balance_workspace_bytes(d, 1) == 0
+        assert topk(L, d) == 1 and loss(L, d) == 1 and back(L, d) == 1
