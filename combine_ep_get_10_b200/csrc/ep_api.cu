@@ -1041,7 +1041,7 @@ ep_status_t check_row_args(const ep_routing_desc_t* routing, const ep_layout_t* 
     st = check_rows(routing, layout, mode, max_tokens, num_rows);
     if (st != EP_OK)
         return st;
-    if (num_rows >= (int64_t{1} << 31))
+    if (num_rows > ep::kLoraMaxRows)
         return EP_ERR_INVALID_ARG;
     return EP_OK;
 }

@@ -13,6 +13,7 @@ namespace ep {
 
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxAdapters = 1024;
+constexpr int64_t kLoraMaxRows = (int64_t{1} << 31) - 1024; // a row a few tiles past the last is still an int
 
 // The rows of every adapter, and where a row's data is.
 struct LoraRows {

@@ -5,6 +5,7 @@ import ctypes
 import pytest
 
 from combine_ep_get_10_b200 import binding as B
+from test_lora_cpu import LAYOUT, bwd, fwd, routing
 from test_router_cpu import back, desc, loss, topk
 
 
@@ -25,3 +26,16 @@ def test_more_tokens_than_an_index_holds_are_refused(L):
         d = ctypes.byref(desc(num_tokens=T, num_experts=1, num_topk=1))
         assert L.ep_balance_workspace_bytes(d, 1) == 0
         assert topk(L, d) == 1 and loss(L, d) == 1 and back(L, d) == 1
+
+
+def test_more_rows_than_an_index_holds_are_refused(L):
+    """A padded buffer may have rows up to the limit whatever the routing's pairs;
+    past it a row a few tiles behind the last would overflow."""
+    pairs, E = 16, 8
+    for rows in ((1 << 31) - 1023, (1 << 31) - 1):
+        for mt in (1 << 28, (1 << 31) - 1):
+            kw = dict(rows=rows, mode=1, mt=mt, rt=None)
+            assert fwd(L, r=routing(T=pairs, E=E), **kw) == 1 and bwd(L, r=routing(T=pairs, E=E), **kw) == 1
+        assert L.ep_row_tokens(ctypes.byref(routing()), ctypes.byref(LAYOUT), 1, 1 << 28, rows, 0x7000, None) == 1
+    # at the limit the next check speaks: h is missing
+    assert fwd(L, rows=(1 << 31) - 1024, mode=1, mt=1 << 28, rt=None, h=None) == 1
