@@ -98,6 +98,15 @@ struct LaneGroups {
     }
 };
 
+// Does the layout have more rows than the routing has pairs: the grids are for
+// those, so none of its rows is worked on, by any kernel of the call.  mine: the
+// lane's share of them.  One warp.
+__device__ __forceinline__ bool too_many_rows(const LoraRows& g, int64_t mine)
+{
+    const int64_t most = g.pairs + 1; // at most 2^24 + 1: 32 lanes' fit
+    return __reduce_add_sync(kFullMask, static_cast<uint32_t>(mine < most ? mine : most)) > static_cast<uint32_t>(g.pairs);
+}
+
 // The lane in whose run of `n` item i lies, and the items before that lane's;
 // -1 when there are fewer items.  One warp.
 __device__ __forceinline__ int find_lane(int n, int i, int lane, int& before)
@@ -122,13 +131,15 @@ __device__ __forceinline__ bool find_tile(const LoraRows& g, int i, int lane, in
     const LaneGroups groups(g, lane);
     const auto tiles = [](const RowRange& r) { return (r.end - r.begin + TILE - 1) / TILE; };
     int n = 0;
+    int64_t all = 0;
     groups.each(g, [&](int, const RowRange& r) {
         n += tiles(r);
+        all += r.end - r.begin;
         return false;
     });
     int before;
     const int from = find_lane(n, i, lane, before);
-    if (from < 0)
+    if (from < 0 || too_many_rows(g, all))
         return false;
     int found = 0, left = i - before;
     RowRange mine{0, 0};
@@ -150,9 +161,9 @@ __device__ __forceinline__ bool find_tile(const LoraRows& g, int i, int lane, in
     return true;
 }
 
-// Rows that the routing fills past num_rows are left out, and so may be rows
-// where the layout has more than the routing has pairs (it is another routing's,
-// or the routing is a part of the layout's); the first CTA of a call's first
+// Rows that the routing fills past num_rows are left out, and all rows where the
+// layout has more than the routing has pairs (it is another routing's, or the
+// routing is a part of the layout's); the first CTA of a call's first
 // kernel says so.  One warp.
 __device__ __forceinline__ void report_overflow(const LoraRows& g, int lane)
 {
@@ -467,11 +478,15 @@ __device__ __forceinline__ bool find_share(const LoraRows& g, int i, int steps, 
     const auto tiles_of = [](const RowRange& r) { return (r.end - r.begin + kExpandTile - 1) / kExpandTile; };
     uint32_t cost = 0; // below 2^26: at most 2^24 rows
     uint32_t tiles = 0;
+    int64_t all = 0;
     groups.each(g, [&](int, const RowRange& r) {
+        all += r.end - r.begin;
         tiles += tiles_of(r);
         cost += r.end - r.begin + tiles_of(r) * kStepRows;
         return false;
     });
+    if (too_many_rows(g, all))
+        return false;
     tiles = __reduce_add_sync(kFullMask, tiles);
     cost = max(__reduce_add_sync(kFullMask, cost), 1u);
     const uint32_t spare = max(kExpandGrid - static_cast<int>(tiles), 0);
@@ -1057,6 +1072,7 @@ struct OuterTiles {
     int parts, part, places, place; // CTAs a tile, which of them; clusters, which of them
     int adapter;   // lane i: the i-th adapter by rows
     RowRange rows; // and its rows
+    bool none;     // no rows at all (too_many_rows)
 
     // One warp.
     __device__ __forceinline__ OuterTiles(const LoraRows& g, int in_tiles_, int out_tiles_, int parts_, int lane)
@@ -1065,11 +1081,19 @@ struct OuterTiles {
           places(static_cast<int>(gridDim.x) / (SPLIT ? parts_ : 1)),
           place(static_cast<int>(blockIdx.x) / (SPLIT ? parts_ : 1)), adapter(0), rows{0, 0}
     {
-        if (g.E > 32)
+        int64_t all = 0;
+        if (g.E > 32) {
+            for (int e = lane; e < g.E; e += 32) {
+                const RowRange r = group_rows(g, e);
+                all += r.end - r.begin;
+            }
+            none = too_many_rows(g, all);
             return;
+        }
         RowRange mine{0, -1};
         if (lane < g.E)
             mine = group_rows(g, lane);
+        none = too_many_rows(g, max(mine.end - mine.begin, 0));
         const int n = mine.end - mine.begin;
         int before = 0;
         for (int j = 0; j < g.E; ++j) {
@@ -1100,6 +1124,8 @@ struct OuterTiles {
             t.rows.begin = __shfl_sync(kFullMask, rows.begin, at);
             t.rows.end = __shfl_sync(kFullMask, rows.end, at);
         }
+        if (none)
+            t.rows.end = t.rows.begin;
         t.stages = (t.rows.end - t.rows.begin + kOuterRows - 1) / kOuterRows;
         if (SPLIT) {
             const int mine = (t.stages + parts - 1) / parts;

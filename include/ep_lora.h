@@ -51,9 +51,9 @@ extern "C" {
  * Limits: num_rows <= 2^31 - 1024; rank a multiple of 8, 8 <= rank <= 128;
  * hidden_in and hidden_out positive multiples of 8; E <= 1024; x, a, b, base, out, h and the gradients
  * 16-byte aligned.  Rows at or past num_rows are skipped with
- * EP_DEVERR_OVERFLOW.  The layout is the routing's own: one that has rows of
- * more pairs than the routing (of which the routing is a part) is flagged so
- * too, and some of its rows are skipped.
+ * EP_DEVERR_OVERFLOW.  The layout is the routing's own: with one that has rows of
+ * more pairs than the routing (of which the routing is a part) all rows are
+ * skipped and flagged so.
  * ---------------------------------------------------------------------- */
 typedef struct {
     int32_t rank;
