@@ -634,8 +634,11 @@ int chunk_tokens(int64_t T)
     return static_cast<int>((each + kBalanceWarps - 1) / kBalanceWarps * kBalanceWarps);
 }
 
-// Most chunks that T tokens in S sequences make (at most one part one a
-// sequence); grows with T.
+// The chunks of sequence s are numbered from begin / chunk + s on: a sequence of n
+// tokens has at most n / chunk + 1 of them, so numbers do not meet, some stay
+// unused, and a number's sequence is found by bisection, a sequence's numbers
+// without a look at the others.  T / chunk + S are enough, which is at most this; it
+// grows with T.
 __host__ __device__ __forceinline__ int64_t most_chunks(int64_t T, int64_t S)
 {
     const int64_t full = (T + kBalanceWarps - 1) / kBalanceWarps;
@@ -668,69 +671,68 @@ __device__ __forceinline__ TokenRange seq_range(const int32_t* offsets, int T, i
     return {b, min(max(__ldg(offsets + s + 1), b), T)};
 }
 
+// How many of the `count` values f(0) <= f(1) <= .. are at most x: each step reads 32
+// of them spread over what is left.  One warp; lanes agree.  (Whatever f gives, the
+// answer is in [0, count].)
+template <typename F>
+__device__ __forceinline__ int count_up_to(int count, int x, int lane, F&& f)
+{
+    int lo = 0, len = count; // lo of them so far
+    while (len > 0) {
+        const int step = (len + 31) / 32;
+        const int at = lo + (lane + 1) * step - 1; // the last one of the lane's run
+        const bool le = at < lo + len && f(at) <= x;
+        const int runs = __popc(__ballot_sync(kFullMask, le));
+        lo += runs * step;
+        if (step == 1)
+            break;
+        len = min(step - 1, count - lo);
+    }
+    return lo;
+}
+
+// The sequence of token t (the last one that begins at or before it), -1 when
+// it is in none.
+__device__ __forceinline__ int find_seq(const int32_t* offsets, int S, int t, int lane)
+{
+    if (offsets == nullptr)
+        return 0;
+    const int s = count_up_to(S + 1, t, lane, [&](int i) { return __ldg(offsets + i); }) - 1;
+    return s < S ? s : -1;
+}
+
 struct Chunk {
-    int64_t first, index; // the sequence's first chunk, this one
-    int seq, of;          // the sequence, its number of chunks
+    int seq, of; // the sequence, its number of chunks
     TokenRange tokens;
 };
 
-// Chunk i, and the number of chunks in all (the return value); i past them
-// leaves `c` as it was.  One warp; lanes agree.
-__device__ __forceinline__ int64_t find_chunk(const int32_t* offsets, int T, int S, int chunk, int64_t i, int lane,
-                                              Chunk& c)
+// A sequence's first chunk, and how many it has.
+__device__ __forceinline__ int first_chunk(const TokenRange& r, int chunk, int s)
 {
-    int64_t before = 0;
-    for (int base = 0; base < S; base += 32) {
-        int n = 0;
-        if (base + lane < S) {
-            const TokenRange r = seq_range(offsets, T, base + lane);
-            n = (r.end - r.begin + chunk - 1) / chunk;
-        }
-        int inc = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(kFullMask, inc, d);
-            if (lane >= d)
-                inc += o;
-        }
-        const int l = __ffs(__ballot_sync(kFullMask, before <= i && before + inc > i)) - 1;
-        if (l >= 0) {
-            c.of = __shfl_sync(kFullMask, n, l);
-            c.first = before + __shfl_sync(kFullMask, inc, l) - c.of;
-            c.index = i;
-            c.seq = base + l;
-            const TokenRange r = seq_range(offsets, T, c.seq);
-            c.tokens.begin = r.begin + static_cast<int>(i - c.first) * chunk;
-            c.tokens.end = min(r.end, c.tokens.begin + chunk);
-        }
-        before += __shfl_sync(kFullMask, inc, 31);
-    }
-    return before;
+    return r.begin / chunk + s;
 }
 
-struct SeqChunks {
-    int64_t first, total; // the sequence's first chunk; the chunks of all
-    int of;               // the sequence's chunks
-};
-
-__device__ __forceinline__ SeqChunks find_seq_chunks(const int32_t* offsets, int T, int S, int chunk, int s, int lane)
+__device__ __forceinline__ int chunks_of(const TokenRange& r, int chunk)
 {
-    int64_t before = 0, total = 0;
-    int of = 0;
-    for (int i = lane; i < S; i += 32) {
-        const TokenRange r = seq_range(offsets, T, i);
-        const int n = (r.end - r.begin + chunk - 1) / chunk;
-        total += n;
-        before += i < s ? n : 0;
-        of = i == s ? n : of;
-    }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) {
-        before += __shfl_xor_sync(kFullMask, before, d);
-        total += __shfl_xor_sync(kFullMask, total, d);
-        of = max(of, __shfl_xor_sync(kFullMask, of, d));
-    }
-    return {before, total, of};
+    return (r.end - r.begin + chunk - 1) / chunk;
+}
+
+// Chunk i; `of` is 0 for a number that no sequence uses.  One warp; lanes agree.
+__device__ __forceinline__ Chunk find_chunk(const int32_t* offsets, int T, int S, int chunk, int i, int lane)
+{
+    const int s = count_up_to(S, i, lane, [&](int j) { return first_chunk(seq_range(offsets, T, j), chunk, j); }) - 1;
+    Chunk c{};
+    if (s < 0)
+        return c;
+    const TokenRange r = seq_range(offsets, T, s);
+    const int at = i - first_chunk(r, chunk, s), of = chunks_of(r, chunk);
+    if (at < 0 || at >= of)
+        return c;
+    c.seq = s;
+    c.of = of;
+    c.tokens.begin = r.begin + at * chunk;
+    c.tokens.end = min(r.end, c.tokens.begin + chunk);
+    return c;
 }
 
 // The results of sequence s from its sums: thread e < E holds expert e's.  All
@@ -772,7 +774,6 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch 
     __shared__ float s_z[kBalanceWarps], s_red[kBalanceWarps];
     __shared__ int s_n[kBalanceWarps];
     __shared__ Chunk s_chunk;
-    __shared__ int64_t s_total;
     pdl_wait();
     if (finish)
         pdl_launch_dependents(); // balance_finish_kernel, which waits for this grid
@@ -782,32 +783,28 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch 
     const int64_t chunks = most_chunks(T, S);
     const BalanceSums part = balance_sums(a.workspace, chunks, E);
     if (warp == 0) {
-        Chunk found{};
-        const int64_t n = find_chunk(a.seq_offsets, T, S, chunk, blockIdx.x, lane, found);
-        if (lane == 0) {
+        const Chunk found = find_chunk(a.seq_offsets, T, S, chunk, blockIdx.x, lane);
+        if (lane == 0)
             s_chunk = found;
-            s_total = n;
+    }
+    if (static_cast<int>(blockIdx.x) < S) { // a sequence without tokens
+        const int64_t s = blockIdx.x;
+        const TokenRange r = seq_range(a.seq_offsets, T, static_cast<int>(s));
+        if (r.begin >= r.end) {
+            for (int e = tid; e < E; e += kBalanceThreads) {
+                a.counts[s * E + e] = 0;
+                if (a.mean_scores != nullptr)
+                    a.mean_scores[s * E + e] = 0.0f;
+            }
+            if (tid == 0) {
+                a.losses[2 * s] = a.losses[2 * s + 1] = 0.0f;
+                a.seq_tokens[s] = 0;
+            }
         }
     }
     __syncthreads();
     const Chunk c = s_chunk;
-    const int64_t total = s_total;
-    const bool sound = total <= chunks; // else the offsets are not sorted: no sequence has tokens
-    for (int64_t s = blockIdx.x; s < S; s += gridDim.x) { // sequences without tokens
-        const TokenRange r = seq_range(a.seq_offsets, T, static_cast<int>(s));
-        if (sound && r.begin < r.end)
-            continue;
-        for (int e = tid; e < E; e += kBalanceThreads) {
-            a.counts[s * E + e] = 0;
-            if (a.mean_scores != nullptr)
-                a.mean_scores[s * E + e] = 0.0f;
-        }
-        if (tid == 0) {
-            a.losses[2 * s] = a.losses[2 * s + 1] = 0.0f;
-            a.seq_tokens[s] = 0;
-        }
-    }
-    if (!sound || static_cast<int64_t>(blockIdx.x) >= total)
+    if (c.of == 0)
         return;
     for (int e = tid; e < E; e += kBalanceThreads)
         s_cnt[e] = 0;
@@ -888,7 +885,7 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch 
             sum += s_q[w * E + e];
         s_q[e] = sum; // only this thread reads the column again
         if (c.of > 1)
-            part.sums[c.index * E + e] = make_int2(__float_as_int(sum), s_cnt[e]);
+            part.sums[static_cast<int64_t>(blockIdx.x) * E + e] = make_int2(__float_as_int(sum), s_cnt[e]);
     }
     float z = 0.0f;
     int n = 0;
@@ -901,10 +898,13 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch 
         return;
     }
     if (tid == 0)
-        part.tails[c.index] = make_int2(__float_as_int(z), n);
+        part.tails[blockIdx.x] = make_int2(__float_as_int(z), n);
 }
 
-// One cluster a sequence: the results of those that are made of several chunks.
+// The results of the sequences that are made of several chunks, a cluster each.
+// Where there are more sequences than chunks (by_token), cluster j takes the one that
+// token j * chunk is the first such token of: those of several chunks all have one,
+// and there are no more clusters than chunks, however many sequences.
 // The CTAs share out the experts and, in each, the warps the chunks (one CTA
 // alone would draw all the partial sums through one SM: 7 us for 148 chunks of
 // 256 experts).
@@ -912,7 +912,7 @@ constexpr int kFinishCluster = 8;
 constexpr int kFinishLoads = 10; // 16 warps: 160 chunks in one go, the most a sequence of a long batch has
 constexpr int kFinishExperts = kRouterMaxExperts / kFinishCluster; // a CTA, at most
 
-__global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(BalanceLaunch a, int chunk)
+__global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(BalanceLaunch a, int chunk, bool by_token)
 {
     __shared__ float s_q[kBalanceWarps][kFinishExperts];
     __shared__ int s_cnt[kBalanceWarps][kFinishExperts];
@@ -920,29 +920,27 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(Balance
     __shared__ int s_n;
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = static_cast<int>(cluster.block_rank());
-    const int E = a.r.num_experts, T = a.r.num_tokens, S = a.num_seqs, s = blockIdx.x / kFinishCluster;
+    const int E = a.r.num_experts, T = a.r.num_tokens, S = a.num_seqs, j = blockIdx.x / kFinishCluster;
     const int64_t chunks = most_chunks(T, S);
     const BalanceSums part = balance_sums(a.workspace, chunks, E);
     // (what it reads before the wait is older than the kernel that it waits for)
-    const TokenRange own = seq_range(a.seq_offsets, T, s);
-    if (own.end - own.begin <= chunk) { // one chunk at most: there are many of these where there are many sequences
-        pdl_wait();
-        return; // the whole cluster
-    }
-    const SeqChunks c = find_seq_chunks(a.seq_offsets, T, S, chunk, s, lane);
+    const int s = by_token ? find_seq(a.seq_offsets, S, j * chunk, lane) : j;
+    const TokenRange own = s >= 0 ? seq_range(a.seq_offsets, T, s) : TokenRange{0, 0};
     pdl_wait();
-    if (c.total > chunks)
-        return;
+    const int64_t before = static_cast<int64_t>(j - 1) * chunk;
+    if (own.end - own.begin <= chunk || (by_token && own.begin <= before))
+        return; // one chunk at most, or another cluster's: the whole cluster
+    const int first = first_chunk(own, chunk, s), of = chunks_of(own, chunk);
     const int per = (E + kFinishCluster - 1) / kFinishCluster, e0 = min(rank * per, E), n_e = min(per, E - e0);
     for (int x = lane; x < n_e; x += 32) {
         float q = 0.0f;
         int cnt = 0;
-        for (int base = warp; base < c.of; base += kFinishLoads * kBalanceWarps) {
+        for (int base = warp; base < of; base += kFinishLoads * kBalanceWarps) {
             int2 o[kFinishLoads]; // all on their way at once
 #pragma unroll
             for (int u = 0; u < kFinishLoads; ++u) {
                 const int i = base + u * kBalanceWarps;
-                o[u] = i < c.of ? __ldcg(part.sums + (c.first + i) * E + e0 + x) : make_int2(0, 0);
+                o[u] = i < of ? __ldcg(part.sums + static_cast<int64_t>(first + i) * E + e0 + x) : make_int2(0, 0);
             }
 #pragma unroll
             for (int u = 0; u < kFinishLoads; ++u) {
@@ -956,11 +954,11 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(Balance
     if (warp == kBalanceWarps - 1) { // every CTA needs the tokens
         float z = 0.0f;
         int n = 0;
-        for (int base = lane; base < c.of; base += 5 * 32) {
+        for (int base = lane; base < of; base += 5 * 32) {
             int2 o[5];
 #pragma unroll
             for (int u = 0; u < 5; ++u)
-                o[u] = base + 32 * u < c.of ? __ldcg(part.tails + c.first + base + 32 * u) : make_int2(0, 0);
+                o[u] = base + 32 * u < of ? __ldcg(part.tails + first + base + 32 * u) : make_int2(0, 0);
 #pragma unroll
             for (int u = 0; u < 5; ++u) {
                 z += __int_as_float(o[u].x);
@@ -1021,27 +1019,6 @@ constexpr int kBackwardWarps = 4;
 // gradient, with 16 an SM 26.6 us, with 32 27.2 us.
 constexpr int kBackwardFill = 148 * 24;
 constexpr int kMostRun = 16;
-
-// The sequence of token t (the last one that begins at or before it), -1 when
-// it is in none: each step reads 32 offsets spread over what is left.
-__device__ __forceinline__ int find_seq(const int32_t* offsets, int S, int t, int lane)
-{
-    if (offsets == nullptr)
-        return 0;
-    int lo = 0, len = S + 1; // how many of the S + 1 offsets are <= t: lo of them so far
-    while (len > 0) {
-        const int step = (len + 31) / 32;
-        const int at = lo + (lane + 1) * step - 1; // the last one of the lane's run
-        const bool le = at < lo + len && __ldg(offsets + at) <= t;
-        const int runs = __popc(__ballot_sync(kFullMask, le));
-        lo += runs * step;
-        if (step == 1)
-            break;
-        len = min(step - 1, S + 1 - lo);
-    }
-    const int s = lo - 1;
-    return s < S ? s : -1;
-}
 
 // 16 bytes of shared or global memory at a time where the lane's experts lie
 // together.
@@ -1385,13 +1362,15 @@ cudaError_t launch_balance_loss(const BalanceLaunch& a, cudaStream_t stream)
                 return e;
         }
         const int T = a.r.num_tokens, chunk = chunk_tokens(std::max(T, 1));
-        const unsigned grid = static_cast<unsigned>(most_chunks(T, a.num_seqs));
+        const unsigned grid = static_cast<unsigned>(T / chunk + a.num_seqs);
         const bool finish = T > chunk; // else no sequence has a second chunk
         const cudaError_t e = launch_after(kernel, grid, kBalanceThreads, smem, 1, stream, a, chunk, finish);
         if (e != cudaSuccess || !finish)
             return e;
-        return launch_after(balance_finish_kernel, static_cast<unsigned>(a.num_seqs) * kFinishCluster, kBalanceThreads, 0,
-                            kFinishCluster, stream, a, chunk);
+        const int tokens = (T - 1) / chunk + 1;
+        const bool by_token = a.num_seqs > tokens;
+        return launch_after(balance_finish_kernel, static_cast<unsigned>(by_token ? tokens : a.num_seqs) * kFinishCluster,
+                            kBalanceThreads, 0, kFinishCluster, stream, a, chunk, by_token);
     });
 }
 
