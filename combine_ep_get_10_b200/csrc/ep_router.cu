@@ -1355,7 +1355,7 @@ cudaError_t launch_balance_loss(const BalanceLaunch& a, cudaStream_t stream)
     return with_row_shape(r, address(a.logits), [&](auto npl, auto bf16, auto vec) {
         const auto kernel = balance_kernel<npl(), bf16(), vec()>;
         const size_t smem = sizeof(float) * 2 * kBalanceWarps * a.r.num_experts;
-        if (smem > 48 * 1024) {
+        if (smem > 47 * 1024) { // 48 KB, the kernel's own arrays among them, need no leave
             const cudaError_t e =
                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
             if (e != cudaSuccess)

@@ -37,7 +37,8 @@ def lengths(kind, S, g):
 
 
 @pytest.mark.parametrize("kind,S,E", [("short", 4000, 24), ("some long", 3000, 24), ("about a chunk", 150, 40),
-                                      ("about a chunk", 700, 8), ("one", 1000, 16), ("some long", 37, 256)])
+                                      ("about a chunk", 700, 8), ("one", 1000, 16), ("some long", 37, 256),
+                                      ("about a chunk", 20, 383), ("about a chunk", 20, 384), ("about a chunk", 20, 385)])
 @pytest.mark.parametrize("first,behind", [(0, 0), (333, 70)])
 def test_many_sequences_of_all_lengths(kind, S, E, first, behind):
     g = torch.Generator().manual_seed(S + E)
@@ -111,3 +112,41 @@ def test_time_grows_with_the_sequences_not_with_their_square():
 
     few, many = us(16384), us(65536)
     assert many < 8 * few, (few, many)
+
+
+def test_arrays_past_2_32_bytes():
+    """Logits and gradients of more than 2^32 bytes, in which the last rows are as
+    right as the first."""
+    T, E, K = 2 ** 21 - 1, 1024, 2
+    logits = torch.empty((T, E), device="cuda")
+    for t in range(0, T, 1 << 18):
+        part = logits[t:t + (1 << 18)]
+        part.copy_(torch.randn((1 << 18, E), generator=torch.Generator(device="cuda").manual_seed(t), device="cuda")
+                   [:part.shape[0]])
+    router = B.Router(E, K)
+    idx, w = torch.empty((T, K), dtype=torch.int64, device="cuda"), torch.empty((T, K), device="cuda")
+    B.ep_router_topk(logits, router, idx, w)
+    stats = B.BalanceStats(router, T, num_seqs=2)
+    off = torch.tensor([0, T - 1000, T], dtype=torch.int32, device="cuda")
+    B.ep_balance_loss(logits, router, idx, stats, seq_offsets=off)
+    d = torch.empty_like(logits)
+    dl = torch.tensor([[1.0, 0.0], [0.5, 0.25]], device="cuda")
+    dw = torch.ones((T, K), device="cuda")
+    dw[:, 1] = -1.0
+    B.ep_router_backward(logits, router, idx, d, d_topk_weights=dw, stats=stats, d_losses=dl, seq_offsets=off)
+    for t0, t1, s, n in ((0, 200, 0, T - 1000), (T - 1200, T - 1000, 0, T - 1000), (T - 1000, T, 1, 1000)):
+        l = logits[t0:t1].double()
+        top = l.topk(K, dim=1)
+        assert torch.equal(idx[t0:t1], top.indices)
+        want = torch.softmax(top.values, dim=1)
+        assert torch.all((w[t0:t1] - want).abs() <= RTOL * want)
+        q = torch.softmax(l, dim=1)
+        gain = dl[s, 0].double() * E / (K * n * n) * stats.counts[s].double()
+        grad = q * (gain - (gain * q).sum(dim=1, keepdim=True)) + \
+            (dl[s, 1] * 2 * torch.logsumexp(l, dim=1) / n)[:, None] * q
+        part = want * (dw[t0:t1] - (want * dw[t0:t1]).sum(dim=1, keepdim=True))
+        grad.scatter_add_(1, top.indices, part)
+        size = gain.max() + float(dl[s, 1]) * 2 * 16 / n + 2.0
+        assert torch.all((d[t0:t1] - grad).abs() <= 4 * RTOL * size)
+    last = torch.bincount(idx[T - 1000:].reshape(-1), minlength=E)
+    assert torch.equal(stats.counts[1].long(), last) and int(stats.counts[0].sum()) == (T - 1000) * K
