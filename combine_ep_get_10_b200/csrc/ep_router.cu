@@ -769,8 +769,7 @@ __device__ __forceinline__ void write_balance(const BalanceLaunch& a, int s, int
 template <int NPL, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceLaunch a, int chunk, bool finish)
 {
-    // [2 * kBalanceWarps, E] floats at most: each warp's sums, then the experts'
-    extern __shared__ float s_q[];
+    extern __shared__ float s_q[]; // [kBalanceWarps, E] each warp's sums, [E] the experts' counts
     __shared__ float s_z[kBalanceWarps], s_red[kBalanceWarps];
     __shared__ int s_n[kBalanceWarps];
     __shared__ Chunk s_chunk;
@@ -1354,7 +1353,7 @@ cudaError_t launch_balance_loss(const BalanceLaunch& a, cudaStream_t stream)
     r.num_groups = 1; // the groups are the choice's alone
     return with_row_shape(r, address(a.logits), [&](auto npl, auto bf16, auto vec) {
         const auto kernel = balance_kernel<npl(), bf16(), vec()>;
-        const size_t smem = sizeof(float) * 2 * kBalanceWarps * a.r.num_experts;
+        const size_t smem = sizeof(float) * (kBalanceWarps + 1) * a.r.num_experts;
         if (smem > 47 * 1024) { // 48 KB, the kernel's own arrays among them, need no leave
             const cudaError_t e =
                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));

@@ -38,7 +38,9 @@ def lengths(kind, S, g):
 
 @pytest.mark.parametrize("kind,S,E", [("short", 4000, 24), ("some long", 3000, 24), ("about a chunk", 150, 40),
                                       ("about a chunk", 700, 8), ("one", 1000, 16), ("some long", 37, 256),
-                                      ("about a chunk", 20, 383), ("about a chunk", 20, 384), ("about a chunk", 20, 385)])
+                                      ("about a chunk", 20, 383), ("about a chunk", 20, 384), ("about a chunk", 20, 385),
+                                      ("about a chunk", 20, 707), ("about a chunk", 20, 719), ("about a chunk", 20, 722),
+                                      ("about a chunk", 20, 723), ("short", 30, 1024)])
 @pytest.mark.parametrize("first,behind", [(0, 0), (333, 70)])
 def test_many_sequences_of_all_lengths(kind, S, E, first, behind):
     g = torch.Generator().manual_seed(S + E)
