@@ -39,3 +39,14 @@ def test_more_rows_than_an_index_holds_are_refused(L):
         assert L.ep_row_tokens(ctypes.byref(routing()), ctypes.byref(LAYOUT), 1, 1 << 28, rows, 0x7000, None) == 1
     # at the limit the next check speaks: h is missing
     assert fwd(L, rows=(1 << 31) - 1024, mode=1, mt=1 << 28, rt=None, h=None) == 1
+
+
+def test_the_rule_between_kernels_is_the_one_that_tests_assume():
+    import os
+
+    import lora_paths
+    from combine_ep_get_10_b200 import build
+
+    with open(os.path.join(build.CSRC, "ep_lora.cu")) as f:
+        source = f.read()
+    assert lora_paths.RULE in source and "constexpr int kFewRank = 64;" in source
