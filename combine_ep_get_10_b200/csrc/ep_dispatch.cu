@@ -765,7 +765,7 @@ cudaError_t launch_quant(const QuantArgs& a, int32_t T, int32_t K, cudaStream_t 
 {
     const size_t smem = quant_smem_bytes(kFmt, a.H, K, a.map.E, kFused ? T : 0, kFused);
     auto kernel = quant_dispatch_kernel<kFmt, kFused>;
-    if (smem > 48 * 1024) {
+    if (smem > 47 * 1024) { // 48 KB, the kernel's own arrays among them, need no leave
         cudaError_t st = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (st != cudaSuccess)
             return st;
