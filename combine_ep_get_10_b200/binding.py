@@ -729,7 +729,9 @@ def ep_router_backward(logits: torch.Tensor, router: Router, topk_idx, d_logits:
 # ------------------------------------------------------ low-rank adapters
 class Lora:
     """The factors of E adapters: a bf16 [E, rank, hidden_in], b bf16 [E,
-    hidden_out, rank], scales fp32 [E] or None (1); see include/ep_lora.h."""
+    hidden_out, rank], scales fp32 [E] or None (1); see include/ep_lora.h.  They
+    may be replaced by others of their shapes: they are checked, and their
+    addresses taken, when they are set."""
 
     def __init__(self, a: torch.Tensor, b: torch.Tensor, scales: torch.Tensor | None = None):
         if a.dim() != 3 or b.dim() != 3:
@@ -738,11 +740,19 @@ class Lora:
         hout = b.shape[1]
         self.E, self.rank, self.hidden_in, self.hidden_out = E, r, hin, hout
         self.index = a.get_device()
-        self.a, self.b, self.scales = a, b, scales  # kept alive with the descriptor
-        self.desc = LoraDesc(r, hin, hout, _arg("a", a, torch.bfloat16, (E, r, hin)),
-                             _arg("b", b, torch.bfloat16, (E, hout, r), self.index),
-                             _arg("scales", scales, torch.float32, (E,), self.index))
+        self._shapes = {"a": (torch.bfloat16, (E, r, hin)), "b": (torch.bfloat16, (E, hout, r)),
+                        "scales": (torch.float32, (E,))}
+        self.desc = LoraDesc(r, hin, hout)
         self.ref = ctypes.byref(self.desc)
+        self.a, self.b, self.scales = a, b, scales  # kept alive with the descriptor
+
+    def __setattr__(self, name, value):
+        shapes = self.__dict__.get("_shapes", {})
+        if name in shapes:
+            if value is None and name != "scales":
+                raise TypeError("%s must be a tensor" % name)
+            setattr(self.desc, name, _arg(name, value, *shapes[name], self.index))
+        object.__setattr__(self, name, value)
 
 
 def ep_row_tokens(routing: Routing, layout: Layout, row_token: torch.Tensor, *, mode=EP_LAYOUT_COMPACT,

@@ -1,0 +1,33 @@
+"""What may be assigned to the binding's objects, and what a call then uses."""
+import pytest
+import torch
+
+from combine_ep_get_10_b200 import binding as B
+
+BF = torch.bfloat16
+
+
+def adapters():
+    return B.Lora(torch.zeros((4, 8, 64), dtype=BF), torch.zeros((4, 32, 8), dtype=BF), torch.ones(4))
+
+
+def test_replaced_factors_are_the_ones_that_calls_use():
+    lo = adapters()
+    for name, t in (("a", torch.ones((4, 8, 64), dtype=BF)), ("b", torch.ones((4, 32, 8), dtype=BF)),
+                    ("scales", torch.zeros(4))):
+        setattr(lo, name, t)
+        assert getattr(lo, name) is t and getattr(lo.desc, name) == t.data_ptr()
+    lo.scales = None
+    assert lo.desc.scales is None
+
+
+def test_replaced_factors_are_checked():
+    lo = adapters()
+    before = (lo.a, lo.b, lo.scales, lo.desc.a, lo.desc.b, lo.desc.scales)
+    for name, t, error in (("a", torch.zeros((4, 16, 64), dtype=BF), TypeError), ("a", torch.zeros((4, 8, 64)), TypeError),
+                           ("a", None, TypeError), ("b", torch.zeros((5, 32, 8), dtype=BF), TypeError),
+                           ("b", torch.zeros((4, 8, 32), dtype=BF).transpose(1, 2), ValueError),
+                           ("scales", torch.zeros(5), TypeError)):
+        with pytest.raises(error):
+            setattr(lo, name, t)
+    assert before == (lo.a, lo.b, lo.scales, lo.desc.a, lo.desc.b, lo.desc.scales)
