@@ -600,6 +600,12 @@ def _device_of(t) -> int:
     return index
 
 
+def _fixed(obj, name: str, fixed: tuple) -> None:
+    """Refuses to change a size that buffers or descriptors were made for."""
+    if name in fixed and name in obj.__dict__:
+        raise AttributeError("%s of a %s is fixed; make a new one" % (name, type(obj).__name__))
+
+
 class Router:
     """How logits become experts and weights (see include/ep_router.h)."""
 
@@ -610,6 +616,10 @@ class Router:
                         1 if normalize else 0, float(scale))
         self._score = int(score)
         self._last = (None, None, None, None)  # the descriptor of the last number of tokens and type
+
+    def __setattr__(self, name, value):
+        _fixed(self, name, ("num_experts", "num_topk"))
+        object.__setattr__(self, name, value)
 
     def desc(self, num_tokens: int, dtype) -> RouterDesc:
         return RouterDesc(self._score, EP_BF16 if dtype == torch.bfloat16 else EP_FP32, num_tokens, *self._fields)
@@ -667,6 +677,7 @@ class BalanceStats:
             setattr(self, name, torch.empty(shape, dtype=dtype, device=device))
 
     def __setattr__(self, name, value):
+        _fixed(self, name, ("num_seqs", "num_experts"))
         shapes = self.__dict__.get("_shapes", {})
         if name in shapes:
             dtype, shape = shapes[name]
@@ -747,6 +758,7 @@ class Lora:
         self.a, self.b, self.scales = a, b, scales  # kept alive with the descriptor
 
     def __setattr__(self, name, value):
+        _fixed(self, name, ("E", "rank", "hidden_in", "hidden_out", "index", "desc", "ref"))
         shapes = self.__dict__.get("_shapes", {})
         if name in shapes:
             if value is None and name != "scales":

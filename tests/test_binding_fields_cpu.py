@@ -31,3 +31,17 @@ def test_replaced_factors_are_checked():
         with pytest.raises(error):
             setattr(lo, name, t)
     assert before == (lo.a, lo.b, lo.scales, lo.desc.a, lo.desc.b, lo.desc.scales)
+
+
+def test_sizes_that_buffers_were_made_for_stay():
+    """A call checks its arrays by these and passes on the descriptor's: were
+    they to differ, a kernel would write past the arrays."""
+    router = B.Router(8, 2)
+    stats = B.BalanceStats(router, 4, num_seqs=3, device="cpu")
+    for obj, names in ((router, ("num_experts", "num_topk")), (stats, ("num_seqs", "num_experts")),
+                       (adapters(), ("E", "rank", "hidden_in", "hidden_out"))):
+        for name in names:
+            old = getattr(obj, name)
+            with pytest.raises(AttributeError):
+                setattr(obj, name, old + 1)
+            assert getattr(obj, name) == old
