@@ -767,11 +767,18 @@ class Lora:
         object.__setattr__(self, name, value)
 
 
+def _layout_on(layout, index: int) -> None:
+    """The layout's buffers have to be where the rows are."""
+    if getattr(layout, "parent", layout).workspace.get_device() != index:
+        raise ValueError("the layout's buffers are on another device than the rows, which are on cuda:%d" % index)
+
+
 def ep_row_tokens(routing: Routing, layout: Layout, row_token: torch.Tensor, *, mode=EP_LAYOUT_COMPACT,
                   max_tokens_per_expert=0, stream=None) -> None:
     """row_token int32 [num_rows]: the source token of every row (-1: no pair's)."""
     if row_token.dtype != torch.int32 or row_token.dim() != 1:
         raise TypeError("row_token must be an int32 vector")
+    _layout_on(layout, _device_of(row_token))
     _check(lib().ep_row_tokens(ctypes.byref(routing.desc), ctypes.byref(layout.desc), int(mode),
                                int(max_tokens_per_expert), row_token.shape[0], _ptr(row_token), _stream(stream)),
            "ep_row_tokens")
@@ -785,6 +792,7 @@ def _lora_rows(routing: Routing, layout: Layout, lora: Lora, first: torch.Tensor
         raise ValueError("the layout is a view of some of its tokens; the adapters' rows are those of a whole layout")
     if routing.E != lora.E:
         raise ValueError("the routing names %d adapters, the factors are of %d" % (routing.E, lora.E))
+    _layout_on(layout, dev)
     if lora.index != dev:
         raise ValueError("the factors are on another device than the rows, which are on cuda:%d" % dev)
     rows = h.shape[0]

@@ -49,6 +49,23 @@ def test_a_layout_of_more_rows_is_left_alone(T, part, E, rank, mode, mt):
                                                else 0)
 
 
+def test_a_layout_that_is_not_with_the_rows_is_refused():
+    from types import SimpleNamespace
+
+    c = Case(ids(100, 4, 70), 4, 16, 64, 72, 71)
+    elsewhere = SimpleNamespace(desc=c.layout.desc, workspace=torch.empty(1, dtype=torch.uint8))
+    out = torch.empty((100, 72), dtype=torch.bfloat16, device="cuda")
+    h = torch.empty((c.num_rows, 16), device="cuda")
+    with pytest.raises(ValueError):
+        B.ep_lora(c.x.cuda(), c.routing, elsewhere, c.lora, out, h, row_token=c.row_token)
+    with pytest.raises(ValueError):
+        B.ep_lora_backward(c.dy.cuda(), None, None, c.routing, elsewhere, c.lora, h, row_token=c.row_token)
+    with pytest.raises(ValueError):
+        B.ep_row_tokens(c.routing, elsewhere, c.row_token)
+    with pytest.raises(ValueError):
+        B.ep_row_tokens(c.routing, c.layout, c.row_token.cpu())
+
+
 def many(T, E, rank, seed, hin, hout, **kw):
     """A case whose forward call takes the two kernels for many rows."""
     idx = ids(T, E, seed, **kw) if isinstance(T, int) else T
