@@ -963,8 +963,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) lora_few_kernel(LoraFewLaunch 
         for (int c = 1; c < kFewCluster; ++c)
             if (c < parts)
                 add4(sum, v[c]);
-        // (ranks past the last are zeros: their rows of the factor count as zeros)
-        sum = make_float4(scale * sum.x, scale * sum.y, scale * sum.z, scale * sum.w);
+        // ranks past the last are zeros (their rows of the factor count as zeros, but an
+        // infinite x times those is no number)
+        sum = j < a.rank ? make_float4(scale * sum.x, scale * sum.y, scale * sum.z, scale * sum.w)
+                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         *reinterpret_cast<float4*>(s_u + at) = sum;
         if (row % parts == part && j < a.rank && rows.begin + row < rows.end)
             *reinterpret_cast<float4*>(a.u + static_cast<int64_t>(rows.begin + row) * a.rank + j) = sum;

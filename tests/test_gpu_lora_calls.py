@@ -66,6 +66,25 @@ def test_a_layout_that_is_not_with_the_rows_is_refused():
         B.ep_row_tokens(c.routing, c.layout, c.row_token.cpu())
 
 
+@pytest.mark.parametrize("rank", [8, 16, 24, 40, 64, 72])
+@pytest.mark.parametrize("T", [30, 2700])
+def test_an_infinite_row_gives_what_its_products_give(rank, T):
+    """x with an infinity whose products with the first factor are all of one sign
+    where they are infinite: h is infinite, and so is what the second factor takes of
+    it, whatever ranks the kernel adds to a full step."""
+    idx = torch.zeros((T, 1), dtype=torch.int64)
+    c = Case(idx, 1, rank, 72, 64, 72, scales=False)
+    c.x[3] = 1.0
+    c.x[3, 5] = math.inf
+    lora = B.Lora(torch.ones_like(c.lora.a), torch.ones_like(c.lora.b))
+    out = torch.empty((T, 64), dtype=torch.bfloat16, device="cuda")
+    h = torch.empty((T, rank), device="cuda")
+    B.ep_lora(c.x.cuda(), c.routing, c.layout, lora, out, h, row_token=c.row_token)
+    rows = (c.row_token == 3).nonzero().squeeze(1)
+    assert bool((h[rows] == math.inf).all()) and bool(torch.isfinite(h).all(dim=1).sum() == T - 1)
+    assert bool((out[3] == math.inf).all())
+
+
 def many(T, E, rank, seed, hin, hout, **kw):
     """A case whose forward call takes the two kernels for many rows."""
     idx = ids(T, E, seed, **kw) if isinstance(T, int) else T
