@@ -180,6 +180,18 @@ __device__ __forceinline__ uint4 ld_nc_v4_if(const void* p, bool on)
     return r;
 }
 
+// The same of memory that the kernel writes too.
+__device__ __forceinline__ uint4 ld_v4_if(const void* p, bool on)
+{
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                 "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)
+                 : "l"(p), "r"(on ? 1u : 0u)
+                 : "memory");
+    return r;
+}
+
 __device__ __forceinline__ uint2 ld_nc_v2_if(const void* p, bool on)
 {
     uint2 r = make_uint2(0u, 0u);

@@ -891,8 +891,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) lora_few_kernel(LoraFewLaunch 
         const int col = group * 32 + q * 8;
         const bool in = col < a.N && a.base != nullptr;
         const uint16_t* b = static_cast<const uint16_t*>(a.base) + col;
-        c.base[0] = ld_nc_v4_if(b + static_cast<int64_t>(max(at0, 0)) * a.N, in && at0 >= 0);
-        c.base[1] = ld_nc_v4_if(b + static_cast<int64_t>(max(at1, 0)) * a.N, in && at1 >= 0);
+        c.base[0] = ld_v4_if(b + static_cast<int64_t>(max(at0, 0)) * a.N, in && at0 >= 0);
+        c.base[1] = ld_v4_if(b + static_cast<int64_t>(max(at1, 0)) * a.N, in && at1 >= 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int n = group * 32 + 8 * (g / 2) + 2 * j + g % 2;
