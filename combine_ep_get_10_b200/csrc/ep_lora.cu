@@ -238,11 +238,15 @@ constexpr int kShrinkChain = 2; // stages whose products are summed in tensor me
 
 template <int RP>
 struct ShrinkShape {
-    // warps 0 .. 3 load x, 4 and 5 (and 8 and 9: ranks 64 ..) add the chains up, 6
-    // multiplies, 7 loads w
-    static constexpr int kSumWarps = RP <= 64 ? 2 : 4;
-    static constexpr int kThreads = RP <= 64 ? 256 : 320;
-    static constexpr int kSumRanks = RP <= 64 ? RP : 64; // a warp of those
+    // warps 0 .. 3 load x, 4 and 5 (and 8 and 9: the upper half of the ranks) add the
+    // chains up, 6 multiplies, 7 loads w
+    static constexpr int kSumWarps = RP <= 32 ? 2 : 4;
+    static constexpr int kThreads = RP <= 32 ? 256 : 320;
+    static constexpr int kCtas = RP <= 32 ? 4 : 3;             // 64 registers, so that two leave room for an expand CTA
+    static constexpr int kSumRanks = RP / (kSumWarps / 2);     // a warp of those
+    // in its registers, else in tensor memory (all ranks there: prefill 51.7 us, not 51.1)
+    static constexpr bool kHeld = kSumRanks <= 32;
+    static constexpr int kPlaces = kHeld ? 2 : 1;              // for chains, in tensor memory
     static constexpr int kStages = RP <= 32 ? 4 : (RP == 64 ? 3 : 2); // two CTAs an SM
     static constexpr int kHalfBytes = kShrinkTile * 128; // 64 channels of x
     static constexpr int kXBytes = kShrinkTile * kDepth * 2;
@@ -254,7 +258,7 @@ struct ShrinkShape {
     static constexpr int kBehind = kHalfBytes - kWBytes; // past the last stage
     static constexpr int kBytes = kStages * kStageBytes + (kBehind > 0 ? kBehind : 0) + 1024;
     static_assert(kSumBytes <= kStages * kStageBytes, "the sums take the stages' place");
-    static constexpr int kCols = 2 * RP; // tensor memory: two chains' sums
+    static constexpr int kCols = 2 * RP; // tensor memory: two chains' sums, or one's and those before
     static constexpr Swizzle kSwizzle = RP == 16 ? Swizzle::k32 : (RP == 32 ? Swizzle::k64 : Swizzle::k128);
     static constexpr int kWBox = RP < 64 ? RP : 64; // ranks a box of w [K, rank]
 };
@@ -270,10 +274,10 @@ struct ShrinkShape {
 // another multiplies from shared memory into tensor memory: what
 // is in flight is bounded by the stages alone.  Chains of kShrinkChain stages
 // alternate between two places in tensor memory; while one is summed, two warps
-// (rows 0 .. 31 and 32 .. 63) add the other one to their registers.  The product has
-// 128 rows: what lies behind a stage's 64 gives sums that nobody reads.
+// (rows 0 .. 31 and 32 .. 63) add the other one to their registers, or, where that
+// takes too many of them, to a sum in tensor memory.  The product has 128 rows: what lies behind a stage's 64 gives sums that nobody reads.
 template <int RP, bool TRANS>
-__global__ void __launch_bounds__(ShrinkShape<RP>::kThreads, 2)
+__global__ void __launch_bounds__(ShrinkShape<RP>::kThreads, ShrinkShape<RP>::kCtas)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap w_map, LoraShrinkLaunch a)
 {
     using S = ShrinkShape<RP>;
@@ -341,8 +345,8 @@ __global__ void __launch_bounds__(ShrinkShape<RP>::kThreads, 2)
     const uint32_t tmem = s_tmem;
 
     const bool sums_up = warp == 4 || warp == 5 || warp >= 8;
-    const int ranks0 = warp >= 8 ? 64 : 0; // of a warp that adds up
-    float total[S::kSumRanks];
+    const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 1) * 32) << 16) + (warp >= 8 ? S::kSumRanks : 0);
+    float total[S::kHeld ? S::kSumRanks : 1];
     bool alive = true; // no wait has run out
     if (warp < 4) {
         for (int i = 0; i < n; ++i) {
@@ -376,26 +380,44 @@ __global__ void __launch_bounds__(ShrinkShape<RP>::kThreads, 2)
             }
         }
     } else if (sums_up) {
+        if (S::kHeld) {
 #pragma unroll
-        for (int j = 0; j < S::kSumRanks; ++j)
-            total[j] = 0.0f;
-        const uint32_t from = tmem + (static_cast<uint32_t>((warp & 1) * 32) << 16) + ranks0;
+            for (int j = 0; j < S::kSumRanks; ++j)
+                total[j] = 0.0f;
+        }
         for (int chain = 0; chain * kShrinkChain < n; ++chain) {
+            const int place = chain % S::kPlaces;
             if (alive)
-                alive = mbar_wait_bounded(&s_sums[chain & 1], (chain / 2) & 1, a.rows.err);
+                alive = mbar_wait_bounded(&s_sums[place], (chain / S::kPlaces) & 1, a.rows.err);
             tc_fence_after_sync();
+            if constexpr (S::kHeld) {
 #pragma unroll
-            for (int j = 0; j < S::kSumRanks; j += 16) {
-                float d[16];
-                tmem_load16(d, from + (chain & 1) * RP + j);
+                for (int j = 0; j < S::kSumRanks; j += 16) {
+                    float d[16];
+                    tmem_load16(d, mine + place * RP + j);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    total[j + i] += d[i];
+                    for (int i = 0; i < 16; ++i)
+                        total[j + i] += d[i];
+                }
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < S::kSumRanks; j += 16) {
+                    float d[16];
+                    tmem_load16(d, mine + j);
+                    if (chain > 0) {
+                        float before[16];
+                        tmem_load16(before, mine + RP + j);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            d[i] += before[i];
+                    }
+                    tmem_store16(mine + RP + j, d);
+                }
             }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&s_taken[chain & 1]);
+                mbar_arrive(&s_taken[place]);
         }
     } else if (lane == 0) {
         constexpr uint32_t desc = product_desc(128, RP, false, TRANS);
@@ -403,7 +425,9 @@ __global__ void __launch_bounds__(ShrinkShape<RP>::kThreads, 2)
             const int stage = i % S::kStages, chain = i / kShrinkChain, link = i % kShrinkChain;
             if (!mbar_wait_bounded(&s_full[stage], (i / S::kStages) & 1, a.rows.err))
                 break;
-            if (link == 0 && chain >= 2 && !mbar_wait_bounded(&s_taken[chain & 1], (chain / 2 - 1) & 1, a.rows.err))
+            const int place = chain % S::kPlaces;
+            if (link == 0 && chain >= S::kPlaces &&
+                !mbar_wait_bounded(&s_taken[place], (chain / S::kPlaces - 1) & 1, a.rows.err))
                 break;
             fence_proxy_async_shared(); // the copies were the other threads'
             tc_fence_after_sync();
@@ -414,12 +438,12 @@ __global__ void __launch_bounds__(ShrinkShape<RP>::kThreads, 2)
                 const uint64_t wd = TRANS ? operand_desc(ws + kk * 2 * S::kWBox * 16, S::kSwizzle, kDepth * S::kWBox * 2,
                                                          S::kWBox * 16)
                                           : operand_desc(ws + kk / 4 * RP * 128 + kk % 4 * 32, Swizzle::k128, 0, 1024);
-                tc_product(tmem + (chain & 1) * RP, xd, wd, desc, link > 0 || kk > 0);
+                tc_product(tmem + place * RP, xd, wd, desc, link > 0 || kk > 0);
             }
             if (i + S::kStages < n)
                 tc_commit(&s_free[stage]);
             if (link == kShrinkChain - 1 || i == n - 1)
-                tc_commit(&s_sums[chain & 1]);
+                tc_commit(&s_sums[place]);
         }
     }
     __syncwarp();
@@ -428,10 +452,23 @@ __global__ void __launch_bounds__(ShrinkShape<RP>::kThreads, 2)
     // the tile's partial sums to shared memory, then the cluster's sums of them
     float* sums = reinterpret_cast<float*>(smem);
     if (sums_up) {
-        float* row = sums + ((warp & 1) * 32 + lane) * S::kPitch + ranks0;
+        float* row = sums + ((warp & 1) * 32 + lane) * S::kPitch + (warp >= 8 ? S::kSumRanks : 0);
+        const auto store4 = [&](int j, const float* v) { *reinterpret_cast<float4*>(row + j) = make_float4(v[0], v[1], v[2], v[3]); };
+        if constexpr (S::kHeld) {
 #pragma unroll
-        for (int j = 0; j < S::kSumRanks; j += 4)
-            *reinterpret_cast<float4*>(row + j) = make_float4(total[j], total[j + 1], total[j + 2], total[j + 3]);
+            for (int j = 0; j < S::kSumRanks; j += 4)
+                store4(j, total + j);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < S::kSumRanks; j += 16) {
+                float d[16];
+                tmem_load16(d, mine + RP + j);
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    store4(j + i, d + i);
+            }
+            tc_fence_before_sync();
+        }
     }
     cluster.sync();
     if (warp == 6)
@@ -1170,7 +1207,7 @@ __device__ __forceinline__ bool split_warps_any(bool mine)
 // before, to which the warps that split u add a chain when it is done.  The warps
 // that load run on into the next tile's stages while a tile is stored.
 template <int RP, bool SPLIT>
-__global__ void __launch_bounds__(kOuterThreads, OuterShape<RP>::kCtas)
+__global__ void __launch_bounds__(kOuterThreads, RP <= 64 ? 3 : 1) // (64 registers for three)
     lora_outer_kernel(LoraOuterLaunch a, int in_tiles, int out_tiles, int parts)
 {
     using S = OuterShape<RP>;
