@@ -111,3 +111,9 @@ def test_committed_traffic_record_is_well_formed():
         assert int(f["dram_bytes_per_launch"]) > 0
         assert f.get("workload") and f.get("capture")
     assert seen == set(bench.KERNEL_SOURCES)
+
+
+def test_committed_traffic_record_is_of_the_present_sources():
+    """A change of a kernel's sources, shared headers among them, takes the
+    headline's traffic figures away until they are measured again."""
+    assert all(bench.recorded_traffic(k) for k in bench.KERNEL_SOURCES)
