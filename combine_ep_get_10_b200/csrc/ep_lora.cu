@@ -271,11 +271,12 @@ struct ShrinkShape {
 // adds up its share of the tile's rows over the cluster, in CTA order (the
 // same sum every time, no atomics, no partial sums in HBM).  Four warps copy
 // the rows of x from where they are, a thread brings the factor's slice, and
-// another multiplies from shared memory into tensor memory: what
-// is in flight is bounded by the stages alone.  Chains of kShrinkChain stages
-// alternate between two places in tensor memory; while one is summed, two warps
-// (rows 0 .. 31 and 32 .. 63) add the other one to their registers, or, where that
-// takes too many of them, to a sum in tensor memory.  The product has 128 rows: what lies behind a stage's 64 gives sums that nobody reads.
+// another multiplies from shared memory into tensor memory: what is in flight is
+// bounded by the stages alone.  Chains of kShrinkChain stages alternate between two
+// places in tensor memory; while one is summed, two warps (rows 0 .. 31 and 32 .. 63)
+// add the other one to their registers, or, where that takes too many of them, to a
+// sum in tensor memory.  The product has 128 rows: what lies behind a stage's 64
+// gives sums that nobody reads.
 template <int RP, bool TRANS>
 __global__ void __launch_bounds__(ShrinkShape<RP>::kThreads, ShrinkShape<RP>::kCtas)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap w_map, LoraShrinkLaunch a)
@@ -510,7 +511,7 @@ struct ExpandShare {
 // more tiles than that).  One warp; all lanes get the answer.
 __device__ __forceinline__ bool find_share(const LoraRows& g, int i, int steps, int lane, ExpandShare& s)
 {
-    constexpr int kStepRows = 128; // 4096 rows of 16 adapters: 52 us, with 64 58 us, with 160 52 us
+    constexpr int kStepRows = 128; // 4096 rows of 16 adapters: 51 us, with 64 57 us, with 160 50 us
     const LaneGroups groups(g, lane);
     const auto tiles_of = [](const RowRange& r) { return (r.end - r.begin + kExpandTile - 1) / kExpandTile; };
     uint32_t cost = 0; // below 2^26: at most 2^24 rows
@@ -1628,8 +1629,8 @@ cudaError_t launch_lora_shrink(const LoraShrinkLaunch& a, cudaStream_t stream)
         if (st != cudaSuccess)
             return st;
         const int steps = (a.K + kDepth - 1) / kDepth;
-        // One resident wave of clusters: at 4096 rows of 8 adapters 18 us, with
-        // room for 444 CTAs 25 us (the last clusters wait for eight free places).
+        // One resident wave of clusters: forward of 4096 rows of 16 adapters 51 us,
+        // with room for 444 CTAs 58 us (the last clusters wait for free places).
         const int parts = std::max(1, std::min({8, 2 * 148 / tiles, steps / 4}));
         const unsigned grid = static_cast<unsigned>(tiles) * parts;
         return a.transposed ? launch_after<lora_shrink_kernel<RP, true>>(grid, S::kThreads, S::kBytes, parts, stream, w_map, a)
@@ -1665,13 +1666,16 @@ cudaError_t launch_lora_expand(const LoraExpandLaunch& a, cudaStream_t stream)
 // average, the fewer the more ranks its registers have to hold, or by all rows,
 // where the other kernels' starts and ends weigh more.  Measured at 4096 -> 4096
 // against the kernels for many rows, us:
-//   rank 16: 16 rows 7.2 / 14.6 and 14.6 / 25.5 (16, 64 adapters), 256 rows 28 / 33
-//   rank 32: 16 rows 8.9 / 15.1, 64 rows 37 / 42 (64 adapters), 256 rows 36 / 34
-//   rank 64: 16 rows 12.8 / 15.7 and 28 / 30, 64 rows 23.9 / 22.2 and 50 / 47
-//   rank 128: 16 rows 30 / 24 (not kept)
-//   one adapter, rank 16: 1024 rows 10.4 / 16.3, 4096 rows 28 / 29 (and 45 / 42 at 7168)
-//   8 adapters, rank 32: 768 rows 13 / 17; 64 adapters 6144 rows 65 / 57
-//   one adapter, rank 64: 128 rows 9.2 / 10.9, 256 rows 12.0 / 11.7
+//   rank 16: 16 rows 7.4 / 16.4 and 10.6 / 29 (16, 64 adapters), 256 rows 24 / 30
+//   rank 32: 16 rows 9.2 / 17.0, 64 rows 35 / 41 (64 adapters), 256 rows 33.6 / 33.0
+//   rank 64: 16 rows 13.0 / 18.4 and 28 / 35, 64 rows 25.1 / 20.7 and 54 / 47
+//   one adapter, rank 16: 1024 rows 10.4 / 17.3, 4096 rows 25.1 / 27.9
+//   8 adapters, rank 32: 768 rows 12.9 / 17.4, 2048 rows 19.6 / 22.0
+//   one adapter, rank 64: 128 rows 10.2 / 11.3, 256 rows 13.0 / 12.0
+// The adapters in memory are counted, since the host does not know which have rows.
+// All rows with one of many: rank 16 4096 rows of 256 adapters 26 / 39, 16384 of 1024
+// 214 / 286; rank 32 35 / 41 and 233 / 290; rank 64 1024 rows of 64 25.8 / 21.7, 4096 of
+// 256 56 / 44, 16384 of 1024 299 / 315.
 bool lora_few(const LoraRows& rows, int rank)
 {
     if (rank > kFewRank || rows.pairs == 0 || rows.num_rows == 0)
@@ -1707,8 +1711,8 @@ cudaError_t launch_lora_outer(const LoraOuterLaunch& a, cudaStream_t stream)
         const int64_t total = static_cast<int64_t>(a.rows.E) * (in_tiles + out_tiles);
         // Fewer tiles than places (one adapter, narrow layers): parts of kPartStages
         // stages and more.  4096 rows of one adapter, rank 64, 4096 -> 4096: all
-        // gradients 66 us, whole tiles 99; 512 rows, rank 32, 7168 -> 7168: in two
-        // parts of four stages 28 us, whole 24 (a cluster starts later and joins).
+        // gradients 67 us, whole tiles 108; 1024 rows, rank 32, 7168 -> 7168: in two
+        // parts 36.9 us, whole 35.8 (a cluster starts later and joins).
         constexpr int kPartStages = 8;
         const int64_t places = 148 * S::kCtas, stages = a.rows.pairs / a.rows.E / kOuterRows;
         const int parts = static_cast<int>(std::max<int64_t>(

@@ -3,8 +3,9 @@
 // All kernels give a token's row of E <= 1024 logits to one warp and keep it in
 // registers, NPL of them a lane (RowMap).  None is bound by its bytes at the sizes
 // of a step (4096 x 256 logits are 0.6 us of memory): it is chains of dependent
-// instructions, 10 cycles each, that last, so the next row is on its way while one
-// is worked on, and what few rows need (fp64) is kept short.
+// instructions, 10 cycles each, that last, so in the losses and the gradient the next
+// row is on its way while one is worked on (the choice has one row a warp), and what
+// few rows need (fp64) is kept short.
 #include <algorithm>
 #include <cfloat>
 
@@ -391,6 +392,8 @@ __device__ __forceinline__ int place_in_order(T value, int e, int count)
 // as long as its slowest row: at 4096 x 256 in 8 groups 10.5 us where every such
 // row is done whole.  Values that are equal because logit and bias are equal
 // need no second look.
+// (The fp64 parts take registers: in groups 12 to 40 bytes a thread spill around
+// them.)
 enum class Choice { kLogit, kScore, kGrouped }; // by the logits, by scores, by scores in groups
 
 template <int NPL, bool BF16, Choice CHOICE, bool VEC>
@@ -621,8 +624,8 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(RouterTopk
 // order, no floating-point atomics, nothing that one call leaves for the next).
 constexpr int kBalanceWarps = 16;
 constexpr int kBalanceThreads = kBalanceWarps * 32;
-// Chunks of a long batch, one an SM: at 4096 x 256 20.8 us a loss and gradient,
-// with two an SM 28.5 us.
+// Chunks of a long batch, one an SM: at 4096 x 256 14.4 us a loss and gradient, with
+// two an SM 16.3 us; at 16384 x 256 in 13 sequences 24.5 and 22.1 us.
 constexpr int kBalanceCtas = 148;
 constexpr int kFewTokens = 256; // one chunk a sequence: 128 x 8 3 us less of a caller's time
 
@@ -1014,8 +1017,8 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_finish_kernel(Balance
 
 // ---------------------------------------------------------------- backward
 constexpr int kBackwardWarps = 4;
-// Warps to keep before runs get longer: at 16384 x 256 24.9 us a loss and
-// gradient, with 16 an SM 26.6 us, with 32 27.2 us.
+// Warps to keep before runs get longer: at 16384 x 256 24.5 us a loss and
+// gradient, with 16 an SM 26.1 us, with 32 26.7 us.
 constexpr int kBackwardFill = 148 * 24;
 constexpr int kMostRun = 16;
 
@@ -1041,8 +1044,9 @@ __device__ __forceinline__ void each_expert(const RowMap<NPL, BF16, false, VEC>&
 // A warp has `run` consecutive tokens: the next one's row, mask, ids and
 // gradients are on their way while one is worked on, and the counts of a
 // sequence stay in registers until its last token.  Latencies bound it: 64
-// registers, for 32 warps an SM, take 15.7 us for loss and gradient of 4096 x
-// 256, 80 registers 17.3 us.
+// registers, for 32 warps an SM, take 14.4 us for loss and gradient of 4096 x
+// 256, 80 registers 15.7 us, though at 8 logits a lane (256 experts) 40 to 100 bytes a
+// thread spill.
 template <int NPL, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kBackwardWarps * 32, NPL <= 8 ? 8 : 1) router_backward_kernel(RouterBackwardLaunch a, int run)
 {

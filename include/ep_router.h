@@ -75,7 +75,9 @@ EP_API size_t ep_balance_workspace_bytes(const ep_router_desc_t* router, int32_t
 /* Balance loss, z loss and expert counts of each of S = num_seqs sequences.
  *   seq_offsets  int32 [S+1], not decreasing: sequence s is tokens
  *                [seq_offsets[s], seq_offsets[s+1]); NULL (with S = 1): all
- *                tokens.  Tokens of no sequence contribute nothing.
+ *                tokens.  Tokens of no sequence contribute nothing.  S at most
+ *                2^24.  (Offsets that decrease leave the results undefined;
+ *                nothing else is touched.)
  * Over the N tokens of sequence s that are not masked and have an open logit:
  *   counts      int32 [S, E]  entries of topk_idx [T, K] equal to e; ids
  *                             outside [0, E) are not counted
