@@ -4,7 +4,7 @@
 // ordinary matrix product with that adapter's factors: the rows are read where
 // they are (row_token, or the dispatched rows themselves).  Three products, all
 // bound by memory at the ranks they are for (4 rank flops a byte of row data
-// and less; the tensor cores are busy 8 to 12 % of the time at rank 32):
+// and less; the tensor cores are busy 10 to 15 % of the time at rank 32):
 //   shrink  u = s_e X W        long sum over the hidden width, rank columns
 //   expand  out = base + u W   rank-long sum, hidden columns, base and out move
 //   outer   dW = sum of rows   sum over a group's rows
@@ -263,8 +263,8 @@ struct ShrinkShape {
     static constexpr int kWBox = RP < 64 ? RP : 64; // ranks a box of w [K, rank]
 };
 
-// Bound by the rows' bytes: 4096 x 7168, 8 adapters of rank 32, 18 us with the
-// launch (59 MB, 3.3 TB/s; a kernel that only copies such rows 12.4 us).  What is
+// Bound by the rows' bytes: 4096 x 7168, 8 adapters of rank 32, 17 us with the
+// launch (59 MB, 3.4 TB/s; a kernel that only copies such rows 12.4 us).  What is
 // left are the ends: 2 us to find the tile and its rows, 2 us for the sums.
 //
 // A cluster has one tile of rows; its CTAs split the hidden width, and each
@@ -845,8 +845,9 @@ struct FewShape {
 // read again from L2, and what lasts is latency.  A cluster has a tile; its warps split the hidden
 // width, add their sums up over the cluster, and split the output columns.  One
 // launch, no shared memory between HBM and the warp product, the first columns'
-// factors and base on their way while u is added up: 128 rows of 64 adapters,
-// rank 16, 7168 -> 4096, 9.1 us, with the two kernels for many rows 19.4 us.
+// factors and base on their way while u is added up: 128 rows of 64 adapters, all
+// of them in use, rank 16, 7168 -> 4096, 10 us, with the two kernels for many rows
+// 31 us.
 //
 // A sum may take its terms in any order, so a lane loads 16 consecutive bytes of
 // a row of x and of the factor and calls them the product's columns k that it
@@ -1074,8 +1075,8 @@ struct OuterShape {
     static constexpr int kVBytes = kOuterRows * kOuterCols * 2;
     static constexpr int kTermBytes = kOuterRows * RP * 2;
     static constexpr int kUBytes = 3 * kTermBytes;         // u as it is in HBM, then its three terms
-    // Three CTAs an SM as far as the rank allows, the stages of a CTA in 72 KB: at
-    // rank 32 two CTAs with 87 KB take 96 us for all gradients of 4096 rows.
+    // Three CTAs an SM as far as the rank allows, the stages of a CTA in 72 KB: all
+    // gradients of 4096 rows, rank 32, 80 us, with two CTAs and 87 KB 96 us.
     static constexpr int kCtas = RP <= 32 ? 3 : (RP == 64 ? 2 : 1);
     static constexpr int kStages = RP == 128 ? 4 : 3;  // of x or dy
     static constexpr int kUStages = RP == 16 || RP == 128 ? 3 : 2; // of u
@@ -1195,9 +1196,10 @@ __device__ __forceinline__ bool split_warps_any(bool mine)
     return any != 0u;
 }
 
-// Bound by x and dy: 4096 x 7168 each, 8 adapters of rank 32, 30 us after the
-// product before it (117 MB, 3.9 TB/s), and by the chains that turn u into its
-// terms, 1200 cycles a stage, of which three CTAs an SM hide most.
+// Bound by x and dy: 4096 x 7168 each, 8 adapters of rank 32, 34 us after the
+// product before it (117 MB, 3.5 TB/s), and by the chains that turn u into its
+// terms, of which three CTAs an SM hide most (rank 64, two CTAs: 61 us; rank 128,
+// one: 139 us).
 //
 // dW of one adapter and kOuterCols columns of x or dy, tile after tile: the
 // columns are the product's rows (M), the rank its columns (N), and the sum
