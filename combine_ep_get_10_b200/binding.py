@@ -683,7 +683,8 @@ class BalanceStats:
             dtype, shape = shapes[name]
             if name == "workspace" and value.dim() == 1 and value.shape[0] >= shape[0]:
                 shape = tuple(value.shape)  # a larger one will do
-            self._at[name] = _arg(name, value, dtype, shape)
+            # (a new dict: a copy of this object keeps its own)
+            object.__setattr__(self, "_at", {**self._at, name: _arg(name, value, dtype, shape)})
             index = value.get_device()
             if any(getattr(self, n).get_device() != index for n in shapes if n != name and n in self.__dict__):
                 index = -2  # not all on one device: no call takes them
@@ -753,9 +754,12 @@ class Lora:
         self.index = a.get_device()
         self._shapes = {"a": (torch.bfloat16, (E, r, hin)), "b": (torch.bfloat16, (E, hout, r)),
                         "scales": (torch.float32, (E,))}
-        self.desc = LoraDesc(r, hin, hout)
-        self.ref = ctypes.byref(self.desc)
+        self._describe(LoraDesc(r, hin, hout))
         self.a, self.b, self.scales = a, b, scales  # kept alive with the descriptor
+
+    def _describe(self, desc: LoraDesc) -> None:
+        object.__setattr__(self, "desc", desc)
+        object.__setattr__(self, "ref", ctypes.byref(desc))
 
     def __setattr__(self, name, value):
         _fixed(self, name, ("E", "rank", "hidden_in", "hidden_out", "index", "desc", "ref"))
@@ -763,7 +767,9 @@ class Lora:
         if name in shapes:
             if value is None and name != "scales":
                 raise TypeError("%s must be a tensor" % name)
-            setattr(self.desc, name, _arg(name, value, *shapes[name], self.index))
+            desc = LoraDesc.from_buffer_copy(self.desc)  # (a copy of this object keeps its own)
+            setattr(desc, name, _arg(name, value, *shapes[name], self.index))
+            self._describe(desc)
         object.__setattr__(self, name, value)
 
 

@@ -45,3 +45,18 @@ def test_sizes_that_buffers_were_made_for_stay():
             with pytest.raises(AttributeError):
                 setattr(obj, name, old + 1)
             assert getattr(obj, name) == old
+
+
+def test_a_copy_keeps_its_own_addresses():
+    import copy
+
+    lo = adapters()
+    other = copy.copy(lo)
+    other.a = torch.ones_like(lo.a)
+    assert lo.desc.a == lo.a.data_ptr() and other.desc.a == other.a.data_ptr() != lo.desc.a
+    stats = B.BalanceStats(B.Router(8, 2), 4, device="cpu")
+    other = copy.copy(stats)
+    other.losses = torch.zeros_like(stats.losses)
+    router = B.Router(8, 2)
+    assert stats.at(router, -1)["losses"] == stats.losses.data_ptr()
+    assert other.at(router, -1)["losses"] == other.losses.data_ptr() != stats.losses.data_ptr()
