@@ -50,9 +50,8 @@ extern "C" {
  * Sums are taken in a fixed order: the same call gives the same bytes.
  * Limits: num_rows <= 2^31 - 1024; rank a multiple of 8, 8 <= rank <= 128;
  * hidden_in and hidden_out positive multiples of 8 up to 2^20; E <= 1024; T * K
- * <= 2^24; x, a, b, base, out, h and the gradients
- * 16-byte aligned.  Rows at or past num_rows are skipped with
- * EP_DEVERR_OVERFLOW.  The layout is the routing's own: with one that has rows of
+ * <= 2^24; x, a, b, base, out, h and the gradients 16-byte aligned.  Rows at or
+ * past num_rows are skipped with EP_DEVERR_OVERFLOW.  The layout is the routing's own: with one that has rows of
  * more pairs than the routing (of which the routing is a part) all rows are
  * skipped and flagged so.
  * ---------------------------------------------------------------------- */
